@@ -12,10 +12,14 @@ pointers, sizes, stream handle):
     cfp32_linear, cfp32_linear_noalloc, cfp32_linear_workspace_bytes, cfp32_linear_ex,
     cfp32_linear_ex_workspace_bytes, cfp32_linear_geglu,
     cfp32_linear_geglu_workspace_bytes, cfp32_linear_f32, cfp32_qkv_rotary, cfp32_status_string,
-    cfp32_last_hip_error
+    cfp32_last_hip_error, cfp32_attention_prompt, cfp32_attention_decode,
+    cfp32_cache_reserve, cfp32_cache_append, cfp32_cache_copy_pages,
+    cfp32_cache_fork, cfp32_cache_free, cfp32_cache_compact and the
+    *_workspace_bytes of those that take a workspace
 
-Tensor-level helpers (``split``, ``gemm``, ``merge``, ``linear``) check dtype,
-device and layout, pass ``data_ptr()`` and the current stream, and raise
+Tensor-level helpers (``split``, ``gemm``, ``merge``, ``linear``,
+``attention_prompt``, ``attention_decode``, ``cache_*``) check dtype, device
+and layout, pass ``data_ptr()`` and the current stream, and raise
 ``Cfp32Error`` on a non-zero status.  FP16 tensors may be ``torch.float16``
 or ``torch.int16``/``torch.uint16`` bit patterns.
 """
@@ -46,9 +50,22 @@ EXPORTS = (
     "cfp32_linear_geglu",
     "cfp32_linear_f32",
     "cfp32_qkv_rotary",
+    "cfp32_attention_prompt_workspace_bytes",
+    "cfp32_attention_prompt",
+    "cfp32_attention_decode_workspace_bytes",
+    "cfp32_attention_decode",
+    "cfp32_cache_reserve",
+    "cfp32_cache_append",
+    "cfp32_cache_copy_pages",
+    "cfp32_cache_fork_workspace_bytes",
+    "cfp32_cache_fork",
+    "cfp32_cache_free",
+    "cfp32_cache_compact_workspace_bytes",
+    "cfp32_cache_compact",
 )
 
 W_KN, W_NK = 0, 1
+KV_F32, KV_F16 = 0, 1
 
 
 class Cfp32Error(RuntimeError):
@@ -103,6 +120,34 @@ def load_library():
     lib.cfp32_linear_f32.restype = I32
     lib.cfp32_qkv_rotary.argtypes = [P, I64, P, ctypes.c_double, P, P, P, I64, I64, I64, P]
     lib.cfp32_qkv_rotary.restype = I32
+    SZ, F64 = ctypes.c_size_t, ctypes.c_double
+    view, pool = [P, I64, I64], [P, I64, I64, I64]
+    lib.cfp32_attention_prompt_workspace_bytes.argtypes = [I64] * 4 + [I32]
+    lib.cfp32_attention_prompt_workspace_bytes.restype = SZ
+    lib.cfp32_attention_prompt.argtypes = view * 3 + [I32, P, P] + view + [I64] * 6 + [I32, F64, P, SZ, P]
+    lib.cfp32_attention_prompt.restype = I32
+    lib.cfp32_attention_decode_workspace_bytes.argtypes = [I64] * 7 + [I32]
+    lib.cfp32_attention_decode_workspace_bytes.restype = SZ
+    lib.cfp32_attention_decode.argtypes = view + pool * 2 + [I32, I64, I64, P, I64, I64, P, I64] + view + [I64] * 4 + \
+        [F64, P, SZ, P]
+    lib.cfp32_attention_decode.restype = I32
+    lib.cfp32_cache_reserve.argtypes = [P, I64, P, P, P, P, I64, P, P, I64, I64, I64, I64, P]
+    lib.cfp32_cache_reserve.restype = I32
+    lib.cfp32_cache_append.argtypes = view * 2 + [P] * 3 + pool * 2 + [I32, I64, I64, P] + [I64] * 6 + [P]
+    lib.cfp32_cache_append.restype = I32
+    lib.cfp32_cache_copy_pages.argtypes = pool * 2 + [I32] + [I64] * 4 + [P, P, I64, P]
+    lib.cfp32_cache_copy_pages.restype = I32
+    lib.cfp32_cache_fork_workspace_bytes.argtypes = [I64]
+    lib.cfp32_cache_fork_workspace_bytes.restype = SZ
+    lib.cfp32_cache_fork.argtypes = pool * 2 + [I32] + [I64] * 4 + [P, I64, P, P, P, P, I64, P, P, P] + [I64] * 3 + \
+        [P, SZ, P]
+    lib.cfp32_cache_fork.restype = I32
+    lib.cfp32_cache_free.argtypes = [P, I64, P, P, I64, I64, I64, P]
+    lib.cfp32_cache_free.restype = I32
+    lib.cfp32_cache_compact_workspace_bytes.argtypes = [I64]
+    lib.cfp32_cache_compact_workspace_bytes.restype = SZ
+    lib.cfp32_cache_compact.argtypes = pool * 2 + [I32] + [I64] * 4 + [P, I64, P, P, I64, P, P, I64, I64, P, SZ, P]
+    lib.cfp32_cache_compact.restype = I32
     _lib = lib
     return lib
 
@@ -170,6 +215,79 @@ def cfp32_linear_f32(x, ldx, w, ldw, y, ldy, M, N, K, stream) -> int:
 
 def cfp32_qkv_rotary(qkv, ldq, positions, theta, q, k, v, T, H, D, stream) -> int:
     return int(load_library().cfp32_qkv_rotary(qkv, ldq, positions, theta, q, k, v, T, H, D, stream))
+
+
+def cfp32_attention_prompt_workspace_bytes(S, Tk, Hkv, D, kv_type) -> int:
+    return int(load_library().cfp32_attention_prompt_workspace_bytes(S, Tk, Hkv, D, kv_type))
+
+
+def cfp32_attention_prompt(q, q_tok, q_head, k, k_tok, k_head, v, v_tok, v_head, kv_type, cu_q, cu_k, out, out_tok,
+                           out_head, S, Tq, Tk, Hq, Hkv, D, causal, scale, workspace, workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_attention_prompt(q, q_tok, q_head, k, k_tok, k_head, v, v_tok, v_head, kv_type,
+                                                     cu_q, cu_k, out, out_tok, out_head, S, Tq, Tk, Hq, Hkv, D,
+                                                     causal, scale, workspace, workspace_bytes, stream))
+
+
+def cfp32_attention_decode_workspace_bytes(B, Hq, Hkv, D, W, page, shared_pages, kv_type) -> int:
+    return int(load_library().cfp32_attention_decode_workspace_bytes(B, Hq, Hkv, D, W, page, shared_pages, kv_type))
+
+
+def cfp32_attention_decode(q, q_seq, q_head, k_pages, k_page, k_head, k_tok, v_pages, v_page, v_head, v_tok, kv_type,
+                           P, page, table, ld_table, W, lens, shared_pages, out, out_seq, out_head, B, Hq, Hkv, D,
+                           scale, workspace, workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_attention_decode(q, q_seq, q_head, k_pages, k_page, k_head, k_tok, v_pages,
+                                                     v_page, v_head, v_tok, kv_type, P, page, table, ld_table, W,
+                                                     lens, shared_pages, out, out_seq, out_head, B, Hq, Hkv, D,
+                                                     scale, workspace, workspace_bytes, stream))
+
+
+def cfp32_cache_reserve(table, ld_table, lens, cu, refs, table_out, ld_out, refs_out, missing, S, W, P, page,
+                        stream) -> int:
+    return int(load_library().cfp32_cache_reserve(table, ld_table, lens, cu, refs, table_out, ld_out, refs_out,
+                                                  missing, S, W, P, page, stream))
+
+
+def cfp32_cache_append(k, k_tok, k_head, v, v_tok, v_head, cu, lens, lens_out, k_pages, kp_page, kp_head, kp_tok,
+                       v_pages, vp_page, vp_head, vp_tok, kv_type, P, page, table, ld_table, S, W, T, Hkv, D,
+                       stream) -> int:
+    return int(load_library().cfp32_cache_append(k, k_tok, k_head, v, v_tok, v_head, cu, lens, lens_out, k_pages,
+                                                 kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head, vp_tok,
+                                                 kv_type, P, page, table, ld_table, S, W, T, Hkv, D, stream))
+
+
+def cfp32_cache_copy_pages(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head, vp_tok, kv_type, P, page,
+                           Hkv, D, src, dst, n, stream) -> int:
+    return int(load_library().cfp32_cache_copy_pages(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head,
+                                                     vp_tok, kv_type, P, page, Hkv, D, src, dst, n, stream))
+
+
+def cfp32_cache_fork_workspace_bytes(C) -> int:
+    return int(load_library().cfp32_cache_fork_workspace_bytes(C))
+
+
+def cfp32_cache_fork(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head, vp_tok, kv_type, P, page, Hkv, D,
+                     table, ld_table, lens, refs, parents, table_out, ld_out, lens_out, refs_out, missing, S, W, C,
+                     workspace, workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_cache_fork(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head, vp_tok,
+                                               kv_type, P, page, Hkv, D, table, ld_table, lens, refs, parents,
+                                               table_out, ld_out, lens_out, refs_out, missing, S, W, C, workspace,
+                                               workspace_bytes, stream))
+
+
+def cfp32_cache_free(rows, ld_rows, refs, refs_out, R, W, P, stream) -> int:
+    return int(load_library().cfp32_cache_free(rows, ld_rows, refs, refs_out, R, W, P, stream))
+
+
+def cfp32_cache_compact_workspace_bytes(P) -> int:
+    return int(load_library().cfp32_cache_compact_workspace_bytes(P))
+
+
+def cfp32_cache_compact(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head, vp_tok, kv_type, P, page, Hkv,
+                        D, table, ld_table, refs, table_out, ld_out, refs_out, live, S, W, workspace,
+                        workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_cache_compact(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head,
+                                                  vp_tok, kv_type, P, page, Hkv, D, table, ld_table, refs, table_out,
+                                                  ld_out, refs_out, live, S, W, workspace, workspace_bytes, stream))
 
 
 # -- tensor helpers -------------------------------------------------------------
@@ -417,3 +535,265 @@ def qkv_rotary(qkv, H: int, D: int, positions=None, theta: float = 10000.0, stre
     _check(cfp32_qkv_rotary(pq, ldq, pp, float(theta), q.data_ptr(), k.data_ptr(), v.data_ptr(), T, H, D,
                             _stream(stream)), "cfp32_qkv_rotary")
     return q, k, v
+
+
+# -- attention and the paged cache ----------------------------------------------
+
+def _heads(t, dtypes, name, device):
+    """(pointer, token stride, head stride) of a [tokens, heads, D] tensor with unit stride along D."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise TypeError(f"{name}: expected a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name}: on another device")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected a 3-D tensor")
+    a, b, c = t.stride()
+    if c != 1 and t.shape[2] > 1 and t.numel():
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), a, b
+
+
+def _ints(t, name, device, dim):
+    """Pointer of an int32 tensor: contiguous along its last dimension."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device:
+        raise TypeError(f"{name}: expected an int32 tensor on {device}")
+    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel()):
+        raise ValueError(f"{name}: expected a {dim}-D tensor with contiguous rows")
+    return t.data_ptr()
+
+
+def _ld(t):
+    return max(t.stride(0) if t.shape[0] > 1 else 0, t.shape[1])
+
+
+def _pools(k_pages, v_pages):
+    """(K and V as pointer and page, head and token strides), kv_type and shape of a pair of pools."""
+    torch = _torch()
+    at = []
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+            raise TypeError(f"{name}: expected a GPU tensor")
+        if t.dtype not in (torch.float32, torch.float16):
+            raise TypeError(f"{name}: dtype {t.dtype} is neither float32 nor float16")
+        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1 and t.numel()):
+            raise ValueError(f"{name}: expected [pages, heads, tokens, D] with contiguous D")
+        at += [t.data_ptr(), *t.stride()[:3]]
+    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device:
+        raise ValueError("k_pages and v_pages differ in shape, dtype or device")
+    return at, KV_F16 if k_pages.dtype == torch.float16 else KV_F32, k_pages.shape
+
+
+def _on(stream):
+    """The torch stream of a helper call (an integer handle is wrapped)."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.current_stream()
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor in the memory of the stream that writes it, so that the
+    allocator's reuse is ordered with the work queued there."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_on(stream)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(need, device, workspace, stream):
+    st = _on(stream)
+    if not need:
+        return None, _stream(st)
+    ws = (workspace or _default_workspace(device, st)).get(need, device, st)
+    return ws.data_ptr(), _stream(st)
+
+
+def attention_prompt(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None, out=None,
+                     workspace: Workspace | None = None, stream=None):
+    """Attention over packed prompts: q FP32 [Tq, Hq, D]; k, v FP32 or FP16
+    [Tk, Hkv, D] (any strides with contiguous D: pass ``qkv_rotary``'s
+    [H, T, D] as ``.transpose(0, 1)``); cu_q, cu_k int32 [S + 1] offsets of
+    the sequences (cu_k defaults to cu_q).  Causal rows are aligned to the
+    end of their sequence's keys.  scale defaults to 1 / sqrt(D).  Returns
+    FP32 [Tq, Hq, D]; rows outside all sequences are not written."""
+    torch = _torch()
+    pq = _heads(q, (torch.float32,), "q", q.device)
+    dev = q.device
+    pk = _heads(k, (torch.float32, torch.float16), "k", dev)
+    pv = _heads(v, (k.dtype,), "v", dev)
+    Tq, Hq, D = q.shape
+    Tk, Hkv, D2 = k.shape
+    if v.shape != k.shape or D2 != D or Hkv == 0 or Hq % Hkv:
+        raise ValueError("shape mismatch between q, k and v")
+    cu_k = cu_q if cu_k is None else cu_k
+    cq, ck = _ints(cu_q, "cu_q", dev, 1), _ints(cu_k, "cu_k", dev, 1)
+    S = cu_q.shape[0] - 1
+    if S < 0 or cu_k.shape[0] != S + 1:
+        raise ValueError("cu_q and cu_k must both have one entry more than there are sequences")
+    if out is None:
+        out = _empty((Tq, Hq, D), torch.float32, dev, stream)
+    elif out.shape != q.shape:
+        raise ValueError("out has the wrong shape")
+    po = _heads(out, (torch.float32,), "out", dev)
+    kv = KV_F16 if k.dtype == torch.float16 else KV_F32
+    need = cfp32_attention_prompt_workspace_bytes(S, Tk, Hkv, D, kv)
+    ws, st = _scratch(need, dev, workspace, stream)
+    _check(cfp32_attention_prompt(*pq, *pk, *pv, kv, cq, ck, *po, S, Tq, Tk, Hq, Hkv, D, 1 if causal else 0,
+                                  D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention_prompt")
+    return out
+
+
+def attention_decode(q, k_pages, v_pages, table, lens, shared_pages: int = 0, scale: float | None = None, out=None,
+                     workspace: Workspace | None = None, stream=None):
+    """Attention of one new token per sequence against a paged cache: q FP32
+    [B, Hq, D]; pools [P, Hkv, page, D]; table int32 [B, W]; lens int32 [B].
+    The first ``shared_pages`` table entries are the same in every row and
+    are read once for the batch.  Returns FP32 [B, Hq, D]."""
+    torch = _torch()
+    dev = q.device
+    pq = _heads(q, (torch.float32,), "q", dev)
+    at, kv, (P, Hkv, page, D2) = _pools(k_pages, v_pages)
+    B, Hq, D = q.shape
+    if k_pages.device != dev or D2 != D or Hkv == 0 or Hq % Hkv:
+        raise ValueError("q and the pools differ in head size, heads or device")
+    pt, pl = _ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1)
+    W = table.shape[1]
+    if table.shape[0] != B or lens.shape[0] != B:
+        raise ValueError("table and lens must have one row per sequence")
+    if out is None:
+        out = _empty((B, Hq, D), torch.float32, dev, stream)
+    elif out.shape != q.shape:
+        raise ValueError("out has the wrong shape")
+    po = _heads(out, (torch.float32,), "out", dev)
+    need = cfp32_attention_decode_workspace_bytes(B, Hq, Hkv, D, W, page, shared_pages, kv)
+    ws, st = _scratch(need, dev, workspace, stream)
+    _check(cfp32_attention_decode(*pq, *at, kv, P, page, pt, _ld(table), W, pl, shared_pages, *po, B, Hq, Hkv, D,
+                                  D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention_decode")
+    return out
+
+
+def cache_reserve(table, lens, refs, cu, page: int, missing=None, table_out=None, refs_out=None, stream=None):
+    """(table, refs) with the lowest free pages in the entries that the new
+    tokens need: sequence s holds lens[s] tokens and gets cu[s+1] - cu[s]
+    more.  ``missing`` (int32 [1]) receives how many pages could not be given."""
+    torch = _torch()
+    dev = table.device
+    pt, pl, pr, pc = (_ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1), _ints(refs, "refs", dev, 1),
+                      _ints(cu, "cu", dev, 1))
+    S, W = table.shape
+    if lens.shape[0] != S or cu.shape[0] != S + 1:
+        raise ValueError("lens must have one entry per sequence, cu one more")
+    table_out = _empty((S, W), torch.int32, dev, stream) if table_out is None else table_out
+    refs_out = _empty(refs.shape, torch.int32, dev, stream) if refs_out is None else refs_out
+    pto, pro = _ints(table_out, "table_out", dev, 2), _ints(refs_out, "refs_out", dev, 1)
+    pm = None if missing is None else _ints(missing, "missing", dev, 1)
+    if table_out.shape != table.shape or refs_out.shape != refs.shape or (missing is not None and not missing.numel()):
+        raise ValueError("table_out, refs_out or missing has the wrong shape")
+    _check(cfp32_cache_reserve(pt, _ld(table), pl, pc, pr, pto, _ld(table_out), pro, pm, S, W, refs.shape[0], page,
+                               _stream(stream)), "cfp32_cache_reserve")
+    return table_out, refs_out
+
+
+def cache_append(k, v, cu, k_pages, v_pages, table, lens, lens_out=None, stream=None):
+    """Writes new tokens, k and v FP32 [T, Hkv, D], into the pools (rounded to
+    their type): rows cu[s] .. cu[s+1] - 1 become tokens lens[s], ... of
+    sequence s.  Returns the new lengths."""
+    torch = _torch()
+    at, kv, (P, Hkv, page, D) = _pools(k_pages, v_pages)
+    dev = k_pages.device
+    pk, pv = _heads(k, (torch.float32,), "k", dev), _heads(v, (torch.float32,), "v", dev)
+    if k.shape != v.shape or k.shape[1] != Hkv or k.shape[2] != D:
+        raise ValueError("k, v and the pools differ in heads or head size")
+    pt, pl, pc = _ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1), _ints(cu, "cu", dev, 1)
+    S, W = table.shape
+    if lens.shape[0] != S or cu.shape[0] != S + 1:
+        raise ValueError("lens must have one entry per sequence, cu one more")
+    lens_out = _empty(lens.shape, torch.int32, dev, stream) if lens_out is None else lens_out
+    plo = _ints(lens_out, "lens_out", dev, 1)
+    if lens_out.shape != lens.shape:
+        raise ValueError("lens_out has the wrong shape")
+    _check(cfp32_cache_append(*pk, *pv, pc, pl, plo, *at, kv, P, page, pt, _ld(table), S, W, k.shape[0], Hkv, D,
+                              _stream(stream)), "cfp32_cache_append")
+    return lens_out
+
+
+def cache_copy_pages(k_pages, v_pages, src, dst, stream=None):
+    """Copies page src[i] of both pools to page dst[i] (int32 [n] each)."""
+    at, kv, (P, Hkv, page, D) = _pools(k_pages, v_pages)
+    dev = k_pages.device
+    ps, pd = _ints(src, "src", dev, 1), _ints(dst, "dst", dev, 1)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst differ in length")
+    _check(cfp32_cache_copy_pages(*at, kv, P, page, Hkv, D, ps, pd, src.shape[0], _stream(stream)),
+           "cfp32_cache_copy_pages")
+
+
+def cache_fork(k_pages, v_pages, table, lens, refs, parents, missing=None, refs_out=None,
+               workspace: Workspace | None = None, stream=None):
+    """(table, refs, lens) of children of running sequences: child c shares the
+    whole pages of sequence parents[c] and gets a copy of its partly filled
+    last page.  ``missing`` (int32 [1]) receives how many last pages the pool
+    had no page for."""
+    torch = _torch()
+    at, kv, (P, Hkv, page, D) = _pools(k_pages, v_pages)
+    dev = k_pages.device
+    pt, pl, pr, pp = (_ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1), _ints(refs, "refs", dev, 1),
+                      _ints(parents, "parents", dev, 1))
+    (S, W), C = table.shape, parents.shape[0]
+    if lens.shape[0] != S or refs.shape[0] != P:
+        raise ValueError("lens must have one entry per sequence, refs one per page")
+    table_out = _empty((C, W), torch.int32, dev, stream)
+    lens_out = _empty(C, torch.int32, dev, stream)
+    refs_out = _empty(refs.shape, torch.int32, dev, stream) if refs_out is None else refs_out
+    pro = _ints(refs_out, "refs_out", dev, 1)
+    pm = None if missing is None else _ints(missing, "missing", dev, 1)
+    if refs_out.shape != refs.shape or (missing is not None and not missing.numel()):
+        raise ValueError("refs_out or missing has the wrong shape")
+    need = cfp32_cache_fork_workspace_bytes(C)
+    ws, st = _scratch(need, dev, workspace, stream)
+    _check(cfp32_cache_fork(*at, kv, P, page, Hkv, D, pt, _ld(table), pl, pr, pp, table_out.data_ptr(), W,
+                            lens_out.data_ptr(), pro, pm, S, W, C, ws, need, st), "cfp32_cache_fork")
+    return table_out, refs_out, lens_out
+
+
+def cache_free(rows, refs, refs_out=None, stream=None):
+    """refs with the pages named in rows [R, W] (tables of ended sequences) given up."""
+    torch = _torch()
+    dev = refs.device
+    pw, pr = _ints(rows, "rows", dev, 2), _ints(refs, "refs", dev, 1)
+    refs_out = _empty(refs.shape, torch.int32, dev, stream) if refs_out is None else refs_out
+    pro = _ints(refs_out, "refs_out", dev, 1)
+    if refs_out.shape != refs.shape:
+        raise ValueError("refs_out has the wrong shape")
+    R, W = rows.shape
+    _check(cfp32_cache_free(pw, _ld(rows), pr, pro, R, W, refs.shape[0], _stream(stream)), "cfp32_cache_free")
+    return refs_out
+
+
+def cache_compact(k_pages, v_pages, table, refs, table_out=None, refs_out=None, workspace: Workspace | None = None,
+                  stream=None):
+    """(table, refs, n) of the pool made dense: its n live pages are moved to
+    pages 0 .. n - 1, and the table names them there.  n is an int32 [1] tensor."""
+    torch = _torch()
+    at, kv, (P, Hkv, page, D) = _pools(k_pages, v_pages)
+    dev = k_pages.device
+    pt, pr = _ints(table, "table", dev, 2), _ints(refs, "refs", dev, 1)
+    S, W = table.shape
+    if refs.shape[0] != P:
+        raise ValueError("refs must have one entry per page")
+    table_out = _empty((S, W), torch.int32, dev, stream) if table_out is None else table_out
+    refs_out = _empty(refs.shape, torch.int32, dev, stream) if refs_out is None else refs_out
+    pto, pro = _ints(table_out, "table_out", dev, 2), _ints(refs_out, "refs_out", dev, 1)
+    if table_out.shape != table.shape or refs_out.shape != refs.shape:
+        raise ValueError("table_out or refs_out has the wrong shape")
+    live = _empty(1, torch.int32, dev, stream)
+    need = cfp32_cache_compact_workspace_bytes(P)
+    ws, st = _scratch(need, dev, workspace, stream)
+    _check(cfp32_cache_compact(*at, kv, P, page, Hkv, D, pt, _ld(table), pr, pto, _ld(table_out), pro,
+                               live.data_ptr(), S, W, ws, need, st), "cfp32_cache_compact")
+    return table_out, refs_out, live

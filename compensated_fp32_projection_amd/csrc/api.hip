@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/cfp32.h"
+#include "api_common.h"
 #include "launchers.h"
 
 namespace {
@@ -146,6 +147,13 @@ cfp32_status linear_paths(const float *x, int64_t ldx, const uint16_t *w, int64_
                           hipStream_t s);
 
 }  // namespace
+
+namespace cfp32 {
+
+cfp32_status api_check_device() { return check_device(); }
+cfp32_status api_launched(hipError_t e) { return launched(e); }
+
+}  // namespace cfp32
 
 extern "C" {
 

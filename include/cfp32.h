@@ -338,6 +338,168 @@ CFP32_API cfp32_status cfp32_linear_f32(const float *x, int64_t ldx, const uint1
 CFP32_API cfp32_status cfp32_qkv_rotary(const float *qkv, int64_t ldq, const int64_t *positions, double theta,
                               float *q, float *k, float *v, int64_t T, int64_t H, int64_t D, void *stream);
 
+/* ---- Attention and the paged cache ------------------------------------------
+ *
+ * What a layer runs between cfp32_qkv_rotary and its output projection:
+ * causal attention over packed prompts, attention of new tokens against a
+ * paged cache, and the pages themselves.  Activations (q, out, the tokens
+ * written into a cache) are FP32; K and V are FP32 (as cfp32_qkv_rotary
+ * writes them) or FP16 (exact operands, as the weights are).  Products run
+ * on the FP16 matrix units with FP32-grade results, as in the projection:
+ * every FP32 operand is brought to a power of two near the top of FP16's
+ * range and split into two FP16 parts; sums and softmax statistics are FP32.
+ *
+ * Shapes, in addition to the conventions above:
+ * - Every dimension is below 2^31; Hq is a multiple of Hkv (query head h
+ *   reads K/V head h / (Hq / Hkv)); 1 <= D <= 128.
+ * - *_tok, *_head, *_seq and *_page are strides in elements between
+ *   consecutive tokens, heads, sequences and pages; the D values of one
+ *   token and head are contiguous.  Strides of inputs are >= 0 (0 repeats);
+ *   rows of an output must not overlap.
+ * - Cache pools are [P, Hkv, page, D], `page` tokens to a page (a power of
+ *   two up to 65536); a table row lists a sequence's page ids in order, -1
+ *   where it has none.  refs[P] counts the tables' uses of each page; a page
+ *   whose count is 0 or less is free.
+ * - Lengths, offsets, page ids and counts are int32 device arrays, which the
+ *   host cannot check: the kernels keep every access within the tensors
+ *   given here whatever they hold.
+ */
+typedef enum {
+    CFP32_KV_F32 = 0,
+    CFP32_KV_F16 = 1
+} cfp32_kv_type;
+
+/* Workspace bytes of cfp32_attention_prompt; 0 for sizes it refuses. */
+CFP32_API size_t cfp32_attention_prompt_workspace_bytes(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, int kv_type);
+
+/* Attention over packed prompts.
+ *   q, out     : FP32 [Tq, Hq, D].
+ *   k, v       : [Tk, Hkv, D] of kv_type.
+ *   cu_q, cu_k : int32 [S + 1]: sequence s has query rows cu_q[s] ..
+ *                cu_q[s+1] - 1 and keys cu_k[s] .. cu_k[s+1] - 1
+ *                (non-decreasing, within [0, Tq] and [0, Tk]).
+ *   scale      : factor on q . k.
+ * Row i of a sequence with Lq rows and Lk keys sees all of its keys, or with
+ * `causal` those at j <= i + Lk - Lq (the last row sees the last key: Lk > Lq
+ * continues a cached prefix).  out = softmax(scale q K^T) V over the keys a
+ * row sees; a row that sees none is 0.  What a row does not see does not
+ * reach it, NaN and infinities included; an infinite or NaN value of V that
+ * a row sees reaches it as IEEE arithmetic has it, an infinite or NaN entry
+ * of a key or query as NaN.  Rows of out outside all sequences are not written.
+ * FP32 K and V: values below 2^-24 of the largest in a 64-key tile of a head
+ * keep fewer bits than FP32 holds (their error is below 2^-39 of that
+ * largest). */
+CFP32_API cfp32_status cfp32_attention_prompt(const float *q, int64_t q_tok, int64_t q_head,
+                                    const void *k, int64_t k_tok, int64_t k_head,
+                                    const void *v, int64_t v_tok, int64_t v_head, int kv_type,
+                                    const int32_t *cu_q, const int32_t *cu_k,
+                                    float *out, int64_t out_tok, int64_t out_head,
+                                    int64_t S, int64_t Tq, int64_t Tk, int64_t Hq, int64_t Hkv, int64_t D,
+                                    int causal, double scale, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Workspace bytes of cfp32_attention_decode; 0 for sizes it refuses. */
+CFP32_API size_t cfp32_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W,
+                                              int64_t page, int64_t shared_pages, int kv_type);
+
+/* Attention of one new token per sequence against a paged cache.
+ *   q, out       : FP32 [B, Hq, D].
+ *   k_pages, v_pages : pools of P pages of kv_type.
+ *   table        : int32 [B, W], leading dimension ld_table >= W.
+ *   lens         : int32 [B]: sequence b sees its first lens[b] tokens
+ *                  (clamped to [0, W * page]); 0 gives a row of 0.
+ *   shared_pages : the first shared_pages (<= W) table entries are the same
+ *                  in every row (row 0's are read): the batch reads those
+ *                  pages once, together.  A sequence whose length ends
+ *                  inside them is right too, at the cost of reading its
+ *                  pages on its own.
+ * A page id outside [0, P) where lens needs a page makes the row NaN. */
+CFP32_API cfp32_status cfp32_attention_decode(const float *q, int64_t q_seq, int64_t q_head,
+                                    const void *k_pages, int64_t k_page, int64_t k_head, int64_t k_tok,
+                                    const void *v_pages, int64_t v_page, int64_t v_head, int64_t v_tok,
+                                    int kv_type, int64_t P, int64_t page,
+                                    const int32_t *table, int64_t ld_table, int64_t W, const int32_t *lens,
+                                    int64_t shared_pages, float *out, int64_t out_seq, int64_t out_head,
+                                    int64_t B, int64_t Hq, int64_t Hkv, int64_t D, double scale,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Pages for new tokens.  Sequence s holds lens[s] tokens and will get
+ * cu[s+1] - cu[s] more; every table entry below its new page count that is
+ * -1 takes a free page, in order of (sequence, entry), lowest page first.
+ *   table_out, refs_out : the new tables and counts (1 for a page taken);
+ *                         may be table and refs themselves.
+ *   missing : int32 [1] or NULL: how many pages were wanted and not given
+ *             (the pool ran out, or the table is too narrow); such entries
+ *             stay -1. */
+CFP32_API cfp32_status cfp32_cache_reserve(const int32_t *table, int64_t ld_table, const int32_t *lens, const int32_t *cu,
+                                 const int32_t *refs, int32_t *table_out, int64_t ld_out, int32_t *refs_out,
+                                 int32_t *missing, int64_t S, int64_t W, int64_t P, int64_t page, void *stream);
+
+/* Writes new tokens into their pages, rounded to kv_type (to nearest even).
+ *   k, v     : FP32 [T, Hkv, D]; rows cu[s] .. cu[s+1] - 1 become tokens
+ *              lens[s], lens[s] + 1, ... of sequence s.
+ *   lens_out : int32 [S]: lens[s] + cu[s+1] - cu[s]; not lens itself.
+ * Tokens whose table entry is not a page of the pool, or beyond the table,
+ * are not written. */
+CFP32_API cfp32_status cfp32_cache_append(const float *k, int64_t k_tok, int64_t k_head,
+                                const float *v, int64_t v_tok, int64_t v_head,
+                                const int32_t *cu, const int32_t *lens, int32_t *lens_out,
+                                void *k_pages, int64_t kp_page, int64_t kp_head, int64_t kp_tok,
+                                void *v_pages, int64_t vp_page, int64_t vp_head, int64_t vp_tok,
+                                int kv_type, int64_t P, int64_t page,
+                                const int32_t *table, int64_t ld_table, int64_t S, int64_t W, int64_t T,
+                                int64_t Hkv, int64_t D, void *stream);
+
+/* Copies page src[i] of both pools to page dst[i], i < n (all at once: no
+ * page may be both a source and a destination, or a destination twice).
+ * Pairs with an id outside [0, P) are passed over. */
+CFP32_API cfp32_status cfp32_cache_copy_pages(void *k_pages, int64_t kp_page, int64_t kp_head, int64_t kp_tok,
+                                    void *v_pages, int64_t vp_page, int64_t vp_head, int64_t vp_tok,
+                                    int kv_type, int64_t P, int64_t page, int64_t Hkv, int64_t D,
+                                    const int32_t *src, const int32_t *dst, int64_t n, void *stream);
+
+/* Workspace bytes of cfp32_cache_fork for C children. */
+CFP32_API size_t cfp32_cache_fork_workspace_bytes(int64_t C);
+
+/* Children of running sequences.  Child c of sequence p = parents[c] gets
+ * p's length, shares its whole pages (their counts go up by one), and where
+ * p's last page is partly filled takes a free page (lowest first, in the
+ * order of the children) and a copy of that page.
+ *   table_out [C, W], lens_out [C] : the children's; refs_out [P] (may be refs).
+ *   missing : int32 [1] or NULL: how many last pages the pool had no page
+ *             for; such a child ends with its whole pages.
+ * A parent outside [0, S) gives an empty child. */
+CFP32_API cfp32_status cfp32_cache_fork(void *k_pages, int64_t kp_page, int64_t kp_head, int64_t kp_tok,
+                              void *v_pages, int64_t vp_page, int64_t vp_head, int64_t vp_tok,
+                              int kv_type, int64_t P, int64_t page, int64_t Hkv, int64_t D,
+                              const int32_t *table, int64_t ld_table, const int32_t *lens, const int32_t *refs,
+                              const int32_t *parents, int32_t *table_out, int64_t ld_out, int32_t *lens_out,
+                              int32_t *refs_out, int32_t *missing, int64_t S, int64_t W, int64_t C,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gives up the pages of ended sequences: the count of each page goes down by
+ * one for every entry of rows [R, W] that names it (-1 and ids outside the
+ * pool name none).  refs_out may be refs. */
+CFP32_API cfp32_status cfp32_cache_free(const int32_t *rows, int64_t ld_rows, const int32_t *refs, int32_t *refs_out,
+                              int64_t R, int64_t W, int64_t P, void *stream);
+
+/* Workspace bytes of cfp32_cache_compact for a pool of P pages. */
+CFP32_API size_t cfp32_cache_compact_workspace_bytes(int64_t P);
+
+/* Makes the pool dense: of n live pages, the j-th at or above page n moves
+ * into the j-th free page below n, with its count; the tables follow.
+ *   table_out [S, W], refs_out [P] : may be table and refs themselves.
+ *   live : int32 [1]: n.
+ * Pages below n that are live stay where they are; counts at and above n
+ * become 0.  Every table that names pages of the pool has to be given (a
+ * name outside [0, P) stays as it is). */
+CFP32_API cfp32_status cfp32_cache_compact(void *k_pages, int64_t kp_page, int64_t kp_head, int64_t kp_tok,
+                                 void *v_pages, int64_t vp_page, int64_t vp_head, int64_t vp_tok,
+                                 int kv_type, int64_t P, int64_t page, int64_t Hkv, int64_t D,
+                                 const int32_t *table, int64_t ld_table, const int32_t *refs,
+                                 int32_t *table_out, int64_t ld_out, int32_t *refs_out, int32_t *live,
+                                 int64_t S, int64_t W, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
