@@ -1,0 +1,168 @@
+// Device code shared by the attention kernels.
+#pragma once
+
+#include "attention.h"
+#include "device_common.h"
+
+namespace cfp32 {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }  // results below 2^-126: 0
+
+// The running maximum follows the scores only where they exceed it by more
+// than this (in powers of two): weights are then at most 2^kLazy, and most
+// steps leave the sums as they are.
+constexpr float kLazy = 4.0f;
+
+// The sequence that owns unit `id` of a packed batch, where sequence s starts
+// at unit cu[s] * mul / div + s (so sequences of n tokens own up to
+// ceil(n * mul / div) units, and some units belong to none).
+__device__ __forceinline__ int find_unit(const int32_t *cu, int S, int mul, int div, int64_t id, int64_t &start)
+{
+    int lo = 0, hi = S;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if ((int64_t)cu[mid] * mul / div + mid <= id) lo = mid;
+        else hi = mid;
+    }
+    start = (int64_t)cu[lo] * mul / div + lo;
+    return lo;
+}
+
+// A sequence of a packed batch: rows [q0, q0 + nq) and keys [k0, k0 + nk),
+// within the tensors whatever the offsets say.
+struct Sequence {
+    int q0, nq, k0, nk;
+    bool causal;
+    // How many keys row i sees.
+    __device__ __forceinline__ int limit(int i) const { return causal ? max(0, min(nk, nk - nq + i + 1)) : nk; }
+};
+
+__device__ __forceinline__ Sequence sequence(const PromptArgs &a, int s)
+{
+    Sequence r;
+    r.q0 = min(max(a.cu_q[s], 0), a.Tq);
+    r.nq = min(max(a.cu_q[s + 1], r.q0), a.Tq) - r.q0;
+    r.k0 = min(max(a.cu_k[s], 0), a.Tk);
+    r.nk = min(max(a.cu_k[s + 1], r.k0), a.Tk) - r.k0;
+    r.causal = a.causal;
+    return r;
+}
+
+__device__ __forceinline__ int decode_length(const DecodeArgs &a, int b)
+{
+    return min(max(a.lens[b], 0), a.W << a.page_log2);
+}
+
+// One row as it is written, by one wave: a lane scores a key, 64 at a time;
+// FP32 throughout.  What a row does not see is never multiplied, so it serves
+// the rows whose result is not finite (matrix instructions multiply masked
+// values by a weight of 0, which NaN and infinities survive), and pools
+// without pages.  key(j, k, v) gives the addresses of key j and its value, or
+// false where they cannot be read.
+template <class T, class Key>
+__device__ __attribute__((noinline)) void attend_row(const float *q, int D, int n, float scale, Key key, float *out)
+{
+    constexpr int kPer = kAttnMaxDim / 64;
+    const int lane = threadIdx.x & 63;
+    float m = -INFINITY, l = 0.0f, o[kPer] = {};
+    for (int64_t j0 = 0; j0 < n; j0 += 64) {
+        const int64_t j = j0 + lane;
+        const T *k = nullptr, *v = nullptr;
+        float s = -INFINITY;
+        if (j < n) {
+            s = NAN;
+            if (key((int)j, k, v)) {
+                s = 0.0f;
+                for (int d = 0; d < D; ++d) s = fmaf(q[d], (float)k[d], s);
+                s *= scale;
+            }
+        }
+        float mx = s;
+#pragma unroll
+        for (int x = 32; x; x >>= 1) mx = fmaxf(mx, __shfl_xor(mx, x));
+        const float mn = __any(s != s) ? NAN : fmaxf(m, mx);
+        const float c = m == -INFINITY ? 0.0f : exp2f((m - mn) * kLog2e);
+        const float p = s == -INFINITY ? 0.0f : exp2f((s - mn) * kLog2e);
+        float t = p;
+#pragma unroll
+        for (int x = 32; x; x >>= 1) t += __shfl_xor(t, x);
+        l = l * c + t;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] *= c;
+        m = mn;
+        for (int u = 0; u < 64 && j0 + u < n; ++u) {
+            const float pu = __shfl(p, u);
+            const T *vu = (const T *)__shfl((unsigned long long)v, u);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 64 * i < D) o[i] = vu ? fmaf(pu, (float)vu[lane + 64 * i], o[i]) : NAN;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+        if (lane + 64 * i < D) out[lane + 64 * i] = l == 0.0f ? 0.0f : o[i] / l;
+}
+
+// attend_row's keys: of a packed sequence, and of a decoded one.
+template <class T>
+__device__ __forceinline__ void attend_prompt_row(const PromptArgs &a, const Sequence &sq, int i, int h)
+{
+    const int kh = h / (a.Hq / a.Hkv);
+    const int64_t t = sq.q0 + i;
+    attend_row<T>(
+        (const float *)a.q.data + t * a.q.tok + h * a.q.head, a.D, sq.limit(i), a.scale,
+        [&](int j, const T *&k, const T *&v) {
+            k = (const T *)a.k.data + (int64_t)(sq.k0 + j) * a.k.tok + kh * a.k.head;
+            v = (const T *)a.v.data + (int64_t)(sq.k0 + j) * a.v.tok + kh * a.v.head;
+            return true;
+        },
+        a.out + t * a.out_tok + h * a.out_head);
+}
+
+template <class T>
+__device__ __forceinline__ void attend_decode_row(const DecodeArgs &a, int64_t b, int h)
+{
+    const int kh = h / (a.Hq / a.Hkv);
+    attend_row<T>(
+        a.q + b * a.q_seq + h * a.q_head, a.D, decode_length(a, (int)b), a.scale,
+        [&](int j, const T *&k, const T *&v) {
+            const int e = j >> a.page_log2, o = j - (e << a.page_log2);
+            const int page = a.table[(e < a.shared_pages ? 0 : b) * a.ld_table + e];
+            if (page < 0 || page >= a.P) return false;
+            k = (const T *)a.k.data + page * a.k.page + kh * a.k.head + o * a.k.tok;
+            v = (const T *)a.v.data + page * a.v.page + kh * a.v.head + o * a.v.tok;
+            return true;
+        },
+        a.out + b * a.out_seq + h * a.out_head);
+}
+
+// The power of two that brings `mx` (the largest magnitude of a group, >= 0)
+// to [2^14, 2^15), the top of FP16's range; 0 for zero.
+__device__ __forceinline__ int top_shift(float mx)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, mx);
+    if (u == 0 || u >= 0x7F800000u) return 0;
+    return 14 - (__builtin_amdgcn_frexp_expf(mx) - 1);
+}
+
+// x scaled by 2^e as two FP16 parts with 22 significant bits together (at the
+// same scale: hi is below 2^15, so lo keeps its bits down to 2^-24).
+__device__ __forceinline__ void split_scaled(float x, int e, _Float16 &hi, _Float16 &lo)
+{
+    const float y = __builtin_amdgcn_ldexpf(x, e);
+    hi = (_Float16)y;
+    lo = (_Float16)(y - (float)hi);
+}
+
+// What several blocks contribute to one row (decode): unnormalised sums,
+// their maxima (in powers of two) and weights.  Slot i of row r is entry
+// r * slots + i.
+struct Partials {
+    float *o;   // [rows * slots, dim]
+    float *m, *l;
+    int slots, dim;
+};
+
+}  // namespace cfp32
