@@ -48,6 +48,9 @@ struct DecodeArgs {
 
 size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
 hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream);
+// Its form for many rows (attention_tile.hip); FP16 K and V have to allow 16-byte loads.
+size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
+hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream);
 
 size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int page_log2,
                                   int64_t shared_pages, bool kv_f16);

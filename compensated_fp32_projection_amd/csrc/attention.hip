@@ -19,6 +19,7 @@
 // These products are bounded by memory, not by the matrix units: 16 rows
 // against FP32 keys need 1024 cycles of a SIMD for 8 KiB at D = 64, which is
 // 19 TB/s over the chip.
+#include <stdlib.h>
 #include "attention_device.h"
 
 namespace cfp32 {
@@ -533,14 +534,19 @@ bool wide(const void *p, int64_t strides, int D, bool f16)
         }                                                                                             \
     } while (0)
 
-size_t attention_prompt_workspace(int64_t, int64_t, int64_t, int64_t, bool) { return 0; }
+size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16)
+{
+    return prompt_tile_workspace(S, Tk, Hkv, D, kv_f16);
+}
 
-hipError_t launch_attention_prompt(const PromptArgs &a, void *, hipStream_t stream)
+hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream)
 {
     const int g = a.Hq / a.Hkv;
     const int64_t units = (int64_t)a.Tq * g / kRows + a.S;
     if (a.Hkv > 65535 || units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     const bool w = wide(a.k.data, a.k.tok | a.k.head, a.D, a.kv_f16) && wide(a.v.data, a.v.tok | a.v.head, a.D, a.kv_f16);
+    static const int force = getenv("CF_FORCE") ? atoi(getenv("CF_FORCE")) : 0;
+    if (a.Tk > 0 && (w || !a.kv_f16) && (force == 2 || (force == 0 && a.Tq >= 1024))) return launch_prompt_tile(a, workspace, stream);
     const dim3 grid((unsigned)units, (unsigned)a.Hkv);
     CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, w, grid, 64 * kWaves, a);
     return hipGetLastError();

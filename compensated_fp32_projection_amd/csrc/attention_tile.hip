@@ -1,0 +1,506 @@
+// Attention of many rows that see the same keys: long packed prompts, and the
+// prefix that a decoded batch shares.
+//
+// A block's waves hold 32 rows each (tokens x heads of one K/V head: grouped
+// heads are rows like others) and go through the keys 64 at a time.  A tile
+// of K and V comes from memory straight into LDS (global_load_lds, 16 bytes a
+// lane) while the tile before it is multiplied; one barrier to a tile.
+//   * Products: v_mfma_f32_32x32x16_f16 with FP32 sums.  An FP32 operand is
+//     scaled by a power of two to the top of FP16's range and split into two
+//     FP16 parts of 22 bits together (rows on the way in, weights as they are
+//     made, FP32 K and V in a pass over them beforehand, tile by tile);
+//     high x high, high x low and low x high are summed, low x low (below
+//     2^-22) is not.  FP16 K and V are exact: two products.  The parts share
+//     one scale, so all products go to the same accumulators.
+//   * S^T = K Q^T leaves a lane with 32 scores of one row (column lane % 32):
+//     its maximum and sum need one exchange, with lane + 32.  O^T = V^T P^T
+//     takes the weights where the scores lay: keys 16 s + 4 (lane / 32) + j
+//     and + 8, j < 4, are its s-th step's, and V is read in that order.
+//   * V lies in LDS as in memory, a row to a key; ds_read_b64_tr_b16 gives
+//     lane j of 16 the j-th column of four rows, so nothing is transposed.
+//   * 16-byte chunks of a row are XORed with the row, for K (32 rows, one
+//     chunk) so that 16 neighbours fall in different banks, for V (8 rows,
+//     64 bytes) so that four rows do.
+//   * The running maximum is followed lazily (kLazy), so that most tiles do
+//     not touch the output sums.
+#include "attention_device.h"
+
+#define CFP32_LDS __attribute__((address_space(3)))
+#define CFP32_GLOBAL __attribute__((address_space(1)))
+
+namespace cfp32 {
+
+namespace {
+
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef short short8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kTile = 64;       // keys of a tile
+constexpr int kWaveRows = 32;
+constexpr int kTopWeight = 11;  // weights are multiplied at 2^kTopWeight: up to 2^(kTopWeight + kLazy) = 2^15
+constexpr int kNoValues = 1 << 20;  // shift of a tile whose values are all zero
+
+// Planes of FP32 K and V, cut in two: for each K/V head and tile [K hi, K lo,
+// V hi, V lo][64][DP] FP16, zeros beyond the sequence and beyond D, and the
+// shifts of K and V.
+struct Planes {
+    char *tiles;
+    int32_t *shifts;
+    int64_t slots;  // tiles of a head: sequence s starts at cu_k[s] / 64 + s
+};
+
+template <int DP>
+__host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2 * planes * kTile * DP * 2; }
+
+// ---- Where a tile's rows are ------------------------------------------------------
+
+struct PlaneSource {
+    const char *tiles;      // of this head and sequence
+    const int32_t *shifts;
+    template <int DP>
+    __device__ __forceinline__ const char *at(int value, int plane, int tile, int row, int chunk) const
+    {
+        return tiles + (int64_t)tile * tile_bytes<DP>(2) + ((value * 2 + plane) * kTile + row) * (DP * 2) + chunk * 16;
+    }
+    __device__ __forceinline__ int shift(int value, int tile) const { return shifts[2 * tile + value]; }
+};
+
+struct PackedSource {
+    const char *k, *v;      // key 0
+    int64_t k_tok, v_tok;   // bytes
+    int last, chunks;       // a key or chunk beyond the last repeats one: it meets a weight or an element of 0
+    template <int DP>
+    __device__ __forceinline__ const char *at(int value, int, int tile, int row, int chunk) const
+    {
+        const int64_t j = min(tile * kTile + row, last);
+        return (value ? v + j * v_tok : k + j * k_tok) + (chunk < chunks ? chunk : 0) * 16;
+    }
+    __device__ __forceinline__ int shift(int, int) const { return 0; }
+};
+
+constexpr int kPageIds = 2048;  // page ids of one block
+
+struct PagedSource {
+    const char *k, *v;      // the head in page 0
+    int64_t k_page, v_page, k_tok, v_tok;
+    const int *ids;         // LDS: pages from the one of key `first` on
+    int first, last, chunks, lg;
+    template <int DP>
+    __device__ __forceinline__ const char *at(int value, int, int tile, int row, int chunk) const
+    {
+        const int j = min(tile * kTile + row, last);
+        const int64_t p = ids[(j >> lg) - (first >> lg)], o = j & ((1 << lg) - 1);
+        return (value ? v + p * v_page + o * v_tok : k + p * k_page + o * k_tok) + (chunk < chunks ? chunk : 0) * 16;
+    }
+    __device__ __forceinline__ int shift(int, int) const { return 0; }
+};
+
+// ---- The rows of a wave -------------------------------------------------------------
+
+template <int DP>
+struct WaveRows {
+    floatx16_t o[DP / 32];  // O^T: this lane's column; row r of block b is dim 32 b + 8 (r / 4) + 4 (lane / 32) + r % 4
+    float m, l;             // in powers of two; l of this lane's keys
+    int scale;              // o is at 2^scale
+};
+
+// Keys of tiles [t0, t1) for this lane's row q, which sees the first `limit`
+// keys; `most`: the most that a row of the wave sees (uniform, 0 for a wave
+// without rows).
+template <int DP, int PL, int NW, class Source>
+__device__ __forceinline__ void attend_tiles(const float *q, int D, int limit, int most, float scale, int t0, int t1,
+                                             const Source &src, uint4 *buf0, uint4 *buf1, WaveRows<DP> &to)
+{
+    constexpr int CH = DP / 8;         // 16-byte chunks of a row
+    constexpr int PLANE = kTile * CH;  // of a plane
+    constexpr int KK = DP / 16, DB = DP / 32;
+    constexpr int PER = CH / NW;       // loads (64 chunks) of a wave and plane
+    static_assert(CH % NW == 0, "loads are dealt evenly");
+    const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // A row's chunks are XORed with these.
+    auto k_swizzle = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
+    auto v_swizzle = [](int row) { return CH == 16 ? (row & 3) << 2 | ((row >> 2) & 3) : (row & 2) << 1 | ((row >> 2) & 3); };
+
+    auto fetch = [&](int tile, uint4 *buf) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int piece = wave * PER + i, slot = piece * 64 + lane, row = slot / CH, c = slot % CH;
+#pragma unroll
+            for (int value = 0; value < 2; ++value)
+#pragma unroll
+                for (int p = 0; p < PL; ++p) {
+                    const char *from = src.template at<DP>(value, p, tile, row, c ^ (value ? v_swizzle(row) : k_swizzle(row)));
+                    __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)from,
+                                                     (CFP32_LDS void *)(buf + (value * PL + p) * PLANE + piece * 64), 16, 0, 0);
+                }
+        }
+    };
+    fetch(t0, buf0);
+
+    // The row, at 2^e2, as the right operand of the scores.
+    half8_t qh[KK], ql[KK];
+    float f = scale * kLog2e;
+    {
+        float mx = 0.0f;
+        int e2;
+        {
+            float x[KK][8];
+#pragma unroll
+            for (int i = 0; i < KK; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int d = 16 * i + 8 * half + e;
+                    x[i][e] = d < D ? q[d] : 0.0f;
+                    const float ax = fabsf(x[i][e]);
+                    mx = fmaxf(mx, ax < INFINITY ? ax : 0.0f);
+                }
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            e2 = top_shift(mx);
+#pragma unroll
+            for (int i = 0; i < KK; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    _Float16 h, w;
+                    split_scaled(x[i][e], e2, h, w);
+                    qh[i][e] = h, ql[i][e] = w;
+                }
+        }
+        f = __builtin_amdgcn_ldexpf(f, -e2);
+    }
+    float m = -INFINITY, l = 0.0f;
+    int cv = kNoValues;  // values are summed at 2^(kTopWeight + cv)
+    floatx16_t o[DB];
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[b][r] = 0.0f;
+
+    // This lane's byte in a plane: K's row col, chunk `half`; V's row 4 half +
+    // (lane % 16) / 4, columns 16 ((lane / 16) % 2) + 4 (lane % 4).
+    const int k_at = (col * CH + (half ^ k_swizzle(col))) * 16;
+    const int i16 = lane & 15, v_row = 4 * half + (i16 >> 2), v_chunk = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+    const int v_at = (v_row * CH + (v_chunk ^ v_swizzle(v_row))) * 16 + 8 * (i16 & 1);
+
+    auto multiply = [&](int tile, const uint4 *buf) {
+        const int j0 = tile * kTile;
+        if (j0 >= most) return;
+        const char *lds = (const char *)buf;
+        floatx16_t s[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KK; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const char *at = lds + (k_at ^ (i * 32)) + b * 32 * CH * 16;
+                const half8_t kh = *reinterpret_cast<const half8_t *>(at);
+                if (PL == 2) {
+                    const half8_t kl = *reinterpret_cast<const half8_t *>(at + PLANE * 16);
+                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl, qh[i], s[b], 0, 0, 0);
+                }
+                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, ql[i], s[b], 0, 0, 0);
+                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, qh[i], s[b], 0, 0, 0);
+            }
+        const float ft = PL == 2 ? __builtin_amdgcn_ldexpf(f, -src.shift(0, tile)) : f;
+        float mx = -INFINITY;
+        if (__any(j0 + kTile > limit)) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = j0 + 32 * b + 8 * (r / 4) + 4 * half + r % 4;
+                    s[b][r] = j < limit ? s[b][r] * ft : -INFINITY;
+                }
+        } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[b][r] *= ft;
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][r]);
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        int up = 0;  // this tile's values beside the sums' scale
+        bool lower = false;
+        if (PL == 2) {
+            int ev = src.shift(1, tile);
+            if (ev == kNoValues) ev = cv;
+            lower = ev < cv;
+            up = lower ? 1 : min(ev - cv, 60);  // 2^(kTopWeight - 60): nothing in FP16
+            if (lower) {
+                // A step of room: values a little larger do not move the scale again.
+                const int next = ev - 1;
+                const float c = cv == kNoValues ? 1.0f : __builtin_amdgcn_ldexpf(1.0f, max(next - cv, -200));
+#pragma unroll
+                for (int b = 0; b < DB; ++b) o[b] *= c;
+                cv = next;
+            }
+        }
+        if (__any(mx > m + kLazy)) {
+            const float mn = fmaxf(m, mx);
+            const float c = mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
+            m = mn;
+            l *= c;
+#pragma unroll
+            for (int b = 0; b < DB; ++b) o[b] *= c;
+        }
+        const float base = (m == -INFINITY ? 0.0f : m) - (float)(kTopWeight - up);
+        float sum = 0.0f;
+        half8_t ph[4], pl[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p = exp2_raw(s[t / 2][8 * (t % 2) + e] - base);
+                sum += p;
+                const _Float16 h = (_Float16)p;
+                ph[t][e] = h;
+                pl[t][e] = (_Float16)(p - (float)h);
+            }
+        l = PL == 2 ? fmaf(sum, __builtin_amdgcn_ldexpf(1.0f, up), l) : l + sum;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                half8_t v[PL];
+#pragma unroll
+                for (int p = 0; p < PL; ++p) {
+                    short4_t x[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        x[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CFP32_LDS short4_t *)(
+                            (CFP32_LDS char *)lds + ((v_at ^ (b * 64) ^ (u * 32)) + ((PL + p) * PLANE + (16 * t + 8 * u) * CH) * 16)));
+                    v[p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+                if (PL == 2) o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[PL - 1], ph[t], o[b], 0, 0, 0);
+                o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0], pl[t], o[b], 0, 0, 0);
+                o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0], ph[t], o[b], 0, 0, 0);
+            }
+    };
+    // A tile is multiplied when every wave's part of it has landed and no wave
+    // reads the other buffer any more; the next one is then on its way there.
+    auto landed = [] {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+        __syncthreads();
+    };
+    for (int t = t0; t < t1; t += 2) {
+        landed();
+        if (t + 1 < t1) fetch(t + 1, buf1);
+        multiply(t, buf0);
+        if (t + 1 >= t1) break;
+        landed();
+        if (t + 2 < t1) fetch(t + 2, buf0);
+        multiply(t + 1, buf1);
+    }
+#pragma unroll
+    for (int b = 0; b < DB; ++b) to.o[b] = o[b];
+    to.m = m;
+    to.l = l + __shfl_xor(l, 32);
+    to.scale = kTopWeight + (cv == kNoValues ? 0 : PL == 2 ? cv : 0);
+}
+
+// Four consecutive values; `wide`: the address is a multiple of 16 bytes and all four are there.
+__device__ __forceinline__ void store4(float *out, const float (&y)[4], int n, bool wide)
+{
+    if (wide && n >= 4) {
+        *reinterpret_cast<floatx4_t *>(out) = floatx4_t{y[0], y[1], y[2], y[3]};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n) out[e] = y[e];
+}
+
+// ---- Long prompts -------------------------------------------------------------------
+
+template <class T, int DP, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, Planes planes)
+{
+    constexpr int PL = sizeof(T) == 4 ? 2 : 1;
+    constexpr int kBlockRows = NW * kWaveRows;
+    __shared__ uint4 buf0[2 * PL * kTile * DP / 8];
+    __shared__ uint4 buf1[2 * PL * kTile * DP / 8];
+    const int g = a.Hq / a.Hkv;
+    const int kh = blockIdx.x % a.Hkv;
+    const int64_t id = (gridDim.x - 1 - blockIdx.x) / a.Hkv;  // the rows that see most first
+    int64_t start;
+    const int sid = find_unit(a.cu_q, a.S, g, kBlockRows, id, start);
+    const Sequence sq = sequence(a, sid);
+    const int64_t n = (int64_t)sq.nq * g, r0 = (id - start) * kBlockRows;
+    if (id < start || r0 >= n) return;
+    const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
+    const int i = (int)(r / g), h = kh * g + (int)(r - (int64_t)i * g);
+    const bool rows = first < n;
+    const int most = rows ? sq.limit((int)(min(first + kWaveRows, n) - 1) / g) : 0;
+    const int keys = sq.limit((int)((min(r0 + kBlockRows, n) - 1) / g));
+    const int limit = sq.limit(i);
+    const float *q = (const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head;
+    WaveRows<DP> w;
+    const int tiles = (keys + kTile - 1) / kTile;
+    if (tiles == 0) {
+        w.m = -INFINITY, w.l = 0.0f, w.scale = 0;
+#pragma unroll
+        for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w.o[b][e] = 0.0f;
+    } else if constexpr (PL == 2) {
+        const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
+        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot};
+        attend_tiles<DP, PL, NW>(q, a.D, limit, most, a.scale, 0, tiles, src, buf0, buf1, w);
+    } else {
+        const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
+                                  (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
+                                  a.k.tok * 2, a.v.tok * 2, sq.nk - 1, a.D / 8};
+        attend_tiles<DP, PL, NW>(q, a.D, limit, most, a.scale, 0, tiles, src, buf0, buf1, w);
+    }
+    if (!rows) return;
+    const bool live = first + (lane & 31) < n;
+    // l is summed at 2^kTopWeight, o at 2^scale.
+    const float inv = w.l == 0.0f ? 0.0f : __builtin_amdgcn_ldexpf(1.0f / w.l, kTopWeight);
+    float *out = a.out + (sq.q0 + i) * a.out_tok + h * a.out_head;
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)((a.out_tok | a.out_head) * 4)) & 15) == 0;
+    bool odd = false;
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int d = 32 * b + 8 * c + 4 * half;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[e] = __builtin_amdgcn_ldexpf(w.o[b][4 * c + e] * inv, -w.scale);
+                odd |= d + e < a.D && !(fabsf(y[e]) < INFINITY);
+            }
+            if (live) store4(out + d, y, a.D - d, wide);
+        }
+    uint64_t redo = __ballot(odd && live);
+    redo = (redo | redo >> 32) & 0xFFFFFFFFull;
+    for (; redo; redo &= redo - 1) {
+        const int64_t rr = first + __builtin_ctzll(redo);
+        const int ri = (int)(rr / g);
+        attend_prompt_row<T>(a, sq, ri, kh * g + (int)(rr - (int64_t)ri * g));
+    }
+}
+
+// FP32 K and V of one tile and head as two FP16 planes each.
+template <int DP>
+__global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes planes)
+{
+    constexpr int CH = DP / 8, PER = kTile * CH / 256;
+    __shared__ float most[2][4];
+    const int kh = blockIdx.y;
+    int64_t start;
+    const int sid = find_unit(a.cu_k, a.S, 1, kTile, blockIdx.x, start);
+    const Sequence sq = sequence(a, sid);
+    const int64_t j0 = (blockIdx.x - start) * kTile;
+    if (blockIdx.x < start || j0 >= sq.nk) return;
+    const int64_t slot = kh * planes.slots + blockIdx.x;
+    const bool wide = a.D % 4 == 0 &&
+                      ((reinterpret_cast<uintptr_t>(a.k.data) | reinterpret_cast<uintptr_t>(a.v.data) |
+                        (uintptr_t)((a.k.tok | a.k.head | a.v.tok | a.v.head) * 4)) & 15) == 0;
+    float x[2][PER][8], mx[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int value = 0; value < 2; ++value)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int at = threadIdx.x + 256 * i, row = at / CH, d = at % CH * 8;
+            const HeadsView &t = value ? a.v : a.k;
+            const float *p = (const float *)t.data + (sq.k0 + j0 + row) * t.tok + kh * t.head + d;
+            const bool there = j0 + row < sq.nk;
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                if (wide) {
+                    floatx4_t y = {0, 0, 0, 0};
+                    if (there && d + e < a.D) y = *reinterpret_cast<const floatx4_t *>(p + e);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) x[value][i][e + u] = y[u];
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) x[value][i][e + u] = there && d + e + u < a.D ? p[e + u] : 0.0f;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float ax = fabsf(x[value][i][e + u]);
+                    mx[value] = fmaxf(mx[value], ax < INFINITY ? ax : 0.0f);
+                }
+            }
+        }
+#pragma unroll
+    for (int value = 0; value < 2; ++value) {
+#pragma unroll
+        for (int o = 32; o; o >>= 1) mx[value] = fmaxf(mx[value], __shfl_xor(mx[value], o));
+        if ((threadIdx.x & 63) == 0) most[value][threadIdx.x >> 6] = mx[value];
+    }
+    __syncthreads();
+    char *tile = planes.tiles + slot * tile_bytes<DP>(2);
+#pragma unroll
+    for (int value = 0; value < 2; ++value) {
+        const float top = fmaxf(fmaxf(most[value][0], most[value][1]), fmaxf(most[value][2], most[value][3]));
+        const int e2 = top_shift(top);
+        if (threadIdx.x == 0) planes.shifts[2 * slot + value] = value && top == 0.0f ? kNoValues : e2;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int at = threadIdx.x + 256 * i;
+            half8_t hi, lo;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                _Float16 h, w;
+                split_scaled(x[value][i][e], e2, h, w);
+                hi[e] = h, lo[e] = w;
+            }
+            char *to = tile + (int64_t)value * 2 * kTile * DP * 2 + at * 16;
+            *reinterpret_cast<half8_t *>(to) = hi;
+            *reinterpret_cast<half8_t *>(to + kTile * DP * 2) = lo;
+        }
+    }
+}
+
+}  // namespace
+
+size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16)
+{
+    if (kv_f16) return 0;
+    const int64_t tiles = (Tk / kTile + S) * Hkv;
+    return (size_t)(tiles * ((D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)) + 8));
+}
+
+hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream)
+{
+    const int g = a.Hq / a.Hkv;
+    Planes planes = {};
+    if (!a.kv_f16) {
+        planes.slots = a.Tk / kTile + a.S;
+        planes.tiles = (char *)workspace;
+        planes.shifts = (int32_t *)(planes.tiles + planes.slots * a.Hkv * (a.D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)));
+        if (planes.slots > 0x7FFFFFFF || a.Hkv > 65535) return hipErrorInvalidConfiguration;
+        const dim3 grid((unsigned)planes.slots, (unsigned)a.Hkv);
+        if (a.D <= 64) prompt_planes_kernel<64><<<grid, 256, 0, stream>>>(a, planes);
+        else prompt_planes_kernel<128><<<grid, 256, 0, stream>>>(a, planes);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+#define CFP32_PROMPT(T, DP, NW)                                                                                    \
+    do {                                                                                                           \
+        const int64_t units = ((int64_t)a.Tq * g / (NW * kWaveRows) + a.S) * a.Hkv;                                \
+        if (units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;                                               \
+        prompt_tile_kernel<T, DP, NW><<<(unsigned)units, 64 * NW, 0, stream>>>(a, planes);                         \
+    } while (0)
+    if (a.kv_f16) {
+        if (a.D <= 64) CFP32_PROMPT(_Float16, 64, 4);
+        else CFP32_PROMPT(_Float16, 128, 4);
+    } else {
+        if (a.D <= 64) CFP32_PROMPT(float, 64, 4);
+        else CFP32_PROMPT(float, 128, 8);
+    }
+#undef CFP32_PROMPT
+    return hipGetLastError();
+}
+
+}  // namespace cfp32
