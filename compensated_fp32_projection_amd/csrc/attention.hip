@@ -100,7 +100,7 @@ struct Joined {
 // `limit` keys; keys [lo, hi) (lo a multiple of 16 if pages are to be read
 // 16 keys at a time), every kWaves-th step of them.
 template <class T, int DP, bool WIDE, class Keys>
-__device__ __forceinline__ void attend_rows(const float *q, int D, int limit, float scale, int lo, int hi, Keys keys,
+__device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, int limit, float scale, int lo, int hi, Keys keys,
                                             Joined &to)
 {
     constexpr bool F16 = sizeof(T) == 2;
@@ -149,15 +149,20 @@ __device__ __forceinline__ void attend_rows(const float *q, int D, int limit, fl
         // The row, as the right operand of the score products.
         float f = scale * kLog2e;
         half8_t qh[F16 ? KK : 1], ql[F16 ? KK : 1];
-        float qf[F16 ? 1 : KK][KE];
+        float x[KK][KE];
+        if (q_wide) {
+#pragma unroll
+            for (int i = 0; i < KK; ++i) load_floats<KE, true>(q, (i * 4 + quad) * KE, D, x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KK; ++i) load_floats<KE, false>(q, (i * 4 + quad) * KE, D, x[i]);
+        }
         if constexpr (F16) {
-            float x[KK][KE], mx = 0.0f;
+            float mx = 0.0f;
 #pragma unroll
             for (int i = 0; i < KK; ++i)
 #pragma unroll
                 for (int e = 0; e < KE; ++e) {
-                    const int d = (i * 4 + quad) * KE + e;
-                    x[i][e] = d < D ? q[d] : 0.0f;
                     const float ax = fabsf(x[i][e]);
                     mx = fmaxf(mx, ax < INFINITY ? ax : 0.0f);
                 }
@@ -173,14 +178,6 @@ __device__ __forceinline__ void attend_rows(const float *q, int D, int limit, fl
                     qh[i][e] = h, ql[i][e] = w;
                 }
             f = __builtin_amdgcn_ldexpf(f, -e2);
-        } else {
-#pragma unroll
-            for (int i = 0; i < KK; ++i)
-#pragma unroll
-                for (int e = 0; e < KE; ++e) {
-                    const int d = (i * 4 + quad) * KE + e;
-                    qf[i][e] = d < D ? q[d] : 0.0f;
-                }
         }
 
         for (; kb < hi; kb += kWaves * kStep) {
@@ -199,7 +196,7 @@ __device__ __forceinline__ void attend_rows(const float *q, int D, int limit, fl
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            s[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(kr[b][i][e], qf[i][e], s[b], 0, 0, 0);
+                            s[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(kr[b][i][e], x[i][e], s[b], 0, 0, 0);
                     }
                 }
             }
@@ -309,7 +306,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs 
                              (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                              a.k.tok * (int64_t)sizeof(T), a.v.tok * (int64_t)sizeof(T)};
     const int hi = sq.limit((int)((r0 + live - 1) / g));
-    attend_rows<T, DP, WIDE>((const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head, a.D, sq.limit(i), a.scale, 0,
+    attend_rows<T, DP, WIDE>((const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head,
+                             rows_wide(a.q.data, a.q.tok | a.q.head, a.D), a.D, sq.limit(i), a.scale, 0,
                              hi, keys, sh);
     if (threadIdx.x < kRows) sh.unfinished[threadIdx.x] = 0;
     __syncthreads();
@@ -388,7 +386,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs 
                             a.k.page * (int64_t)sizeof(T), a.v.page * (int64_t)sizeof(T),
                             a.k.tok * (int64_t)sizeof(T), a.v.tok * (int64_t)sizeof(T),
                             a.table + (common ? 0 : b * a.ld_table), a.page_log2, a.P, 0x7FFFFFFF};
-    attend_rows<T, DP, WIDE>(a.q + b * a.q_seq + h * a.q_head, a.D, common ? min(n, shared_len) : n, a.scale, lo, hi, keys,
+    attend_rows<T, DP, WIDE>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, common ? min(n, shared_len) : n, a.scale, lo, hi, keys,
                              sh);
     if (threadIdx.x < kRows) sh.unfinished[threadIdx.x] = 0;
     __syncthreads();

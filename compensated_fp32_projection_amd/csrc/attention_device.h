@@ -55,12 +55,41 @@ __device__ __forceinline__ int decode_length(const DecodeArgs &a, int b)
     return min(max(a.lens[b], 0), a.W << a.page_log2);
 }
 
+// Where one row's keys are, for attend_row: packed rows of a head, ...
+template <class T>
+struct PackedRow {
+    const T *k, *v;  // key 0
+    int64_t k_tok, v_tok;
+    __device__ __forceinline__ bool operator()(int j, const T *&kj, const T *&vj) const
+    {
+        kj = k + j * k_tok;
+        vj = v + j * v_tok;
+        return true;
+    }
+};
+// ... or pages.
+template <class T>
+struct PagedRow {
+    PagesView k, v;  // of the head
+    const int32_t *table, *shared_table;
+    int shared_pages, lg, P;
+    __device__ __forceinline__ bool operator()(int j, const T *&kj, const T *&vj) const
+    {
+        const int e = j >> lg, o = j - (e << lg), page = (e < shared_pages ? shared_table : table)[e];
+        if (page < 0 || page >= P) return false;
+        kj = (const T *)k.data + page * k.page + o * k.tok;
+        vj = (const T *)v.data + page * v.page + o * v.tok;
+        return true;
+    }
+};
+
 // One row as it is written, by one wave: a lane scores a key, 64 at a time;
 // FP32 throughout.  What a row does not see is never multiplied, so it serves
 // the rows whose result is not finite (matrix instructions multiply masked
 // values by a weight of 0, which NaN and infinities survive), and pools
-// without pages.  key(j, k, v) gives the addresses of key j and its value, or
-// false where they cannot be read.
+// without pages.  `key` gives the addresses of a key and its value, or false
+// where they cannot be read.  Not inlined: it is rare, and would cost the
+// kernels that call it registers.
 template <class T, class Key>
 __device__ __attribute__((noinline)) void attend_row(const float *q, int D, int n, float scale, Key key, float *out)
 {
@@ -105,37 +134,53 @@ __device__ __attribute__((noinline)) void attend_row(const float *q, int D, int 
         if (lane + 64 * i < D) out[lane + 64 * i] = l == 0.0f ? 0.0f : o[i] / l;
 }
 
-// attend_row's keys: of a packed sequence, and of a decoded one.
+// Row i of a packed sequence, and sequence b's row, of head h.
 template <class T>
 __device__ __forceinline__ void attend_prompt_row(const PromptArgs &a, const Sequence &sq, int i, int h)
 {
     const int kh = h / (a.Hq / a.Hkv);
     const int64_t t = sq.q0 + i;
-    attend_row<T>(
-        (const float *)a.q.data + t * a.q.tok + h * a.q.head, a.D, sq.limit(i), a.scale,
-        [&](int j, const T *&k, const T *&v) {
-            k = (const T *)a.k.data + (int64_t)(sq.k0 + j) * a.k.tok + kh * a.k.head;
-            v = (const T *)a.v.data + (int64_t)(sq.k0 + j) * a.v.tok + kh * a.v.head;
-            return true;
-        },
-        a.out + t * a.out_tok + h * a.out_head);
+    attend_row<T>((const float *)a.q.data + t * a.q.tok + h * a.q.head, a.D, sq.limit(i), a.scale,
+                  PackedRow<T>{(const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head,
+                               (const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head, a.k.tok, a.v.tok},
+                  a.out + t * a.out_tok + h * a.out_head);
 }
 
 template <class T>
 __device__ __forceinline__ void attend_decode_row(const DecodeArgs &a, int64_t b, int h)
 {
     const int kh = h / (a.Hq / a.Hkv);
-    attend_row<T>(
-        a.q + b * a.q_seq + h * a.q_head, a.D, decode_length(a, (int)b), a.scale,
-        [&](int j, const T *&k, const T *&v) {
-            const int e = j >> a.page_log2, o = j - (e << a.page_log2);
-            const int page = a.table[(e < a.shared_pages ? 0 : b) * a.ld_table + e];
-            if (page < 0 || page >= a.P) return false;
-            k = (const T *)a.k.data + page * a.k.page + kh * a.k.head + o * a.k.tok;
-            v = (const T *)a.v.data + page * a.v.page + kh * a.v.head + o * a.v.tok;
-            return true;
-        },
-        a.out + b * a.out_seq + h * a.out_head);
+    PagedRow<T> key = {a.k, a.v, a.table + b * a.ld_table, a.table, a.shared_pages, a.page_log2, a.P};
+    key.k.data = (T *)a.k.data + kh * a.k.head;
+    key.v.data = (T *)a.v.data + kh * a.v.head;
+    attend_row<T>(a.q + b * a.q_seq + h * a.q_head, a.D, decode_length(a, (int)b), a.scale, key,
+                  a.out + b * a.out_seq + h * a.out_head);
+}
+
+// N values of a row of D from p + d on, zeros from D on.  WIDE: p is a
+// multiple of 16 bytes, d, N and D of 4.
+template <int N, bool WIDE>
+__device__ __forceinline__ void load_floats(const float *p, int d, int D, float (&x)[N])
+{
+    if (WIDE) {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const floatx4_t t = *reinterpret_cast<const floatx4_t *>(p + (d + e < D ? d + e : 0));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[e + u] = d + e < D ? t[u] : 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float t = p[d + e < D ? d + e : 0];
+            x[e] = d + e < D ? t : 0.0f;
+        }
+    }
+}
+
+__device__ __forceinline__ bool rows_wide(const void *p, int64_t strides, int D)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(strides * 4)) & 15) == 0 && D % 4 == 0;
 }
 
 // The power of two that brings `mx` (the largest magnitude of a group, >= 0)

@@ -23,17 +23,22 @@
 //     64 bytes) so that four rows do.
 //   * The running maximum is followed lazily (kLazy), so that most tiles do
 //     not touch the output sums.
+#include <type_traits>
+
 #include "attention_device.h"
 
 #define CFP32_LDS __attribute__((address_space(3)))
 #define CFP32_GLOBAL __attribute__((address_space(1)))
+#define CFP32_CONSTANT __attribute__((address_space(4)))
 
 namespace cfp32 {
 
 namespace {
 
 typedef short short4_t __attribute__((ext_vector_type(4)));
-typedef short short8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 64;       // keys of a tile
 constexpr int kWaveRows = 32;
@@ -57,12 +62,18 @@ __host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2
 struct PlaneSource {
     const char *tiles;      // of this head and sequence
     const int32_t *shifts;
+    int last;               // a tile beyond the last repeats it: no row sees it
     template <int DP>
     __device__ __forceinline__ const char *at(int value, int plane, int tile, int row, int chunk) const
     {
-        return tiles + (int64_t)tile * tile_bytes<DP>(2) + ((value * 2 + plane) * kTile + row) * (DP * 2) + chunk * 16;
+        const char *plane_at = tiles + (int64_t)min(tile, last) * tile_bytes<DP>(2) + (value * 2 + plane) * (kTile * DP * 2);
+        return plane_at + (uint32_t)(row * (DP * 2) + chunk * 16);
     }
-    __device__ __forceinline__ int shift(int value, int tile) const { return shifts[2 * tile + value]; }
+    // A scalar load: a vector load would be waited for behind the tiles on their way.
+    __device__ __forceinline__ int shift(int value, int tile) const
+    {
+        return ((const CFP32_CONSTANT int32_t *)shifts)[2 * min(tile, last) + value];
+    }
 };
 
 struct PackedSource {
@@ -95,6 +106,19 @@ struct PagedSource {
     __device__ __forceinline__ int shift(int, int) const { return 0; }
 };
 
+// Two weights as high and low FP16 parts (to nearest even; p - high is exact).
+// The difference takes the FP16 operand as it is, which the compiler does not
+// find by itself (it converts back first).  Only that is written out: what
+// reads an exponential's result too early is for the compiler to see.
+__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t &hi, uint32_t &lo)
+{
+    hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{p0, p1}, half2_t));
+    float r0, r1;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r0) : "v"(hi), "v"(p0));
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r1) : "v"(hi), "v"(p1));
+    lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{r0, r1}, half2_t));
+}
+
 // ---- The rows of a wave -------------------------------------------------------------
 
 template <int DP>
@@ -104,12 +128,12 @@ struct WaveRows {
     int scale;              // o is at 2^scale
 };
 
-// Keys of tiles [t0, t1) for this lane's row q, which sees the first `limit`
-// keys; `most`: the most that a row of the wave sees (uniform, 0 for a wave
-// without rows).
+// Keys of tiles [t0, t1), at least one, for this lane's row q, which sees the
+// first `limit` keys.  Tiles go in pairs (one body of code for each pair of
+// buffers): after an odd number, one that no row sees.
 template <int DP, int PL, int NW, class Source>
-__device__ __forceinline__ void attend_tiles(const float *q, int D, int limit, int most, float scale, int t0, int t1,
-                                             const Source &src, uint4 *buf0, uint4 *buf1, WaveRows<DP> &to)
+__device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D, int limit, float scale, int t0, int t1,
+                                             const Source &src, uint4 *k0, uint4 *k1, uint4 *v0, uint4 *v1, WaveRows<DP> &to)
 {
     constexpr int CH = DP / 8;         // 16-byte chunks of a row
     constexpr int PLANE = kTile * CH;  // of a plane
@@ -123,36 +147,42 @@ __device__ __forceinline__ void attend_tiles(const float *q, int D, int limit, i
     auto k_swizzle = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
     auto v_swizzle = [](int row) { return CH == 16 ? (row & 3) << 2 | ((row >> 2) & 3) : (row & 2) << 1 | ((row >> 2) & 3); };
 
-    auto fetch = [&](int tile, uint4 *buf) {
+    auto fetch = [&](int value, int tile, uint4 *buf) {
+        int from_lane = lane;
+        asm("" : "+v"(from_lane));  // the addresses are made again for every tile: kept, they would cost the products registers
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int piece = wave * PER + i, slot = piece * 64 + lane, row = slot / CH, c = slot % CH;
+            const int piece = wave * PER + i, slot = piece * 64 + from_lane, row = slot / CH, c = slot % CH;
 #pragma unroll
-            for (int value = 0; value < 2; ++value)
-#pragma unroll
-                for (int p = 0; p < PL; ++p) {
-                    const char *from = src.template at<DP>(value, p, tile, row, c ^ (value ? v_swizzle(row) : k_swizzle(row)));
-                    __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)from,
-                                                     (CFP32_LDS void *)(buf + (value * PL + p) * PLANE + piece * 64), 16, 0, 0);
-                }
+            for (int p = 0; p < PL; ++p) {
+                const char *from = src.template at<DP>(value, p, tile, row, c ^ (value ? v_swizzle(row) : k_swizzle(row)));
+                __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)from,
+                                                 (CFP32_LDS void *)(buf + p * PLANE + piece * 64), 16, 0, 0);
+            }
         }
     };
-    fetch(t0, buf0);
+    t1 += (t1 - t0) & 1;
+    fetch(0, t0, k0);
 
     // The row, at 2^e2, as the right operand of the scores.
     half8_t qh[KK], ql[KK];
-    float f = scale * kLog2e;
+    float f = fabsf(scale) * kLog2e;  // the sign goes into the row
     {
         float mx = 0.0f;
         int e2;
         {
             float x[KK][8];
+            if (q_wide) {
+#pragma unroll
+                for (int i = 0; i < KK; ++i) load_floats<8, true>(q, 16 * i + 8 * half, D, x[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KK; ++i) load_floats<8, false>(q, 16 * i + 8 * half, D, x[i]);
+            }
 #pragma unroll
             for (int i = 0; i < KK; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int d = 16 * i + 8 * half + e;
-                    x[i][e] = d < D ? q[d] : 0.0f;
                     const float ax = fabsf(x[i][e]);
                     mx = fmaxf(mx, ax < INFINITY ? ax : 0.0f);
                 }
@@ -163,7 +193,7 @@ __device__ __forceinline__ void attend_tiles(const float *q, int D, int limit, i
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     _Float16 h, w;
-                    split_scaled(x[i][e], e2, h, w);
+                    split_scaled(scale < 0.0f ? -x[i][e] : x[i][e], e2, h, w);
                     qh[i][e] = h, ql[i][e] = w;
                 }
         }
@@ -183,57 +213,66 @@ __device__ __forceinline__ void attend_tiles(const float *q, int D, int limit, i
     const int i16 = lane & 15, v_row = 4 * half + (i16 >> 2), v_chunk = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
     const int v_at = (v_row * CH + (v_chunk ^ v_swizzle(v_row))) * 16 + 8 * (i16 & 1);
 
-    auto multiply = [&](int tile, const uint4 *buf) {
-        const int j0 = tile * kTile;
-        if (j0 >= most) return;
+    floatx16_t s[2];
+    half8_t ph[4], pl[4];
+    // The next fragments are requested before the present ones are multiplied.
+    auto scores = [&](const uint4 *buf) {
         const char *lds = (const char *)buf;
-        floatx16_t s[2];
+        int at0 = k_at;
+        asm("" : "+v"(at0));  // as in fetch
+        half8_t k[2][2][PL];
+        auto read = [&](int i, half8_t (&x)[2][PL]) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int p = 0; p < PL; ++p)
+                    x[b][p] = *reinterpret_cast<const half8_t *>(lds + (at0 ^ (i * 32)) + (b * 32 * CH + p * PLANE) * 16);
+        };
+        read(0, k[0]);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < KK; ++i)
+        for (int i = 0; i < KK; ++i) {
+            if (i + 1 < KK) read(i + 1, k[(i + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            half8_t (&x)[2][PL] = k[i & 1];
+            if (PL == 2) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const char *at = lds + (k_at ^ (i * 32)) + b * 32 * CH * 16;
-                const half8_t kh = *reinterpret_cast<const half8_t *>(at);
-                if (PL == 2) {
-                    const half8_t kl = *reinterpret_cast<const half8_t *>(at + PLANE * 16);
-                    s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kl, qh[i], s[b], 0, 0, 0);
-                }
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, ql[i], s[b], 0, 0, 0);
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kh, qh[i], s[b], 0, 0, 0);
+                for (int b = 0; b < 2; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][PL - 1], qh[i], s[b], 0, 0, 0);
             }
-        const float ft = PL == 2 ? __builtin_amdgcn_ldexpf(f, -src.shift(0, tile)) : f;
-        float mx = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], ql[i], s[b], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], qh[i], s[b], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto weights = [&](int tile, int k_shift, int v_shift) {
+        const int j0 = tile * kTile;
+        float ft = PL == 2 ? __builtin_amdgcn_ldexpf(f, -k_shift) : f;
         if (__any(j0 + kTile > limit)) {
+            const int n = limit - j0 - 4 * half;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int j = j0 + 32 * b + 8 * (r / 4) + 4 * half + r % 4;
-                    s[b][r] = j < limit ? s[b][r] * ft : -INFINITY;
+                    const float x = s[b][r] * ft;
+                    s[b][r] = 32 * b + 8 * (r / 4) + r % 4 < n ? x : -INFINITY;
                 }
-        } else {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[b][r] *= ft;
+            ft = 1.0f;
         }
+        float mx = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][r]);
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, fmaxf(s[0][r], s[1][r]));
+        mx *= ft;  // ft >= 0
         mx = fmaxf(mx, __shfl_xor(mx, 32));
         int up = 0;  // this tile's values beside the sums' scale
-        bool lower = false;
         if (PL == 2) {
-            int ev = src.shift(1, tile);
-            if (ev == kNoValues) ev = cv;
-            lower = ev < cv;
-            up = lower ? 1 : min(ev - cv, 60);  // 2^(kTopWeight - 60): nothing in FP16
-            if (lower) {
+            const int ev = v_shift == kNoValues ? cv : v_shift;
+            up = ev < cv ? 1 : min(ev - cv, 60);  // 2^(kTopWeight - 60): nothing in FP16
+            if (ev < cv) {
                 // A step of room: values a little larger do not move the scale again.
                 const int next = ev - 1;
                 const float c = cv == kNoValues ? 1.0f : __builtin_amdgcn_ldexpf(1.0f, max(next - cv, -200));
@@ -250,54 +289,122 @@ __device__ __forceinline__ void attend_tiles(const float *q, int D, int limit, i
 #pragma unroll
             for (int b = 0; b < DB; ++b) o[b] *= c;
         }
-        const float base = (m == -INFINITY ? 0.0f : m) - (float)(kTopWeight - up);
-        float sum = 0.0f;
-        half8_t ph[4], pl[4];
+        const float base = (float)(kTopWeight - up) - (m == -INFINITY ? 0.0f : m);
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
+            uint32_t h[4], w[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float p = exp2_raw(s[t / 2][8 * (t % 2) + e] - base);
-                sum += p;
-                const _Float16 h = (_Float16)p;
-                ph[t][e] = h;
-                pl[t][e] = (_Float16)(p - (float)h);
+            for (int e = 0; e < 4; ++e) {
+                const float p0 = exp2_raw(fmaf(s[t / 2][8 * (t % 2) + 2 * e], ft, base));
+                const float p1 = exp2_raw(fmaf(s[t / 2][8 * (t % 2) + 2 * e + 1], ft, base));
+                sum[0] += p0;
+                sum[1] += p1;
+                split_pair(p0, p1, h[e], w[e]);
             }
-        l = PL == 2 ? fmaf(sum, __builtin_amdgcn_ldexpf(1.0f, up), l) : l + sum;
+            ph[t] = __builtin_bit_cast(half8_t, uint4_t{h[0], h[1], h[2], h[3]});
+            pl[t] = __builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]});
+            __builtin_amdgcn_sched_barrier(0);  // eight at a time: more would need registers the products hold
+        }
+        const float add = sum[0] + sum[1];
+        l = PL == 2 ? fmaf(add, __builtin_amdgcn_ldexpf(1.0f, up), l) : l + add;
+    };
+    auto values = [&](const uint4 *buf) {
+        const char *lds = (const char *)buf;
+        int at0 = v_at;
+        asm("" : "+v"(at0));
+        half8_t v[2][2][PL];  // two blocks of dims at a time
+        auto read = [&](int i, half8_t (&x)[2][PL]) {
+            const int t = i / (DB / 2), b0 = i % (DB / 2) * 2;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int b = 0; b < DB; ++b) {
-                half8_t v[PL];
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int p = 0; p < PL; ++p) {
-                    short4_t x[2];
+                    short4_t y[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
-                        x[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CFP32_LDS short4_t *)(
-                            (CFP32_LDS char *)lds + ((v_at ^ (b * 64) ^ (u * 32)) + ((PL + p) * PLANE + (16 * t + 8 * u) * CH) * 16)));
-                    v[p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                        y[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CFP32_LDS short4_t *)(
+                            (CFP32_LDS char *)lds + ((at0 ^ ((b0 + b) * 64) ^ (u * 32)) + (p * PLANE + (16 * t + 8 * u) * CH) * 16)));
+                    x[b][p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
                 }
-                if (PL == 2) o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[PL - 1], ph[t], o[b], 0, 0, 0);
-                o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0], pl[t], o[b], 0, 0, 0);
-                o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[0], ph[t], o[b], 0, 0, 0);
+        };
+        constexpr int N = 4 * (DB / 2);
+        read(0, v[0]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i + 1 < N) read(i + 1, v[(i + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            const int t = i / (DB / 2), b0 = i % (DB / 2) * 2;
+            half8_t (&x)[2][PL] = v[i & 1];
+            if (PL == 2) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) o[b0 + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][PL - 1], ph[t], o[b0 + b], 0, 0, 0);
             }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) o[b0 + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], pl[t], o[b0 + b], 0, 0, 0);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) o[b0 + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], ph[t], o[b0 + b], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
-    // A tile is multiplied when every wave's part of it has landed and no wave
-    // reads the other buffer any more; the next one is then on its way there.
-    auto landed = [] {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-        __syncthreads();
+    // Two groups of waves, one of each on every SIMD, half a tile apart: while
+    // one multiplies (values of the tile before, scores of this one), the
+    // other turns scores into weights on the vector units.  Phases end with a
+    // barrier; the first group multiplies in even ones, the second in odd ones.
+    // K(t) and V(t - 1) are read in phases 2 t and 2 t + 1, so their buffers
+    // are refilled from phase 2 t + 2 on, and must have landed when phase
+    // 2 t + 4 begins: every wave waits for its loads at the end of 2 t + 3.
+    auto sync = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
     };
-    for (int t = t0; t < t1; t += 2) {
-        landed();
-        if (t + 1 < t1) fetch(t + 1, buf1);
-        multiply(t, buf0);
-        if (t + 1 >= t1) break;
-        landed();
-        if (t + 2 < t1) fetch(t + 2, buf0);
-        multiply(t + 1, buf1);
-    }
+    auto drain = [] { __builtin_amdgcn_s_waitcnt(0x0F70); };  // vmcnt(0)
+    auto refill = [&](int t, uint4 *kb, uint4 *vb) {  // K(t), V(t - 1)
+        if (t < t1) fetch(0, t, kb);
+        if (t - 1 < t1) fetch(1, t - 1, vb);
+    };
+    // The groups run separate copies of the loop: which loads are on their way
+    // at which read is then plain to the compiler, which would wait otherwise.
+    // All waves go through all tiles (those of the block's last row): the
+    // barriers hold them that long anyway.
+    auto run = [&](auto group) {
+        constexpr bool second = decltype(group)::value;
+        int t = t0;
+        // Weights of tile t, its values, the next one's scores.
+        auto step = [&](uint4 *k_now, uint4 *k_next, uint4 *v_now, uint4 *v_next, auto may_end) {
+            constexpr bool more = !decltype(may_end)::value;  // known to be followed by another
+            if (second) refill(t + 2, k_now, v_next);
+            weights(t, src.shift(0, t), src.shift(1, t));
+            if (!second) {
+                drain();
+                sync();
+                refill(t + 2, k_now, v_next);
+            } else if (more || t + 1 < t1) {
+                sync();
+            }
+            values(v_now);
+            ++t;
+            if (more || t < t1) {
+                scores(k_next);
+                if (second) drain();
+                sync();
+            }
+        };
+        refill(t0 + 1, k1, v0);
+        if (second) sync();
+        scores(k0);
+        if (second) drain();
+        sync();
+        while (t < t1) {
+            step(k0, k1, v0, v1, std::false_type{});
+            step(k1, k0, v1, v0, std::true_type{});
+        }
+    };
+    drain();
+    sync();
+    if (wave >= NW / 2) run(std::true_type{});
+    else run(std::false_type{});
 #pragma unroll
     for (int b = 0; b < DB; ++b) to.o[b] = o[b];
     to.m = m;
@@ -324,8 +431,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
 {
     constexpr int PL = sizeof(T) == 4 ? 2 : 1;
     constexpr int kBlockRows = NW * kWaveRows;
-    __shared__ uint4 buf0[2 * PL * kTile * DP / 8];
-    __shared__ uint4 buf1[2 * PL * kTile * DP / 8];
+    __shared__ uint4 k0[PL * kTile * DP / 8], k1[PL * kTile * DP / 8], v0[PL * kTile * DP / 8], v1[PL * kTile * DP / 8];
     const int g = a.Hq / a.Hkv;
     const int kh = blockIdx.x % a.Hkv;
     const int64_t id = (gridDim.x - 1 - blockIdx.x) / a.Hkv;  // the rows that see most first
@@ -338,10 +444,10 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
     const int i = (int)(r / g), h = kh * g + (int)(r - (int64_t)i * g);
     const bool rows = first < n;
-    const int most = rows ? sq.limit((int)(min(first + kWaveRows, n) - 1) / g) : 0;
     const int keys = sq.limit((int)((min(r0 + kBlockRows, n) - 1) / g));
     const int limit = sq.limit(i);
     const float *q = (const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head;
+    const bool q_wide = rows_wide(a.q.data, a.q.tok | a.q.head, a.D);
     WaveRows<DP> w;
     const int tiles = (keys + kTile - 1) / kTile;
     if (tiles == 0) {
@@ -352,13 +458,13 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
             for (int e = 0; e < 16; ++e) w.o[b][e] = 0.0f;
     } else if constexpr (PL == 2) {
         const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
-        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot};
-        attend_tiles<DP, PL, NW>(q, a.D, limit, most, a.scale, 0, tiles, src, buf0, buf1, w);
+        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot, tiles - 1};
+        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, 0, tiles, src, k0, k1, v0, v1, w);
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                                   (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                                   a.k.tok * 2, a.v.tok * 2, sq.nk - 1, a.D / 8};
-        attend_tiles<DP, PL, NW>(q, a.D, limit, most, a.scale, 0, tiles, src, buf0, buf1, w);
+        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, 0, tiles, src, k0, k1, v0, v1, w);
     }
     if (!rows) return;
     const bool live = first + (lane & 31) < n;
@@ -493,10 +599,10 @@ hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t 
         prompt_tile_kernel<T, DP, NW><<<(unsigned)units, 64 * NW, 0, stream>>>(a, planes);                         \
     } while (0)
     if (a.kv_f16) {
-        if (a.D <= 64) CFP32_PROMPT(_Float16, 64, 4);
-        else CFP32_PROMPT(_Float16, 128, 4);
+        if (a.D <= 64) CFP32_PROMPT(_Float16, 64, 8);
+        else CFP32_PROMPT(_Float16, 128, 8);
     } else {
-        if (a.D <= 64) CFP32_PROMPT(float, 64, 4);
+        if (a.D <= 64) CFP32_PROMPT(float, 64, 8);
         else CFP32_PROMPT(float, 128, 8);
     }
 #undef CFP32_PROMPT
