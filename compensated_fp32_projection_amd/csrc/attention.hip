@@ -544,7 +544,7 @@ hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStre
     if (a.Hkv > 65535 || units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     const bool w = wide(a.k.data, a.k.tok | a.k.head, a.D, a.kv_f16) && wide(a.v.data, a.v.tok | a.v.head, a.D, a.kv_f16);
     static const int force = getenv("CF_FORCE") ? atoi(getenv("CF_FORCE")) : 0;
-    if (a.Tk > 0 && (w || !a.kv_f16) && (force == 2 || (force == 0 && a.Tq >= 1024))) return launch_prompt_tile(a, workspace, stream);
+    if (a.Tk > 0 && (!a.kv_f16 || (w && a.k.tok < ((int64_t)1 << 31) && a.v.tok < ((int64_t)1 << 31))) && (force == 2 || (force == 0 && a.Tq >= 1024))) return launch_prompt_tile(a, workspace, stream);
     const dim3 grid((unsigned)units, (unsigned)a.Hkv);
     CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, w, grid, 64 * kWaves, a);
     return hipGetLastError();

@@ -23,6 +23,7 @@
 //     64 bytes) so that four rows do.
 //   * The running maximum is followed lazily (kLazy), so that most tiles do
 //     not touch the output sums.
+#include <stdlib.h>
 #include <type_traits>
 
 #include "attention_device.h"
@@ -59,15 +60,16 @@ __host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2
 
 // ---- Where a tile's rows are ------------------------------------------------------
 
+// Rows row0 + lr of a tile (row0 the same for the wave), 16-byte chunk `chunk`.
 struct PlaneSource {
     const char *tiles;      // of this head and sequence
     const int32_t *shifts;
     int last;               // a tile beyond the last repeats it: no row sees it
     template <int DP>
-    __device__ __forceinline__ const char *at(int value, int plane, int tile, int row, int chunk) const
+    __device__ __forceinline__ const char *at(int value, int plane, int tile, int row0, int lr, int chunk) const
     {
-        const char *plane_at = tiles + (int64_t)min(tile, last) * tile_bytes<DP>(2) + (value * 2 + plane) * (kTile * DP * 2);
-        return plane_at + (uint32_t)(row * (DP * 2) + chunk * 16);
+        const char *from = tiles + (int64_t)min(tile, last) * tile_bytes<DP>(2) + (value * 2 + plane) * (kTile * DP * 2);
+        return from + row0 * (DP * 2) + (uint32_t)(lr * (DP * 2) + chunk * 16);
     }
     // A scalar load: a vector load would be waited for behind the tiles on their way.
     __device__ __forceinline__ int shift(int value, int tile) const
@@ -78,30 +80,14 @@ struct PlaneSource {
 
 struct PackedSource {
     const char *k, *v;      // key 0
-    int64_t k_tok, v_tok;   // bytes
+    int64_t k_tok, v_tok;   // bytes, below 2^32
     int last, chunks;       // a key or chunk beyond the last repeats one: it meets a weight or an element of 0
     template <int DP>
-    __device__ __forceinline__ const char *at(int value, int, int tile, int row, int chunk) const
+    __device__ __forceinline__ const char *at(int value, int, int tile, int row0, int lr, int chunk) const
     {
-        const int64_t j = min(tile * kTile + row, last);
-        return (value ? v + j * v_tok : k + j * k_tok) + (chunk < chunks ? chunk : 0) * 16;
-    }
-    __device__ __forceinline__ int shift(int, int) const { return 0; }
-};
-
-constexpr int kPageIds = 2048;  // page ids of one block
-
-struct PagedSource {
-    const char *k, *v;      // the head in page 0
-    int64_t k_page, v_page, k_tok, v_tok;
-    const int *ids;         // LDS: pages from the one of key `first` on
-    int first, last, chunks, lg;
-    template <int DP>
-    __device__ __forceinline__ const char *at(int value, int, int tile, int row, int chunk) const
-    {
-        const int j = min(tile * kTile + row, last);
-        const int64_t p = ids[(j >> lg) - (first >> lg)], o = j & ((1 << lg) - 1);
-        return (value ? v + p * v_page + o * v_tok : k + p * k_page + o * k_tok) + (chunk < chunks ? chunk : 0) * 16;
+        const uint32_t j = (uint32_t)min(tile * kTile + row0 + lr, last);
+        const char *base = (value ? v : k) + (uint64_t)j * (uint32_t)(value ? v_tok : k_tok);
+        return base + (chunk < chunks ? chunk : 0) * 16;
     }
     __device__ __forceinline__ int shift(int, int) const { return 0; }
 };
@@ -138,8 +124,10 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
     constexpr int CH = DP / 8;         // 16-byte chunks of a row
     constexpr int PLANE = kTile * CH;  // of a plane
     constexpr int KK = DP / 16, DB = DP / 32;
-    constexpr int PER = CH / NW;       // loads (64 chunks) of a wave and plane
-    static_assert(CH % NW == 0, "loads are dealt evenly");
+    constexpr int PER = CH / 4;        // loads of a loading wave and plane
+    constexpr int LOADS = PL * PER;     // and of K or V of a tile
+    static_assert(PER * (64 / CH) == 16, "a wave's rows begin where the swizzles do");
+    static_assert(NW == 4 || NW == 8, "one or two groups of four waves");
     const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -147,22 +135,22 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
     auto k_swizzle = [](int row) { return CH == 16 ? row & 15 : (row >> 1) & 7; };
     auto v_swizzle = [](int row) { return CH == 16 ? (row & 3) << 2 | ((row >> 2) & 3) : (row & 2) << 1 | ((row >> 2) & 3); };
 
-    auto fetch = [&](int value, int tile, uint4 *buf) {
+    // Loads are 64 chunks each, PER of each of the first four waves to a plane:
+    // load n of a tile's K or V.
+    auto fetch = [&](int value, int tile, uint4 *buf, int n) {
+        const int i = n % PER, p = n / PER, piece = wave * PER + i, row0 = piece * (64 / CH);
         int from_lane = lane;
-        asm("" : "+v"(from_lane));  // the addresses are made again for every tile: kept, they would cost the products registers
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int piece = wave * PER + i, slot = piece * 64 + from_lane, row = slot / CH, c = slot % CH;
-#pragma unroll
-            for (int p = 0; p < PL; ++p) {
-                const char *from = src.template at<DP>(value, p, tile, row, c ^ (value ? v_swizzle(row) : k_swizzle(row)));
-                __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)from,
-                                                 (CFP32_LDS void *)(buf + p * PLANE + piece * 64), 16, 0, 0);
-            }
-        }
+        asm("" : "+v"(from_lane));  // the addresses are made again each time: kept, they would cost the products registers
+        const int lr = from_lane / CH;
+        const int c = (from_lane % CH) ^ (value ? v_swizzle(lr) ^ v_swizzle(i * (64 / CH)) : k_swizzle(lr) ^ k_swizzle(i * (64 / CH)));
+        __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)src.template at<DP>(value, p, tile, row0, lr, c),
+                                         (CFP32_LDS void *)(buf + p * PLANE + piece * 64), 16, 0, 0);
     };
     t1 += (t1 - t0) & 1;
-    fetch(0, t0, k0);
+    if (wave < 4) {
+#pragma unroll
+        for (int n = 0; n < LOADS; ++n) fetch(0, t0, k0, n);
+    }
 
     // The row, at 2^e2, as the right operand of the scores.
     half8_t qh[KK], ql[KK];
@@ -215,40 +203,6 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
 
     floatx16_t s[2];
     half8_t ph[4], pl[4];
-    // The next fragments are requested before the present ones are multiplied.
-    auto scores = [&](const uint4 *buf) {
-        const char *lds = (const char *)buf;
-        int at0 = k_at;
-        asm("" : "+v"(at0));  // as in fetch
-        half8_t k[2][2][PL];
-        auto read = [&](int i, half8_t (&x)[2][PL]) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int p = 0; p < PL; ++p)
-                    x[b][p] = *reinterpret_cast<const half8_t *>(lds + (at0 ^ (i * 32)) + (b * 32 * CH + p * PLANE) * 16);
-        };
-        read(0, k[0]);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < KK; ++i) {
-            if (i + 1 < KK) read(i + 1, k[(i + 1) & 1]);
-            __builtin_amdgcn_sched_barrier(0);
-            half8_t (&x)[2][PL] = k[i & 1];
-            if (PL == 2) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][PL - 1], qh[i], s[b], 0, 0, 0);
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], ql[i], s[b], 0, 0, 0);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) s[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], qh[i], s[b], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    };
     auto weights = [&](int tile, int k_shift, int v_shift) {
         const int j0 = tile * kTile;
         float ft = PL == 2 ? __builtin_amdgcn_ldexpf(f, -k_shift) : f;
@@ -309,61 +263,80 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
         const float add = sum[0] + sum[1];
         l = PL == 2 ? fmaf(add, __builtin_amdgcn_ldexpf(1.0f, up), l) : l + add;
     };
-    auto values = [&](const uint4 *buf) {
-        const char *lds = (const char *)buf;
-        int at0 = v_at;
-        asm("" : "+v"(at0));
-        half8_t v[2][2][PL];  // two blocks of dims at a time
-        auto read = [&](int i, half8_t (&x)[2][PL]) {
-            const int t = i / (DB / 2), b0 = i % (DB / 2) * 2;
+    // The products of a phase: V of one tile with its weights (VALUES), K of
+    // the next with the row (SCORES).  Fragments (4 registers) go through a
+    // ring of R, each requested R - 2 ahead of its use; in between,
+    // also(n) is called for n = 0, 1, ... 2 LOADS - 1 (the next loads).
+    constexpr int R = 7;
+    constexpr int NV = 4 * DB * PL, NK = 2 * KK * PL;
+    auto products = [&](const uint4 *vb, const uint4 *kb, auto with_values, auto with_scores, auto also) {
+        constexpr bool VALUES = decltype(with_values)::value, SCORES = decltype(with_scores)::value;
+        constexpr int from = VALUES ? 0 : NV, to = SCORES ? NV + NK : NV;
+        constexpr int every = (to - from) / (2 * LOADS);
+        half8_t ring[R];
+        int v_lane = v_at, k_lane = k_at;
+        asm("" : "+v"(v_lane), "+v"(k_lane));  // addresses are made where they are used: kept, they would cost registers
+        // Fragments in pairs of accumulators b, b + 1: the low parts, then the high ones.
+        auto part = [](int k) { return PL - 1 - k / 2 % PL; };
+        auto read = [&](int n) -> half8_t {
+            if (n < NV) {  // keys 16 t, dims 32 b
+                const int p = part(n), b = n / (2 * PL) * 2 % DB + n % 2, t = n / PL / DB;
+                short4_t y[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    y[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CFP32_LDS short4_t *)(
+                        (CFP32_LDS char *)vb + ((v_lane ^ (b * 64) ^ (u * 32)) + (p * PLANE + (16 * t + 8 * u) * CH) * 16)));
+                return __builtin_bit_cast(half8_t, __builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
+            }
+            const int k = n - NV, p = part(k), b = k % 2, i = k / PL / 2;  // dims 16 i, keys 32 b
+            return *reinterpret_cast<const half8_t *>((const char *)kb + ((k_lane ^ (i * 32)) + (b * 32 * CH + p * PLANE) * 16));
+        };
+#pragma unroll
+        for (int n = from; n < from + R - 2; ++n) ring[n % R] = read(n);
+        if (SCORES)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int p = 0; p < PL; ++p) {
-                    short4_t y[2];
+                for (int r = 0; r < 16; ++r) s[b][r] = 0.0f;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        y[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CFP32_LDS short4_t *)(
-                            (CFP32_LDS char *)lds + ((at0 ^ ((b0 + b) * 64) ^ (u * 32)) + (p * PLANE + (16 * t + 8 * u) * CH) * 16)));
-                    x[b][p] = __builtin_bit_cast(half8_t, __builtin_shufflevector(y[0], y[1], 0, 1, 2, 3, 4, 5, 6, 7));
-                }
-        };
-        constexpr int N = 4 * (DB / 2);
-        read(0, v[0]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (i + 1 < N) read(i + 1, v[(i + 1) & 1]);
+        for (int n = from; n < to; ++n) {
+            if (n + R - 2 < to) ring[(n + R - 2) % R] = read(n + R - 2);
+            if ((n - from) % every == 0 && (n - from) / every < 2 * LOADS) also((n - from) / every);
             __builtin_amdgcn_sched_barrier(0);
-            const int t = i / (DB / 2), b0 = i % (DB / 2) * 2;
-            half8_t (&x)[2][PL] = v[i & 1];
-            if (PL == 2) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b) o[b0 + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][PL - 1], ph[t], o[b0 + b], 0, 0, 0);
+            // Neighbouring products go to different accumulators: the high
+            // fragments meet the low weights one by one, and the high ones together.
+            const bool value = n < NV;
+            const int k = value ? n : n - NV, p = part(k), t = k / PL / DB, i = k / PL / 2;
+            const int b = value ? k / (2 * PL) * 2 % DB + k % 2 : k % 2;
+            auto multiply = [&](const half8_t &x, int to_b, bool low) {
+                if (value) o[to_b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, low ? pl[t] : ph[t], o[to_b], 0, 0, 0);
+                else s[to_b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, low ? ql[i] : qh[i], s[to_b], 0, 0, 0);
+            };
+            multiply(ring[n % R], b, p == 0);
+            if (p == 0 && k % 2) {
+                multiply(ring[(n - 1) % R], b - 1, false);
+                multiply(ring[n % R], b, false);
             }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) o[b0 + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], pl[t], o[b0 + b], 0, 0, 0);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) o[b0 + b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[b][0], ph[t], o[b0 + b], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // Two groups of waves, one of each on every SIMD, half a tile apart: while
-    // one multiplies (values of the tile before, scores of this one), the
+    // With eight waves: two groups, one of each on every SIMD, half a tile
+    // apart: while one multiplies (values of the tile before, scores of this one), the
     // other turns scores into weights on the vector units.  Phases end with a
     // barrier; the first group multiplies in even ones, the second in odd ones.
     // K(t) and V(t - 1) are read in phases 2 t and 2 t + 1, so their buffers
-    // are refilled from phase 2 t + 2 on, and must have landed when phase
-    // 2 t + 4 begins: every wave waits for its loads at the end of 2 t + 3.
+    // can be filled from phase 2 t + 2 on, and must be full when phase 2 t + 4
+    // begins.  The first group does that: it asks for the loads between its
+    // products in phase 2 t + 2 and waits for them at the end of 2 t + 3.
+    // With four waves there is one group, and a barrier before its products.
     auto sync = [] {
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
     auto drain = [] { __builtin_amdgcn_s_waitcnt(0x0F70); };  // vmcnt(0)
-    auto refill = [&](int t, uint4 *kb, uint4 *vb) {  // K(t), V(t - 1)
-        if (t < t1) fetch(0, t, kb);
-        if (t - 1 < t1) fetch(1, t - 1, vb);
-    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
     // The groups run separate copies of the loop: which loads are on their way
     // at which read is then plain to the compiler, which would wait otherwise.
     // All waves go through all tiles (those of the block's last row): the
@@ -371,40 +344,40 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
     auto run = [&](auto group) {
         constexpr bool second = decltype(group)::value;
         int t = t0;
-        // Weights of tile t, its values, the next one's scores.
-        auto step = [&](uint4 *k_now, uint4 *k_next, uint4 *v_now, uint4 *v_next, auto may_end) {
-            constexpr bool more = !decltype(may_end)::value;  // known to be followed by another
-            if (second) refill(t + 2, k_now, v_next);
-            weights(t, src.shift(0, t), src.shift(1, t));
-            if (!second) {
-                drain();
-                sync();
-                refill(t + 2, k_now, v_next);
-            } else if (more || t + 1 < t1) {
-                sync();
-            }
-            values(v_now);
-            ++t;
-            if (more || t < t1) {
-                scores(k_next);
-                if (second) drain();
-                sync();
-            }
+        // K(u), V(u - 1); beyond the last tile, where no one reads them, the last again.
+        auto refill = [&](int u, uint4 *kb, uint4 *vb) {
+            return [=, &fetch](int n) {
+                if (!second) fetch(n >= LOADS, n >= LOADS ? u - 1 : u, n >= LOADS ? vb : kb, n % LOADS);
+            };
         };
-        refill(t0 + 1, k1, v0);
+        // Weights of tile t, its values, the next one's scores (unless it is the last).
+        auto step = [&](uint4 *k_now, uint4 *k_next, uint4 *v_now, uint4 *v_next, auto last) {
+            constexpr bool more = !decltype(last)::value;
+            weights(t, src.shift(0, t), src.shift(1, t));
+            if (!second) drain();
+            if (!second || more) sync();
+            if constexpr (more) {
+                products(v_now, k_next, yes, yes, refill(t + 2, k_now, v_next));
+                if (NW == 8) sync();
+            } else {
+                products(v_now, k_next, yes, no, [](int) {});
+            }
+            ++t;
+        };
         if (second) sync();
-        scores(k0);
-        if (second) drain();
-        sync();
-        while (t < t1) {
-            step(k0, k1, v0, v1, std::false_type{});
-            step(k1, k0, v1, v0, std::true_type{});
+        products(v0, k0, no, yes, refill(t0 + 1, k1, v0));
+        if (NW == 8) sync();
+        while (t + 2 < t1) {
+            step(k0, k1, v0, v1, no);
+            step(k1, k0, v1, v0, no);
         }
+        step(k0, k1, v0, v1, no);
+        step(k1, k0, v1, v0, yes);
     };
     drain();
     sync();
-    if (wave >= NW / 2) run(std::true_type{});
-    else run(std::false_type{});
+    if (NW == 8 && wave >= 4) run(yes);
+    else run(no);
 #pragma unroll
     for (int b = 0; b < DB; ++b) to.o[b] = o[b];
     to.m = m;
@@ -598,12 +571,13 @@ hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t 
         if (units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;                                               \
         prompt_tile_kernel<T, DP, NW><<<(unsigned)units, 64 * NW, 0, stream>>>(a, planes);                         \
     } while (0)
+    static const int nw = getenv("CF_NW") ? atoi(getenv("CF_NW")) : 8;
     if (a.kv_f16) {
-        if (a.D <= 64) CFP32_PROMPT(_Float16, 64, 8);
-        else CFP32_PROMPT(_Float16, 128, 8);
+        if (a.D <= 64) { if (nw == 4) CFP32_PROMPT(_Float16, 64, 4); else CFP32_PROMPT(_Float16, 64, 8); }
+        else { if (nw == 4) CFP32_PROMPT(_Float16, 128, 4); else CFP32_PROMPT(_Float16, 128, 8); }
     } else {
-        if (a.D <= 64) CFP32_PROMPT(float, 64, 8);
-        else CFP32_PROMPT(float, 128, 8);
+        if (a.D <= 64) { if (nw == 4) CFP32_PROMPT(float, 64, 4); else CFP32_PROMPT(float, 64, 8); }
+        else { if (nw == 4) CFP32_PROMPT(float, 128, 4); else CFP32_PROMPT(float, 128, 8); }
     }
 #undef CFP32_PROMPT
     return hipGetLastError();
