@@ -539,6 +539,44 @@ def qkv_rotary(qkv, H: int, D: int, positions=None, theta: float = 10000.0, stre
 
 # -- attention and the paged cache ----------------------------------------------
 
+_helpers = None
+
+
+def _native():
+    """The helpers' native form (csrc/helpers.cpp), bound to the loaded library."""
+    global _helpers
+    if _helpers is None:
+        torch = _torch()
+        path = os.path.join(_HERE, "_helpers.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m compensated_fp32_projection_amd.build`")
+        import importlib.util
+        spec = importlib.util.spec_from_file_location(__name__ + "._helpers", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        lib = load_library()
+        names = ("cfp32_attention_prompt_workspace_bytes", "cfp32_attention_prompt",
+                 "cfp32_attention_decode_workspace_bytes", "cfp32_attention_decode", "cfp32_cache_reserve",
+                 "cfp32_cache_append", "cfp32_cache_fork_workspace_bytes", "cfp32_cache_fork", "cfp32_cache_free",
+                 "cfp32_cache_compact_workspace_bytes", "cfp32_cache_compact")
+        mod.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                 torch._C._cuda_getCurrentRawStream, _scratch_address)
+        _helpers = mod
+    return _helpers
+
+
+def _scratch_address(need, index, raw):
+    """Address of the helpers' own workspace for the current stream `raw` of device `index`."""
+    ws = _default_ws.get((index, raw))
+    if ws is None or ws.buf is None or ws.buf.numel() < need:
+        torch = _torch()
+        device = torch.device("cuda", index)
+        return _default_workspace(device, torch.cuda.current_stream(device)).get(
+            need, device, torch.cuda.current_stream(device)).data_ptr()
+    return ws.buf.data_ptr()
+
+
 def _heads(t, dtypes, name, device):
     """(pointer, token stride, head stride) of a [tokens, heads, D] tensor with unit stride along D."""
     torch = _torch()
@@ -621,6 +659,10 @@ def attention_prompt(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float
     the sequences (cu_k defaults to cu_q).  Causal rows are aligned to the
     end of their sequence's keys.  scale defaults to 1 / sqrt(D).  Returns
     FP32 [Tq, Hq, D]; rows outside all sequences are not written."""
+    if stream is None and workspace is None:
+        done = _native().attention_prompt(q, k, v, cu_q, cu_k, causal, scale, out)
+        if done is not None:
+            return done
     torch = _torch()
     pq = _heads(q, (torch.float32,), "q", q.device)
     dev = q.device
@@ -654,6 +696,10 @@ def attention_decode(q, k_pages, v_pages, table, lens, shared_pages: int = 0, sc
     [B, Hq, D]; pools [P, Hkv, page, D]; table int32 [B, W]; lens int32 [B].
     The first ``shared_pages`` table entries are the same in every row and
     are read once for the batch.  Returns FP32 [B, Hq, D]."""
+    if stream is None and workspace is None:
+        done = _native().attention_decode(q, k_pages, v_pages, table, lens, shared_pages, scale, out)
+        if done is not None:
+            return done
     torch = _torch()
     dev = q.device
     pq = _heads(q, (torch.float32,), "q", dev)
@@ -681,6 +727,10 @@ def cache_reserve(table, lens, refs, cu, page: int, missing=None, table_out=None
     """(table, refs) with the lowest free pages in the entries that the new
     tokens need: sequence s holds lens[s] tokens and gets cu[s+1] - cu[s]
     more.  ``missing`` (int32 [1]) receives how many pages could not be given."""
+    if stream is None and missing is None and table_out is None and refs_out is None:
+        done = _native().cache_reserve(table, lens, refs, cu, page)
+        if done is not None:
+            return done
     torch = _torch()
     dev = table.device
     pt, pl, pr, pc = (_ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1), _ints(refs, "refs", dev, 1),
@@ -703,6 +753,10 @@ def cache_append(k, v, cu, k_pages, v_pages, table, lens, lens_out=None, stream=
     """Writes new tokens, k and v FP32 [T, Hkv, D], into the pools (rounded to
     their type): rows cu[s] .. cu[s+1] - 1 become tokens lens[s], ... of
     sequence s.  Returns the new lengths."""
+    if stream is None and lens_out is None:
+        done = _native().cache_append(k, v, cu, k_pages, v_pages, table, lens)
+        if done is not None:
+            return done
     torch = _torch()
     at, kv, (P, Hkv, page, D) = _pools(k_pages, v_pages)
     dev = k_pages.device
@@ -739,6 +793,10 @@ def cache_fork(k_pages, v_pages, table, lens, refs, parents, missing=None, refs_
     whole pages of sequence parents[c] and gets a copy of its partly filled
     last page.  ``missing`` (int32 [1]) receives how many last pages the pool
     had no page for."""
+    if stream is None and workspace is None and missing is None and refs_out is None:
+        done = _native().cache_fork(k_pages, v_pages, table, lens, refs, parents)
+        if done is not None:
+            return done
     torch = _torch()
     at, kv, (P, Hkv, page, D) = _pools(k_pages, v_pages)
     dev = k_pages.device
@@ -763,6 +821,10 @@ def cache_fork(k_pages, v_pages, table, lens, refs, parents, missing=None, refs_
 
 def cache_free(rows, refs, refs_out=None, stream=None):
     """refs with the pages named in rows [R, W] (tables of ended sequences) given up."""
+    if stream is None and refs_out is None:
+        done = _native().cache_free(rows, refs)
+        if done is not None:
+            return done
     torch = _torch()
     dev = refs.device
     pw, pr = _ints(rows, "rows", dev, 2), _ints(refs, "refs", dev, 1)
@@ -779,6 +841,10 @@ def cache_compact(k_pages, v_pages, table, refs, table_out=None, refs_out=None, 
                   stream=None):
     """(table, refs, n) of the pool made dense: its n live pages are moved to
     pages 0 .. n - 1, and the table names them there.  n is an int32 [1] tensor."""
+    if stream is None and workspace is None and table_out is None and refs_out is None:
+        done = _native().cache_compact(k_pages, v_pages, table, refs)
+        if done is not None:
+            return done
     torch = _torch()
     at, kv, (P, Hkv, page, D) = _pools(k_pages, v_pages)
     dev = k_pages.device

@@ -1,4 +1,5 @@
-"""Build libcfp32.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libcfp32.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+the native tensor helpers (_helpers.so, host code) with g++.
 
     python -m compensated_fp32_projection_amd.build [--verbose] [--resource-usage]
 
@@ -27,6 +28,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libcfp32.so")
+HELPERS = os.path.join(HERE, "_helpers.so")
 # Written next to the library on every build: the git revision (and whether
 # the tree had uncommitted changes), a hash of the sources and of the
 # library, so a measurement can name the build it ran even where the source
@@ -101,8 +103,32 @@ def write_build_info() -> dict:
     return info
 
 
+def build_helpers(verbose: bool = False) -> str:
+    """Compile the native form of the tensor helpers (csrc/helpers.cpp, host
+    code only) against the installed torch; returns the module's path."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    tmp = HELPERS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           os.path.join(CSRC, "helpers.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stderr}")
+    if res.stderr.strip() and verbose:
+        print(res.stderr, file=sys.stderr)
+    os.replace(tmp, HELPERS)
+    return HELPERS
+
+
 def build(verbose: bool = False, resource_usage: bool = False) -> str:
-    """Compile every HIP source into libcfp32.so; returns the library path."""
+    """Compile every HIP source into libcfp32.so, and the native helpers; returns the library path."""
     tmp = LIB + ".tmp"
     cmd = [hipcc(), *FLAGS, *sources(), "-o", tmp]
     if resource_usage:
@@ -118,6 +144,7 @@ def build(verbose: bool = False, resource_usage: bool = False) -> str:
     if err.strip() and (verbose or resource_usage):
         print(err, file=sys.stderr)
     os.replace(tmp, LIB)
+    build_helpers(verbose)
     write_build_info()
     return LIB
 
