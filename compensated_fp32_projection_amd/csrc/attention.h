@@ -48,9 +48,29 @@ struct DecodeArgs {
 
 size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
 hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream);
-// Its form for many rows (attention_tile.hip); FP16 K and V have to allow 16-byte loads.
+
+// What several blocks contribute to one row: unnormalised sums, their maxima
+// (in powers of two) and weights.  Part i of row r is entry r * slots + i.
+// Null o: one part, which goes straight to the output.
+struct Partials {
+    float *o;   // [rows * slots, dim]
+    float *m, *l;
+    int slots, dim;
+};
+size_t partial_bytes(int64_t rows, int slots, int dim);
+void place_partials(Partials &to, int64_t rows, void *at);
+hipError_t launch_join(const PromptArgs &a, const Partials &from, hipStream_t stream);
+hipError_t launch_join(const DecodeArgs &a, const Partials &from, hipStream_t stream);
+
+// The form for many rows (attention_tile.hip); FP16 K and V have to allow
+// 16-byte loads, and a token's stride to be below 2^32 bytes.
 size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
 hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream);
+
+// The shared keys of a decode with FP16 pages that allow 16-byte loads, in
+// `parts` parts: slots [0, parts).
+int decode_tile_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t keys, int page_log2);
+hipError_t launch_decode_tile(const DecodeArgs &a, const Partials &to, int parts, hipStream_t stream);
 
 size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int page_log2,
                                   int64_t shared_pages, bool kv_f16);

@@ -19,7 +19,6 @@
 // These products are bounded by memory, not by the matrix units: 16 rows
 // against FP32 keys need 1024 cycles of a SIMD for 8 KiB at D = 64, which is
 // 19 TB/s over the chip.
-#include <stdlib.h>
 #include "attention_device.h"
 
 namespace cfp32 {
@@ -287,13 +286,55 @@ __device__ __forceinline__ void join_rows(const Joined &from, float &m, float &l
     }
 }
 
+// A row's sums, of what this block has seen: into its slot, or (all there is)
+// as its result.  Results that are not finite are marked.
+template <int DP>
+__device__ __forceinline__ void leave_row(Joined &sh, const Partials &to, int64_t slot, float *out, int D, bool live)
+{
+    float m, l, x[DP / 16];
+    join_rows<DP>(sh, m, l, x);
+    if (!live) return;
+    const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (DP / 16);
+    if (to.o) {
+        if ((threadIdx.x & 15) == 0) {
+            to.m[slot] = m;
+            to.l[slot] = l;
+        }
+        if (l != 0.0f)
+#pragma unroll
+            for (int e = 0; e < DP / 16; e += 4)
+                *reinterpret_cast<floatx4_t *>(to.o + slot * DP + d0 + e) = floatx4_t{x[e], x[e + 1], x[e + 2], x[e + 3]};
+        return;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < DP / 16; ++e) {
+        const float y = x[e] * inv;
+        if (d0 + e < D) {
+            out[d0 + e] = y;
+            if (!(fabsf(y) < INFINITY)) sh.unfinished[row] = 1;
+        }
+    }
+}
+
+// Keys [lo, hi) in `parts` of equal lengths (in whole units).
+__device__ __forceinline__ void part_range(int lo, int hi, int part, int parts, int unit, int &a, int &b)
+{
+    const int n = max(hi - lo, 0), u = (n + unit - 1) / unit, per = (u + parts - 1) / parts;
+    a = lo + (int)min((int64_t)n, (int64_t)part * per * unit);
+    b = lo + (int)min((int64_t)n, (int64_t)(part + 1) * per * unit);
+}
+
 template <class T, int DP, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs a)
+__global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs a, Partials to)
 {
     __shared__ Joined sh;
-    const int g = a.Hq / a.Hkv, kh = blockIdx.y;
+    constexpr int kUnit = 16 * (DP == 128 ? 2 : 4);
+    // The rows that see most first.  Heads vary fastest: blocks go round the
+    // eight XCDs, so a head's keys are read by few of them.
+    const int g = a.Hq / a.Hkv, kh = blockIdx.x % a.Hkv, part = blockIdx.y;
     int64_t start;
-    const int64_t id = gridDim.x - 1 - blockIdx.x;  // the rows that see most first
+    const int64_t id = (gridDim.x - 1 - blockIdx.x) / a.Hkv;
     const int sid = find_unit(a.cu_q, a.S, g, kRows, id, start);
     const Sequence sq = sequence(a, sid);
     const int64_t n = (int64_t)sq.nq * g;
@@ -305,33 +346,21 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs 
     const PackedKeys keys = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                              (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                              a.k.tok * (int64_t)sizeof(T), a.v.tok * (int64_t)sizeof(T)};
-    const int hi = sq.limit((int)((r0 + live - 1) / g));
+    int lo, hi;
+    part_range(0, sq.limit((int)((r0 + live - 1) / g)), part, to.slots, kUnit, lo, hi);
     attend_rows<T, DP, WIDE>((const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head,
-                             rows_wide(a.q.data, a.q.tok | a.q.head, a.D), a.D, sq.limit(i), a.scale, 0,
-                             hi, keys, sh);
+                             rows_wide(a.q.data, a.q.tok | a.q.head, a.D), a.D, sq.limit(i), a.scale, lo, hi, keys, sh);
     if (threadIdx.x < kRows) sh.unfinished[threadIdx.x] = 0;
     __syncthreads();
-    float m, l, x[DP / 16];
-    join_rows<DP>(sh, m, l, x);
-    const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (DP / 16);
-    if (row < live) {
-        const int ri = (int)((r0 + row) / g), rh = kh * g + (int)(r0 + row - (int64_t)ri * g);
-        float *out = a.out + (sq.q0 + ri) * a.out_tok + rh * a.out_head;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int c = 0; c < DP / 16; ++c) {
-            const float y = x[c] * inv;
-            if (d0 + c < a.D) {
-                out[d0 + c] = y;
-                if (!(fabsf(y) < INFINITY)) sh.unfinished[row] = 1;
-            }
-        }
-    }
+    const int row = threadIdx.x >> 4, ri = (int)((r0 + row) / g), rh = kh * g + (int)(r0 + row - (int64_t)ri * g);
+    leave_row<DP>(sh, to, ((int64_t)(sq.q0 + ri) * a.Hq + rh) * to.slots + part,
+                  a.out + (sq.q0 + ri) * a.out_tok + rh * a.out_head, a.D, row < live);
+    if (to.o) return;
     __syncthreads();
     for (int w = threadIdx.x >> 6; w < live; w += kWaves)
         if (sh.unfinished[w]) {
-            const int ri = (int)((r0 + w) / g);
-            attend_prompt_row<T>(a, sq, ri, kh * g + (int)(r0 + w - (int64_t)ri * g));
+            const int wi = (int)((r0 + w) / g);
+            attend_prompt_row<T>(a, sq, wi, kh * g + (int)(r0 + w - (int64_t)wi * g));
         }
 }
 
@@ -341,15 +370,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs 
 // shared keys, 16 of a sequence's heads for its own.
 struct DecodeParts {
     int shared, own, shared_groups, own_groups;
+    int own_from;  // the first key that is not shared
     Partials to;  // slots: shared + own; null o: straight to the output
 };
-
-__device__ __forceinline__ void part_range(int lo, int hi, int part, int parts, int unit, int &a, int &b)
-{
-    const int n = max(hi - lo, 0), u = (n + unit - 1) / unit, per = (u + parts - 1) / parts;
-    a = lo + (int)min((int64_t)n, (int64_t)part * per * unit);
-    b = lo + (int)min((int64_t)n, (int64_t)(part + 1) * per * unit);
-}
 
 template <class T, int DP, bool WIDE>
 __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs a, DecodeParts c)
@@ -357,7 +380,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs 
     __shared__ Joined sh;
     constexpr int kUnit = kWaves * (DP == 128 ? 32 : 64);
     const int g = a.Hq / a.Hkv, kh = blockIdx.y;
-    const int shared_len = c.shared ? a.shared_pages << a.page_log2 : 0;
+    const int shared_len = c.own_from;
     int id = blockIdx.x;
     const bool common = id < c.shared * c.shared_groups;
     if (!common) id -= c.shared * c.shared_groups;
@@ -390,37 +413,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs 
                              sh);
     if (threadIdx.x < kRows) sh.unfinished[threadIdx.x] = 0;
     __syncthreads();
-    float m, l, x[DP / 16];
-    join_rows<DP>(sh, m, l, x);
-    const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (DP / 16);
+    const int row = threadIdx.x >> 4;
     const int64_t rb = (r0 + row) / g;
     const int rh = kh * g + (int)(r0 + row - rb * g);
-    if (c.to.o) {
-        if (row < live) {
-            const int64_t slot = (rb * a.Hq + rh) * c.to.slots + (common ? part : c.shared + part);
-            if ((threadIdx.x & 15) == 0) {
-                c.to.m[slot] = m;
-                c.to.l[slot] = l;
-            }
-            if (l != 0.0f)
-#pragma unroll
-                for (int e = 0; e < DP / 16; e += 4)
-                    *reinterpret_cast<floatx4_t *>(c.to.o + slot * DP + d0 + e) = floatx4_t{x[e], x[e + 1], x[e + 2], x[e + 3]};
-        }
-        return;
-    }
-    if (row < live) {
-        float *out = a.out + rb * a.out_seq + rh * a.out_head;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-        for (int e = 0; e < DP / 16; ++e) {
-            const float y = x[e] * inv;
-            if (d0 + e < a.D) {
-                out[d0 + e] = y;
-                if (!(fabsf(y) < INFINITY)) sh.unfinished[row] = 1;
-            }
-        }
-    }
+    leave_row<DP>(sh, c.to, (rb * a.Hq + rh) * c.to.slots + (common ? part : c.to.slots - c.own + part),
+                  a.out + rb * a.out_seq + rh * a.out_head, a.D, row < live);
+    if (c.to.o) return;
     __syncthreads();
     for (int w = threadIdx.x >> 6; w < live; w += kWaves)
         if (sh.unfinished[w]) {
@@ -429,32 +427,62 @@ __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs 
         }
 }
 
-// Rows from their parts, a wave to a row.
-template <class T, int DP>
-__global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs a, Partials from)
+// Row (i, h) of a call: where its result goes (null: it is no row of a sequence), and its slow form.
+__device__ __forceinline__ float *row_out(const DecodeArgs &a, int64_t i, int h) { return a.out + i * a.out_seq + h * a.out_head; }
+template <class T>
+__device__ __forceinline__ void redo_row(const DecodeArgs &a, int64_t i, int h) { attend_decode_row<T>(a, i, h); }
+__device__ __forceinline__ bool prompt_row(const PromptArgs &a, int64_t i, Sequence &sq)
+{
+    int lo = 0, hi = a.S;  // the largest s < S with cu_q[s] <= i
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (a.cu_q[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    sq = sequence(a, lo);
+    return i >= sq.q0 && i < sq.q0 + sq.nq;
+}
+__device__ __forceinline__ float *row_out(const PromptArgs &a, int64_t i, int h)
+{
+    Sequence sq;
+    return prompt_row(a, i, sq) ? a.out + i * a.out_tok + h * a.out_head : nullptr;
+}
+template <class T>
+__device__ __forceinline__ void redo_row(const PromptArgs &a, int64_t i, int h)
+{
+    Sequence sq;
+    if (prompt_row(a, i, sq)) attend_prompt_row<T>(a, sq, (int)i - sq.q0, h);
+}
+
+// Rows from their parts.  WAVES: of a row, each taking every WAVES-th part,
+// their sums joined in LDS.  Few parts: a wave to a row (a block to a row made
+// 9600 rows of 2 parts cost 15 us).  Many: four (a wave to a row took 10 us
+// for 1024 rows of 68 parts x 128, for want of loads in flight; now 6).
+template <class T, int DP, int WAVES, class Args>
+__global__ __launch_bounds__(256) void join_kernel(Args a, Partials from, int64_t rows)
 {
     constexpr int E = DP / 64;
-    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (row >= (int64_t)a.B * a.Hq) return;
-    const int lane = threadIdx.x & 63;
+    __shared__ float sums[4][DP], weight[4];
+    const int lane = threadIdx.x & 63, w4 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = w4 % WAVES;
+    const int64_t row = min((int64_t)blockIdx.x * (4 / WAVES) + w4 / WAVES, rows - 1), b = row / a.Hq;
+    const int h = (int)(row - b * a.Hq);
+    float *out = row_out(a, b, h);
     const int64_t s0 = row * from.slots;
+    const int slots = out ? from.slots : 0;
     float m = -INFINITY;
-    for (int i = lane; i < from.slots; i += 64) m = fmaxf(m, from.m[s0 + i]);
+    for (int i = lane; i < slots; i += 64) m = fmaxf(m, from.m[s0 + i]);
 #pragma unroll
     for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
     float l = 0.0f, o[E] = {};
-    for (int i0 = 0; i0 < from.slots; i0 += 64) {
-        const int i = i0 + lane;
+    for (int i0 = 0; i0 < slots; i0 += 64 * WAVES) {
+        const int i = i0 + WAVES * lane + wave;
         float f = 0.0f, li = 0.0f;
-        if (i < from.slots) {
+        if (i < slots) {
             const float mi = from.m[s0 + i];
             f = mi == -INFINITY ? 0.0f : exp2_raw(mi - m);
             li = from.l[s0 + i];
         }
-        float t = f * li;
-#pragma unroll
-        for (int x = 32; x; x >>= 1) t += __shfl_xor(t, x);
-        l += t;
+        l = fmaf(f, li, l);
         if (li == 0.0f) f = 0.0f;  // nothing was written there
         uint64_t used = __ballot(f != 0.0f);
         while (used) {
@@ -470,7 +498,7 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs a, Partials
                     used &= used - 1;
                     w[u] = __shfl(f, k);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[u][e] = from.o[(s0 + i0 + k) * DP + lane * E + e];
+                    for (int e = 0; e < E; ++e) x[u][e] = from.o[(s0 + i0 + WAVES * k + wave) * DP + lane * E + e];
                 }
             }
 #pragma unroll
@@ -479,11 +507,24 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs a, Partials
                 for (int e = 0; e < E; ++e) o[e] = fmaf(w[u], x[u][e], o[e]);
         }
     }
-    const int64_t b = row / a.Hq;
-    const int h = (int)(row - b * a.Hq);
-    float *out = a.out + b * a.out_seq + h * a.out_head;
+#pragma unroll
+    for (int x = 32; x; x >>= 1) l += __shfl_xor(l, x);
+    if (WAVES == 4) {
+        if (lane == 0) weight[wave] = l;
+#pragma unroll
+        for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = o[e];
+        __syncthreads();
+        if (wave) return;
+        l = (weight[0] + weight[1]) + (weight[2] + weight[3]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int d = lane * E + e;
+            o[e] = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
+        }
+    }
+    if (!out) return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    bool odd = false;
+    bool odd = !(fabsf(l) < INFINITY);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float y = o[e] * inv;
@@ -492,8 +533,7 @@ __global__ __launch_bounds__(256) void decode_join_kernel(DecodeArgs a, Partials
             odd |= !(fabsf(y) < INFINITY);
         }
     }
-    odd |= !(fabsf(l) < INFINITY);
-    if (__any(odd)) attend_decode_row<T>(a, b, h);
+    if (__any(odd)) redo_row<T>(a, b, h);
 }
 
 // Rows against a pool without pages: 0, or NaN where a sequence has tokens.
@@ -532,59 +572,153 @@ bool wide(const void *p, int64_t strides, int D, bool f16)
         }                                                                                             \
     } while (0)
 
-size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16)
-{
-    return prompt_tile_workspace(S, Tk, Hkv, D, kv_f16);
-}
+size_t partial_bytes(int64_t rows, int slots, int dim) { return slots > 1 ? (size_t)rows * slots * (dim + 2) * 4 : 0; }
 
-hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream)
+void place_partials(Partials &to, int64_t rows, void *at)
 {
-    const int g = a.Hq / a.Hkv;
-    const int64_t units = (int64_t)a.Tq * g / kRows + a.S;
-    if (a.Hkv > 65535 || units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const bool w = wide(a.k.data, a.k.tok | a.k.head, a.D, a.kv_f16) && wide(a.v.data, a.v.tok | a.v.head, a.D, a.kv_f16);
-    static const int force = getenv("CF_FORCE") ? atoi(getenv("CF_FORCE")) : 0;
-    if (a.Tk > 0 && (!a.kv_f16 || (w && a.k.tok < ((int64_t)1 << 31) && a.v.tok < ((int64_t)1 << 31))) && (force == 2 || (force == 0 && a.Tq >= 1024))) return launch_prompt_tile(a, workspace, stream);
-    const dim3 grid((unsigned)units, (unsigned)a.Hkv);
-    CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, w, grid, 64 * kWaves, a);
-    return hipGetLastError();
+    if (to.slots <= 1) return;
+    const int64_t n = rows * to.slots;
+    to.o = (float *)at;
+    to.m = to.o + n * to.dim;
+    to.l = to.m + n;
 }
 
 namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int padded(int64_t D) { return D <= 64 ? 64 : 128; }
 
-// Parts are made until the grid has kTargetBlocks blocks (2 of 4 waves to a
-// CU, twice over), of at least one step of all waves each.
-DecodeParts decode_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int lg, int64_t shared_pages)
+template <class Args>
+hipError_t join(const Args &a, const Partials &from, int64_t rows, hipStream_t stream)
 {
-    constexpr int64_t kTargetBlocks = 1024;
+    const bool four = from.slots > 16;
+    const unsigned blocks = (unsigned)(four ? rows : ceil_div(rows, 4));
+#define CFP32_JOIN(T, DP)                                                            \
+    do {                                                                           \
+        if (four) join_kernel<T, DP, 4><<<blocks, 256, 0, stream>>>(a, from, rows); \
+        else join_kernel<T, DP, 1><<<blocks, 256, 0, stream>>>(a, from, rows);      \
+    } while (0)
+    if (a.kv_f16) {
+        if (a.D <= 64) CFP32_JOIN(_Float16, 64);
+        else CFP32_JOIN(_Float16, 128);
+    } else {
+        if (a.D <= 64) CFP32_JOIN(float, 64);
+        else CFP32_JOIN(float, 128);
+    }
+#undef CFP32_JOIN
+    return hipGetLastError();
+}
+
+// Parts are made until the grid has `blocks` blocks (of 4 waves), of at least
+// one step of all waves each.
+constexpr int64_t kDecodeBlocks = 512, kPromptBlocks = 256;
+int key_parts(int64_t keys, int64_t unit, int64_t blocks, int64_t target)
+{
+    const int64_t most = ceil_div(keys, unit), want = target / (blocks ? blocks : 1);
+    return (int)(want <= 1 || most <= 1 ? 1 : most < want ? most : want);
+}
+int64_t wave_step(int64_t D) { return D <= 64 ? 64 : 32; }
+
+// How many parts the keys of a short prompt make: by the average sequence's.
+int prompt_parts(int64_t S, int64_t Tk, int64_t blocks, int64_t D)
+{
+    return key_parts(ceil_div(Tk, S), kWaves * wave_step(D), blocks, kPromptBlocks);
+}
+
+// Which kernel a prompt goes through, by estimates in microseconds beyond what
+// both have in common: here FP32 matrix products (45 TFLOP/s of the useful
+// ones, 75 with FP16 keys) and the blocks, there the way through the longest
+// sequence's tiles and what comes before (for FP32 K and V a pass over them).
+// Measured, 16 rows to a block against tiles: FP32 500 / 750 / 1000 x 12 x 64
+// 17 / 26 / 38 against 25 / 30 / 36 us, 300 / 500 x 32/8 x 128 26 / 48 against
+// 31 / 38; FP16 500 / 1500 x 12 x 64 13 / 38 against 17 / 34, 300 / 500 x 32/8 x
+// 128 20 / 33 against 21 / 25, 8 x 60 and 4 x 100 of these 19 and 17 against 14
+// and 14, 50 after 700 16 against 20.
+bool prefer_tiles(const PromptArgs &a, int64_t units)
+{
+    const double keys = (double)a.Tk / a.S, seen = a.causal ? keys - 0.5 * a.Tq / a.S : keys;
+    const double gflop = 4e-9 * a.D * a.Hq * a.Tq * (seen > 0 ? seen : 0), tiles = keys / 64;
+    const double rows_us = gflop * (a.kv_f16 ? 1e3 / 75 : 1e3 / 45) + 0.008 * units * a.Hkv;
+    const double tiles_us = a.kv_f16 ? (a.D <= 64 ? 4 + 1.1 * tiles : 4 + 2 * tiles) : (a.D <= 64 ? 6 + 1.7 * tiles : 10 + 3 * tiles);
+    return rows_us > tiles_us;
+}
+
+}  // namespace
+
+hipError_t launch_join(const PromptArgs &a, const Partials &from, hipStream_t stream)
+{
+    return join(a, from, (int64_t)a.Tq * a.Hq, stream);
+}
+hipError_t launch_join(const DecodeArgs &a, const Partials &from, hipStream_t stream)
+{
+    return join(a, from, (int64_t)a.B * a.Hq, stream);
+}
+
+size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16)
+{
+    // Whatever the rows are, blocks of kRows of them and parts make no more than kPromptBlocks.
+    const size_t parts = prompt_parts(S, Tk, 1, D) > 1 ? partial_bytes(kPromptBlocks * kRows / 2, 2, padded(D)) : 0;
+    const size_t tiles = prompt_tile_workspace(S, Tk, Hkv, D, kv_f16);
+    return parts > tiles ? parts : tiles;
+}
+
+hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream)
+{
+    const int g = a.Hq / a.Hkv;
+    const int64_t units = (int64_t)a.Tq * g / kRows + a.S, rows = (int64_t)a.Tq * a.Hq;
+    if (units > 0x7FFFFFFF / a.Hkv || rows > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    const bool w = wide(a.k.data, a.k.tok | a.k.head, a.D, a.kv_f16) && wide(a.v.data, a.v.tok | a.v.head, a.D, a.kv_f16);
+    const bool can = a.Tk > 0 && (!a.kv_f16 || (w && a.k.tok < ((int64_t)1 << 31) && a.v.tok < ((int64_t)1 << 31)));
+    if (can && prefer_tiles(a, units)) return launch_prompt_tile(a, workspace, stream);
+    Partials to = {nullptr, nullptr, nullptr, prompt_parts(a.S, a.Tk, units * a.Hkv, a.D), padded(a.D)};
+    place_partials(to, rows, workspace);
+    const dim3 grid((unsigned)(units * a.Hkv), (unsigned)to.slots);
+    CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, w, grid, 64 * kWaves, a, to);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || !to.o ? e : launch_join(a, to, stream);
+}
+
+namespace {
+
+// More rows than this share a prefix: its keys go through attention_tile.hip's
+// kernel (if the pages allow).
+constexpr int64_t kTileRows = 32;
+
+// `tiled`: the shared keys are cut for the other kernel, and c.shared is 0.
+DecodeParts decode_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int lg, int64_t shared_pages, bool tiles,
+                         int &tiled)
+{
     DecodeParts c = {};
-    const int64_t g = Hq / Hkv, unit = kWaves * (D <= 64 ? 64 : 32);
-    const int64_t n_shared = B > 1 ? shared_pages << lg : 0;
-    const int64_t n_own = (W << lg) - n_shared;
+    const int64_t g = Hq / Hkv, unit = kWaves * wave_step(D);
+    const int64_t n_shared = B > 1 ? shared_pages << lg : 0, n_own = (W << lg) - n_shared;
     c.shared_groups = (int)ceil_div(B * g, kRows);
     c.own_groups = (int)ceil_div(g, kRows);
-    auto parts = [&](int64_t keys, int64_t blocks) {
-        const int64_t most = ceil_div(keys, unit), want = ceil_div(kTargetBlocks, blocks);
-        return (int)(most < want ? most : want);
-    };
-    if (n_shared) c.shared = parts(n_shared, c.shared_groups * Hkv);
-    c.own = n_own > 0 ? parts(n_own, B * c.own_groups * Hkv) : 0;
-    if (c.shared + c.own == 0) c.own = 1;
-    c.to.slots = c.shared + c.own;
-    c.to.dim = D <= 64 ? 64 : 128;
+    c.own_from = (int)n_shared;
+    tiled = 0;
+    if (n_shared) {
+        if (tiles && B * g > kTileRows) tiled = decode_tile_parts(B, Hq, Hkv, n_shared, lg);
+        else c.shared = key_parts(n_shared, unit, c.shared_groups * Hkv, kDecodeBlocks);
+    }
+    if (n_own > 0) c.own = key_parts(n_own, unit, B * c.own_groups * Hkv, kDecodeBlocks);
+    if (tiled + c.shared + c.own == 0) c.own = 1;
+    c.to.slots = tiled + c.shared + c.own;
+    if (tiled && c.to.slots == 1) c.to.slots = 2;  // always by way of slots; the second is an empty part
+    if (tiled && c.own == 0) c.own = c.to.slots - tiled;
+    c.to.dim = padded(D);
     return c;
 }
 
 }  // namespace
 
-size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int lg,
-                                  int64_t shared_pages, bool)
+size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int lg, int64_t shared_pages,
+                                  bool kv_f16)
 {
     if (Hkv == 0) return 0;
-    const DecodeParts c = decode_parts(B, Hq, Hkv, D, W, lg, shared_pages);
-    return c.to.slots > 1 ? (size_t)(B * Hq) * c.to.slots * (c.to.dim + 2) * 4 : 0;
+    int tiled;
+    const size_t a = partial_bytes(B * Hq, decode_parts(B, Hq, Hkv, D, W, lg, shared_pages, false, tiled).to.slots, padded(D));
+    if (!kv_f16) return a;
+    const size_t b = partial_bytes(B * Hq, decode_parts(B, Hq, Hkv, D, W, lg, shared_pages, true, tiled).to.slots, padded(D));
+    return a > b ? a : b;
 }
 
 hipError_t launch_attention_decode(const DecodeArgs &a, void *workspace, hipStream_t stream)
@@ -595,30 +729,23 @@ hipError_t launch_attention_decode(const DecodeArgs &a, void *workspace, hipStre
         decode_no_pages_kernel<<<grid, 64, 0, stream>>>(a);
         return hipGetLastError();
     }
-    DecodeParts c = decode_parts(a.B, a.Hq, a.Hkv, a.D, a.W, a.page_log2, a.shared_pages);
-    const int64_t rows = (int64_t)a.B * a.Hq, n = rows * c.to.slots;
+    const bool w = wide(a.k.data, a.k.page | a.k.head | a.k.tok, a.D, a.kv_f16) &&
+                   wide(a.v.data, a.v.page | a.v.head | a.v.tok, a.D, a.kv_f16);
+    const bool tiles = a.kv_f16 && w && a.k.tok < ((int64_t)1 << 31) && a.v.tok < ((int64_t)1 << 31);
+    int tiled;
+    DecodeParts c = decode_parts(a.B, a.Hq, a.Hkv, a.D, a.W, a.page_log2, a.shared_pages, tiles, tiled);
+    const int64_t rows = (int64_t)a.B * a.Hq;
     const int64_t blocks = (int64_t)c.shared * c.shared_groups + (int64_t)a.B * c.own_groups * c.own;
-    if (blocks > 0x7FFFFFFF || (rows + 3) / 4 > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    if (c.to.slots > 1) {
-        c.to.o = (float *)workspace;
-        c.to.m = c.to.o + n * c.to.dim;
-        c.to.l = c.to.m + n;
+    if (blocks > 0x7FFFFFFF || rows > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    place_partials(c.to, rows, workspace);
+    if (tiled) {
+        const hipError_t e = launch_decode_tile(a, c.to, tiled, stream);
+        if (e != hipSuccess) return e;
     }
-    const int64_t eb_k = a.k.page | a.k.head | a.k.tok, eb_v = a.v.page | a.v.head | a.v.tok;
-    const bool w = wide(a.k.data, eb_k, a.D, a.kv_f16) && wide(a.v.data, eb_v, a.D, a.kv_f16);
     const dim3 grid((unsigned)blocks, (unsigned)a.Hkv);
     CFP32_BY_TYPE(decode_rows_kernel, a.kv_f16, a.D, w, grid, 64 * kWaves, a, c);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || c.to.slots <= 1) return e;
-    const unsigned join = (unsigned)((rows + 3) / 4);
-    if (a.kv_f16) {
-        if (a.D <= 64) decode_join_kernel<_Float16, 64><<<join, 256, 0, stream>>>(a, c.to);
-        else decode_join_kernel<_Float16, 128><<<join, 256, 0, stream>>>(a, c.to);
-    } else {
-        if (a.D <= 64) decode_join_kernel<float, 64><<<join, 256, 0, stream>>>(a, c.to);
-        else decode_join_kernel<float, 128><<<join, 256, 0, stream>>>(a, c.to);
-    }
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || !c.to.o ? e : launch_join(a, c.to, stream);
 }
 
 }  // namespace cfp32

@@ -201,13 +201,4 @@ __device__ __forceinline__ void split_scaled(float x, int e, _Float16 &hi, _Floa
     lo = (_Float16)(y - (float)hi);
 }
 
-// What several blocks contribute to one row (decode): unnormalised sums,
-// their maxima (in powers of two) and weights.  Slot i of row r is entry
-// r * slots + i.
-struct Partials {
-    float *o;   // [rows * slots, dim]
-    float *m, *l;
-    int slots, dim;
-};
-
 }  // namespace cfp32

@@ -23,7 +23,6 @@
 //     64 bytes) so that four rows do.
 //   * The running maximum is followed lazily (kLazy), so that most tiles do
 //     not touch the output sums.
-#include <stdlib.h>
 #include <type_traits>
 
 #include "attention_device.h"
@@ -61,12 +60,14 @@ __host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2
 // ---- Where a tile's rows are ------------------------------------------------------
 
 // Rows row0 + lr of a tile (row0 the same for the wave), 16-byte chunk `chunk`.
+// page(): what has to be looked up for that, before the loads of several rows.
 struct PlaneSource {
     const char *tiles;      // of this head and sequence
     const int32_t *shifts;
     int last;               // a tile beyond the last repeats it: no row sees it
+    __device__ __forceinline__ int page(int, int, int) const { return 0; }
     template <int DP>
-    __device__ __forceinline__ const char *at(int value, int plane, int tile, int row0, int lr, int chunk) const
+    __device__ __forceinline__ const char *at(int value, int plane, int tile, int row0, int lr, int chunk, int) const
     {
         const char *from = tiles + (int64_t)min(tile, last) * tile_bytes<DP>(2) + (value * 2 + plane) * (kTile * DP * 2);
         return from + row0 * (DP * 2) + (uint32_t)(lr * (DP * 2) + chunk * 16);
@@ -82,11 +83,35 @@ struct PackedSource {
     const char *k, *v;      // key 0
     int64_t k_tok, v_tok;   // bytes, below 2^32
     int last, chunks;       // a key or chunk beyond the last repeats one: it meets a weight or an element of 0
+    __device__ __forceinline__ int page(int, int, int) const { return 0; }
     template <int DP>
-    __device__ __forceinline__ const char *at(int value, int, int tile, int row0, int lr, int chunk) const
+    __device__ __forceinline__ const char *at(int value, int, int tile, int row0, int lr, int chunk, int) const
     {
         const uint32_t j = (uint32_t)min(tile * kTile + row0 + lr, last);
         const char *base = (value ? v : k) + (uint64_t)j * (uint32_t)(value ? v_tok : k_tok);
+        return base + (chunk < chunks ? chunk : 0) * 16;
+    }
+    __device__ __forceinline__ int shift(int, int) const { return 0; }
+};
+
+constexpr int kPageIds = 2048;  // pages of a block's keys
+
+struct PagedSource {
+    const char *k, *v;      // the head in page 0
+    int64_t k_page, v_page;
+    uint32_t k_tok, v_tok;  // bytes
+    const int *ids;         // LDS: the pages from that of key `first` on
+    int first, last, chunks, lg;
+    __device__ __forceinline__ int page(int tile, int row0, int lr) const
+    {
+        return ids[(min(tile * kTile + row0 + lr, last) >> lg) - (first >> lg)];
+    }
+    template <int DP>
+    __device__ __forceinline__ const char *at(int value, int, int tile, int row0, int lr, int chunk, int page) const
+    {
+        const int j = min(tile * kTile + row0 + lr, last);
+        const uint32_t o = j & ((1 << lg) - 1);
+        const char *base = (value ? v : k) + (int64_t)page * (value ? v_page : k_page) + (uint64_t)o * (value ? v_tok : k_tok);
         return base + (chunk < chunks ? chunk : 0) * 16;
     }
     __device__ __forceinline__ int shift(int, int) const { return 0; }
@@ -137,19 +162,20 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
 
     // Loads are 64 chunks each, PER of each of the first four waves to a plane:
     // load n of a tile's K or V.
-    auto fetch = [&](int value, int tile, uint4 *buf, int n) {
+    auto page = [&](int tile, int n) { return src.page(tile, (wave * PER + n % PER) * (64 / CH), lane / CH); };
+    auto fetch = [&](int value, int tile, uint4 *buf, int n, int at_page) {
         const int i = n % PER, p = n / PER, piece = wave * PER + i, row0 = piece * (64 / CH);
         int from_lane = lane;
         asm("" : "+v"(from_lane));  // the addresses are made again each time: kept, they would cost the products registers
         const int lr = from_lane / CH;
         const int c = (from_lane % CH) ^ (value ? v_swizzle(lr) ^ v_swizzle(i * (64 / CH)) : k_swizzle(lr) ^ k_swizzle(i * (64 / CH)));
-        __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)src.template at<DP>(value, p, tile, row0, lr, c),
+        __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)src.template at<DP>(value, p, tile, row0, lr, c, at_page),
                                          (CFP32_LDS void *)(buf + p * PLANE + piece * 64), 16, 0, 0);
     };
     t1 += (t1 - t0) & 1;
     if (wave < 4) {
 #pragma unroll
-        for (int n = 0; n < LOADS; ++n) fetch(0, t0, k0, n);
+        for (int n = 0; n < LOADS; ++n) fetch(0, t0, k0, n, page(t0, n));
     }
 
     // The row, at 2^e2, as the right operand of the scores.
@@ -328,7 +354,10 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
     // can be filled from phase 2 t + 2 on, and must be full when phase 2 t + 4
     // begins.  The first group does that: it asks for the loads between its
     // products in phase 2 t + 2 and waits for them at the end of 2 t + 3.
-    // With four waves there is one group, and a barrier before its products.
+    // With four waves there is one group, often beside another block's, and a
+    // barrier before its products (asking for the loads before the weights
+    // instead, for a longer flight, was slower: 8192 x 32/8 x 128 FP16 955 ->
+    // 1011 us).
     auto sync = [] {
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -346,8 +375,9 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
         int t = t0;
         // K(u), V(u - 1); beyond the last tile, where no one reads them, the last again.
         auto refill = [&](int u, uint4 *kb, uint4 *vb) {
-            return [=, &fetch](int n) {
-                if (!second) fetch(n >= LOADS, n >= LOADS ? u - 1 : u, n >= LOADS ? vb : kb, n % LOADS);
+            return [=, &fetch, &page](int n) {
+                const int tile = n >= LOADS ? u - 1 : u;
+                if (!second) fetch(n >= LOADS, tile, n >= LOADS ? vb : kb, n % LOADS, page(tile, n % LOADS));
             };
         };
         // Weights of tile t, its values, the next one's scores (unless it is the last).
@@ -397,16 +427,56 @@ __device__ __forceinline__ void store4(float *out, const float (&y)[4], int n, b
         if (e < n) out[e] = y[e];
 }
 
+template <int DP>
+__device__ __forceinline__ void no_rows(WaveRows<DP> &w)
+{
+    w.m = -INFINITY, w.l = 0.0f, w.scale = 0;
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w.o[b][e] = 0.0f;
+}
+
+// A wave's rows into their slots.
+template <int DP>
+__device__ __forceinline__ void leave_rows(const WaveRows<DP> &w, const Partials &to, int64_t slot, bool live)
+{
+    const int half = (threadIdx.x & 63) >> 5;
+    if (!live) return;
+    if (half == 0) {
+        to.m[slot] = w.m;
+        to.l[slot] = __builtin_amdgcn_ldexpf(w.l, -kTopWeight);
+    }
+    if (w.l == 0.0f) return;
+#pragma unroll
+    for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            floatx4_t y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = __builtin_amdgcn_ldexpf(w.o[b][4 * c + e], -w.scale);
+            *reinterpret_cast<floatx4_t *>(to.o + slot * DP + 32 * b + 8 * c + 4 * half) = y;
+        }
+}
+
+// Tiles [0, n) in parts of an even number.
+__device__ __forceinline__ void part_tiles(int n, int part, int parts, int &t0, int &t1)
+{
+    const int per = ((n + parts - 1) / parts + 1) & ~1;
+    t0 = (int)min((int64_t)n, (int64_t)part * per);
+    t1 = min(n, t0 + per);
+}
+
 // ---- Long prompts -------------------------------------------------------------------
 
 template <class T, int DP, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, Planes planes)
+__global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, Planes planes, Partials to)
 {
     constexpr int PL = sizeof(T) == 4 ? 2 : 1;
     constexpr int kBlockRows = NW * kWaveRows;
     __shared__ uint4 k0[PL * kTile * DP / 8], k1[PL * kTile * DP / 8], v0[PL * kTile * DP / 8], v1[PL * kTile * DP / 8];
     const int g = a.Hq / a.Hkv;
-    const int kh = blockIdx.x % a.Hkv;
+    const int kh = blockIdx.x % a.Hkv, part = blockIdx.y;
     const int64_t id = (gridDim.x - 1 - blockIdx.x) / a.Hkv;  // the rows that see most first
     int64_t start;
     const int sid = find_unit(a.cu_q, a.S, g, kBlockRows, id, start);
@@ -422,25 +492,23 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     const float *q = (const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head;
     const bool q_wide = rows_wide(a.q.data, a.q.tok | a.q.head, a.D);
     WaveRows<DP> w;
-    const int tiles = (keys + kTile - 1) / kTile;
-    if (tiles == 0) {
-        w.m = -INFINITY, w.l = 0.0f, w.scale = 0;
-#pragma unroll
-        for (int b = 0; b < DP / 32; ++b)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w.o[b][e] = 0.0f;
+    int t0, t1;
+    part_tiles((keys + kTile - 1) / kTile, part, to.slots, t0, t1);
+    if (t0 >= t1) {
+        no_rows<DP>(w);
     } else if constexpr (PL == 2) {
         const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
-        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot, tiles - 1};
-        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, 0, tiles, src, k0, k1, v0, v1, w);
+        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot, t1 - 1};
+        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                                   (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                                   a.k.tok * 2, a.v.tok * 2, sq.nk - 1, a.D / 8};
-        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, 0, tiles, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     }
     if (!rows) return;
     const bool live = first + (lane & 31) < n;
+    if (to.o) return leave_rows<DP>(w, to, ((int64_t)(sq.q0 + i) * a.Hq + h) * to.slots + part, live);
     // l is summed at 2^kTopWeight, o at 2^scale.
     const float inv = w.l == 0.0f ? 0.0f : __builtin_amdgcn_ldexpf(1.0f / w.l, kTopWeight);
     float *out = a.out + (sq.q0 + i) * a.out_tok + h * a.out_head;
@@ -466,6 +534,52 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
         const int ri = (int)(rr / g);
         attend_prompt_row<T>(a, sq, ri, kh * g + (int)(rr - (int64_t)ri * g));
     }
+}
+
+// ---- A prefix that all sequences of a decode share -----------------------------------
+
+// 128 rows (sequences x heads of a K/V head) against one part of the shared
+// keys, into slot `part`.
+template <int DP>
+__global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Partials to, int parts)
+{
+    __shared__ uint4 k0[kTile * DP / 8], k1[kTile * DP / 8], v0[kTile * DP / 8], v1[kTile * DP / 8];
+    __shared__ int ids[kPageIds];
+    __shared__ int first_bad;
+    const int g = a.Hq / a.Hkv, part = blockIdx.x % parts, kh = blockIdx.x / parts % a.Hkv;
+    const int64_t n = (int64_t)a.B * g, r0 = (int64_t)(blockIdx.x / parts / a.Hkv) * 128;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
+    const int64_t b = r / g;
+    const int h = kh * g + (int)(r - b * g);
+    const int shared = a.shared_pages << a.page_log2;
+    const int limit = min(decode_length(a, (int)b), shared);
+    int t0, t1;
+    part_tiles((shared + kTile - 1) / kTile, part, parts, t0, t1);
+    WaveRows<DP> w;
+    if (t0 < t1) {
+        const int j0 = t0 * kTile, last = min(t1 * kTile, shared) - 1, p0 = j0 >> a.page_log2, p1 = last >> a.page_log2;
+        if (threadIdx.x == 0) first_bad = 0x7FFFFFFF;
+        __syncthreads();
+        for (int i = threadIdx.x; i <= p1 - p0; i += 256) {
+            int id = a.table[p0 + i];
+            if (id < 0 || id >= a.P) {  // page 0 instead; rows that see it become NaN
+                id = 0;
+                atomicMin(&first_bad, (p0 + i) << a.page_log2);
+            }
+            ids[i] = id;
+        }
+        __syncthreads();
+        const PagedSource src = {(const char *)((const _Float16 *)a.k.data + kh * a.k.head),
+                                 (const char *)((const _Float16 *)a.v.data + kh * a.v.head), a.k.page * 2, a.v.page * 2,
+                                 (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), ids, j0, last, a.D / 8, a.page_log2};
+        attend_tiles<DP, 1, 4>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, limit, a.scale,
+                               t0, t1, src, k0, k1, v0, v1, w);
+        if (limit > first_bad) w.l = NAN;
+    } else {
+        no_rows<DP>(w);
+    }
+    leave_rows<DP>(w, to, (b * a.Hq + h) * to.slots + part, first + (lane & 31) < n);
 }
 
 // FP32 K and V of one tile and head as two FP16 planes each.
@@ -543,21 +657,45 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
 
 }  // namespace
 
+namespace {
+
+int64_t plane_bytes(int64_t slots, int64_t Hkv, int64_t D)
+{
+    const int64_t n = slots * Hkv * ((D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)) + 8);
+    return (n + 255) & ~(int64_t)255;
+}
+
+// Where blocks of 128 rows are few, their keys make parts, up to kTileBlocks
+// blocks, of at least kPartTiles tiles for the average sequence: 1500 x 12 x
+// 64 FP32 (144 blocks) 55 -> 46 us; with 200 to 256 blocks two parts cost more
+// than they gave (1000 x 32/8 x 128 FP16 43 -> 53 us), and so did parts of
+// four tiles (4 x 300 x 12 x 64 FP16 after 100 each 16 -> 25 us).
+constexpr int64_t kTileBlocks = 320, kPartTiles = 8;
+int tile_parts(int64_t S, int64_t Tk, int64_t blocks)
+{
+    const int64_t most = (Tk / S + kPartTiles * kTile - 1) / (kPartTiles * kTile), want = kTileBlocks / blocks;
+    return (int)(want <= 1 || most <= 1 ? 1 : most < want ? most : want);
+}
+
+}  // namespace
+
 size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16)
 {
-    if (kv_f16) return 0;
-    const int64_t tiles = (Tk / kTile + S) * Hkv;
-    return (size_t)(tiles * ((D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)) + 8));
+    // Whatever the rows are, blocks of 128 of them and parts make no more than kTileBlocks.
+    const size_t parts = tile_parts(S, Tk, 1) > 1 ? partial_bytes(kTileBlocks * 128 / 2, 2, D <= 64 ? 64 : 128) : 0;
+    return parts + (kv_f16 ? 0 : plane_bytes(Tk / kTile + S, Hkv, D));
 }
 
 hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream)
 {
     const int g = a.Hq / a.Hkv;
     Planes planes = {};
+    char *ws = (char *)workspace;
     if (!a.kv_f16) {
         planes.slots = a.Tk / kTile + a.S;
-        planes.tiles = (char *)workspace;
-        planes.shifts = (int32_t *)(planes.tiles + planes.slots * a.Hkv * (a.D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)));
+        planes.tiles = ws;
+        planes.shifts = (int32_t *)(ws + planes.slots * a.Hkv * (a.D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)));
+        ws += plane_bytes(planes.slots, a.Hkv, a.D);
         if (planes.slots > 0x7FFFFFFF || a.Hkv > 65535) return hipErrorInvalidConfiguration;
         const dim3 grid((unsigned)planes.slots, (unsigned)a.Hkv);
         if (a.D <= 64) prompt_planes_kernel<64><<<grid, 256, 0, stream>>>(a, planes);
@@ -565,21 +703,54 @@ hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t 
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-#define CFP32_PROMPT(T, DP, NW)                                                                                    \
-    do {                                                                                                           \
-        const int64_t units = ((int64_t)a.Tq * g / (NW * kWaveRows) + a.S) * a.Hkv;                                \
-        if (units > 0x7FFFFFFF) return hipErrorInvalidConfiguration;                                               \
-        prompt_tile_kernel<T, DP, NW><<<(unsigned)units, 64 * NW, 0, stream>>>(a, planes);                         \
-    } while (0)
-    static const int nw = getenv("CF_NW") ? atoi(getenv("CF_NW")) : 8;
-    if (a.kv_f16) {
-        if (a.D <= 64) { if (nw == 4) CFP32_PROMPT(_Float16, 64, 4); else CFP32_PROMPT(_Float16, 64, 8); }
-        else { if (nw == 4) CFP32_PROMPT(_Float16, 128, 4); else CFP32_PROMPT(_Float16, 128, 8); }
+    const int64_t blocks = ((int64_t)a.Tq * g / 128 + a.S) * a.Hkv;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    Partials to = {nullptr, nullptr, nullptr, tile_parts(a.S, a.Tk, blocks), a.D <= 64 ? 64 : 128};
+    place_partials(to, (int64_t)a.Tq * a.Hq, ws);
+    // Eight waves multiply and make weights at the same time; four give more
+    // and shorter blocks.  Two blocks of four to a CU and not more: four
+    // (1024 x 32/8 x 128 FP16 52 -> 43 us, FP32 77 -> 66; 8192: 903 -> 955 and
+    // 1321 -> 1572).
+    const bool eight = blocks > 512;
+#define CFP32_PROMPT(T, DP, NW)                                                                                       \
+    prompt_tile_kernel<T, DP, NW><<<dim3((unsigned)(((int64_t)a.Tq * g / (NW * kWaveRows) + a.S) * a.Hkv),             \
+                                         (unsigned)to.slots), 64 * NW, 0, stream>>>(a, planes, to)
+    if (a.kv_f16 && a.D <= 64) {
+        if (eight) CFP32_PROMPT(_Float16, 64, 8);
+        else CFP32_PROMPT(_Float16, 64, 4);
+    } else if (a.kv_f16) {
+        if (eight) CFP32_PROMPT(_Float16, 128, 8);
+        else CFP32_PROMPT(_Float16, 128, 4);
+    } else if (a.D <= 64) {
+        if (eight) CFP32_PROMPT(float, 64, 8);
+        else CFP32_PROMPT(float, 64, 4);
     } else {
-        if (a.D <= 64) { if (nw == 4) CFP32_PROMPT(float, 64, 4); else CFP32_PROMPT(float, 64, 8); }
-        else { if (nw == 4) CFP32_PROMPT(float, 128, 4); else CFP32_PROMPT(float, 128, 8); }
+        if (eight) CFP32_PROMPT(float, 128, 8);
+        else CFP32_PROMPT(float, 128, 4);
     }
 #undef CFP32_PROMPT
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || !to.o ? e : launch_join(a, to, stream);
+}
+
+int decode_tile_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t keys, int page_log2)
+{
+    const int64_t blocks = (B * (Hq / Hkv) + 127) / 128 * Hkv, tiles = (keys + kTile - 1) / kTile;
+    int64_t parts = 512 / blocks;  // two blocks to a CU
+    if (parts > (tiles + 3) / 4) parts = (tiles + 3) / 4;
+    if (parts < 1) parts = 1;
+    // A part's page ids (and two tiles' more, by rounding) fit the block's list.
+    const int64_t room = ((int64_t)kPageIds - 2) << page_log2, per = room / kTile - 2;
+    const int64_t least = (tiles + per - 1) / per;
+    return (int)(parts > least ? parts : least);
+}
+
+hipError_t launch_decode_tile(const DecodeArgs &a, const Partials &to, int parts, hipStream_t stream)
+{
+    const int64_t blocks = ((int64_t)a.B * (a.Hq / a.Hkv) + 127) / 128 * a.Hkv * parts;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (a.D <= 64) decode_tile_kernel<64><<<(unsigned)blocks, 256, 0, stream>>>(a, to, parts);
+    else decode_tile_kernel<128><<<(unsigned)blocks, 256, 0, stream>>>(a, to, parts);
     return hipGetLastError();
 }
 
