@@ -95,16 +95,18 @@ struct Joined {
     int unfinished[kRows];
 };
 
-// One wave's share of 16 rows: this lane's row q sees the first
-// `limit` keys; keys [lo, hi) (lo a multiple of 16 if pages are to be read
-// 16 keys at a time), every kWaves-th step of them.
-template <class T, int DP, bool WIDE, class Keys>
-__device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, int limit, float scale, int lo, int hi, Keys keys,
-                                            Joined &to)
+template <int DP>
+constexpr int row_step() { return DP == 128 ? 32 : 64; }  // keys a wave takes at a time
+
+// One wave's share of 16 rows: this lane's row q sees the first `limit` keys;
+// the wave takes keys [kb, hi), row_step at a time, kWaves steps further each
+// time.  FEW: there is one step, of which blocks of 16 keys may be missing.
+template <class T, int DP, bool WIDE, bool FEW, class Keys>
+__device__ __forceinline__ void attend_share(const float *q, bool q_wide, int D, int limit, float scale, int kb, int hi, Keys keys,
+                                             Joined &to)
 {
     constexpr bool F16 = sizeof(T) == 2;
-    constexpr int NB = DP == 128 ? 2 : 4;      // 16-key blocks of a step
-    constexpr int kStep = 16 * NB;
+    constexpr int kStep = row_step<DP>(), NB = kStep / 16;
     constexpr int KK = F16 ? DP / 32 : DP / 16;  // key loads (16 bytes) of a lane and block
     constexpr int KE = F16 ? 8 : 4;
     constexpr int NV = DP / 16;                // value elements of a lane and key
@@ -116,8 +118,15 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
 #pragma unroll
     for (int c = 0; c < NV; ++c) o[c] = floatx4_t{0, 0, 0, 0};
 
-    int kb = lo + wave * kStep;
     if (kb < hi) {
+        float x[KK][KE];
+        if (q_wide) {
+#pragma unroll
+            for (int i = 0; i < KK; ++i) load_floats<KE, true>(q, (i * 4 + quad) * KE, D, x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KK; ++i) load_floats<KE, false>(q, (i * 4 + quad) * KE, D, x[i]);
+        }
         T kr[NB][KK][KE], vr[NB][4][NV];
         int page[NB], next[NB];
         const int last = hi - 1;
@@ -128,6 +137,7 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
         auto load_k = [&](int b0) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
+                if (FEW && b && b0 + 16 * b > last) continue;  // no such keys
                 const char *p = keys.key(min(b0 + 16 * b + col, last), page[b]);
 #pragma unroll
                 for (int i = 0; i < KK; ++i) load_row<T, KE, WIDE>(p, (i * 4 + quad) * KE, D, kr[b][i]);
@@ -135,27 +145,21 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
         };
         auto load_v = [&](int b0) {
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b) {
+                if (FEW && b && b0 + 16 * b > last) continue;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     load_row<T, NV, WIDE>(keys.value(min(b0 + 16 * b + 4 * quad + r, last), page[b]), col * NV, D, vr[b][r]);
+            }
         };
         pages(kb, page);
         load_k(kb);
         load_v(kb);
-        pages(kb + kWaves * kStep, next);
+        if (!FEW) pages(kb + kWaves * kStep, next);
 
         // The row, as the right operand of the score products.
         float f = scale * kLog2e;
         half8_t qh[F16 ? KK : 1], ql[F16 ? KK : 1];
-        float x[KK][KE];
-        if (q_wide) {
-#pragma unroll
-            for (int i = 0; i < KK; ++i) load_floats<KE, true>(q, (i * 4 + quad) * KE, D, x[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < KK; ++i) load_floats<KE, false>(q, (i * 4 + quad) * KE, D, x[i]);
-        }
         if constexpr (F16) {
             float mx = 0.0f;
 #pragma unroll
@@ -179,11 +183,12 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
             f = __builtin_amdgcn_ldexpf(f, -e2);
         }
 
-        for (; kb < hi; kb += kWaves * kStep) {
+        for (bool again = true; again; again = !FEW && kb < hi) {
             floatx4_t s[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 s[b] = floatx4_t{0, 0, 0, 0};
+                if (FEW && b && kb + 16 * b > last) continue;
 #pragma unroll
                 for (int i = 0; i < KK; ++i) {
                     if constexpr (F16) {
@@ -200,7 +205,7 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
                 }
             }
             const int nb = kb + kWaves * kStep;
-            const bool more = nb < hi;
+            const bool more = !FEW && nb < hi;
             if (more) {
                 // The next step's pages are known; ask for those after it first.
 #pragma unroll
@@ -228,7 +233,8 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
             }
             const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b) {
+                if (FEW && b && kb + 16 * b > last) continue;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float p = exp2_raw(s[b][r] - base);
@@ -237,7 +243,9 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
                     for (int c = 0; c < NV; ++c)
                         o[c] = __builtin_amdgcn_mfma_f32_16x16x4f32((float)vr[b][r][c], p, o[c], 0, 0, 0);
                 }
+            }
             if (more) load_v(nb);
+            kb = nb;
         }
         int bad = keys.first_bad();
         if (__any(bad != 0x7FFFFFFF)) {
@@ -261,6 +269,23 @@ __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, 
     if (quad == 0) {
         to.m[wave][col] = m;
         to.l[wave][col] = l;
+    }
+}
+
+// A block's keys [lo, hi) (lo a multiple of 16 if pages are to be read 16 keys
+// at a time), dealt to its waves in steps, or, if they make no more than a
+// step of each, in equal shares of whole blocks of 16 (37 keys x 64: 7.0 ->
+// 5.7 us, all four waves at work).
+template <class T, int DP, bool WIDE, class Keys>
+__device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, int limit, float scale, int lo, int hi, Keys keys,
+                                            Joined &to)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (hi - lo <= kWaves * row_step<DP>()) {
+        const int share = (hi - lo + 16 * kWaves - 1) / (16 * kWaves) * 16, kb = lo + wave * share, end = min(hi, kb + share);
+        attend_share<T, DP, WIDE, true>(q, q_wide, D, min(limit, end), scale, kb, end, keys, to);
+    } else {
+        attend_share<T, DP, WIDE, false>(q, q_wide, D, min(limit, hi), scale, lo + wave * row_step<DP>(), hi, keys, to);
     }
 }
 
@@ -329,7 +354,7 @@ template <class T, int DP, bool WIDE>
 __global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs a, Partials to)
 {
     __shared__ Joined sh;
-    constexpr int kUnit = 16 * (DP == 128 ? 2 : 4);
+    constexpr int kUnit = row_step<DP>();
     // The rows that see most first.  Heads vary fastest: blocks go round the
     // eight XCDs, so a head's keys are read by few of them.
     const int g = a.Hq / a.Hkv, kh = blockIdx.x % a.Hkv, part = blockIdx.y;
@@ -378,7 +403,7 @@ template <class T, int DP, bool WIDE>
 __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs a, DecodeParts c)
 {
     __shared__ Joined sh;
-    constexpr int kUnit = kWaves * (DP == 128 ? 32 : 64);
+    constexpr int kUnit = kWaves * row_step<DP>();
     const int g = a.Hq / a.Hkv, kh = blockIdx.y;
     const int shared_len = c.own_from;
     int id = blockIdx.x;
@@ -609,12 +634,12 @@ hipError_t join(const Args &a, const Partials &from, int64_t rows, hipStream_t s
     return hipGetLastError();
 }
 
-// Parts are made until the grid has `blocks` blocks (of 4 waves), of at least
-// one step of all waves each.
+// Parts are made until the grid has `target` blocks (of 4 waves), of a step
+// of all waves each (a little more than one makes no parts).
 constexpr int64_t kDecodeBlocks = 512, kPromptBlocks = 256;
 int key_parts(int64_t keys, int64_t unit, int64_t blocks, int64_t target)
 {
-    const int64_t most = ceil_div(keys, unit), want = target / (blocks ? blocks : 1);
+    const int64_t most = 4 * keys <= 5 * unit ? 1 : ceil_div(keys, unit), want = target / (blocks ? blocks : 1);
     return (int)(want <= 1 || most <= 1 ? 1 : most < want ? most : want);
 }
 int64_t wave_step(int64_t D) { return D <= 64 ? 64 : 32; }
