@@ -214,14 +214,26 @@ __device__ __forceinline__ void copy_piece(const PageShape &g, int src, int dst,
         if (off[e] >= 0) *reinterpret_cast<V *>(to + off[e]) = x[e];
 }
 
+// Table entries to be made beside the copies, by the first blocks of their
+// launch (of their own they took 2 to 4 us of a fork's or a compaction's).
+struct NoTables {
+    __device__ __forceinline__ void operator()(int64_t) const {}
+};
+
 // Pairs (src, dst), each cut into 2 * pieces pieces (K, then V); pairs with
 // an id outside the pool are passed over.  `count`: how many pairs (null: n).
-template <class V>
+// Blocks below `table_blocks` make the `entries` table entries instead.
+template <class V, class Tables>
 __global__ __launch_bounds__(256) void cache_copy_kernel(PageShape g, const int32_t *src, const int32_t *dst, int n,
-                                                         const int32_t *count, int P, int64_t pieces)
+                                                         const int32_t *count, int P, int64_t pieces, Tables tables,
+                                                         int64_t entries, unsigned table_blocks)
 {
+    if (blockIdx.x < table_blocks) {
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < entries; i += (int64_t)table_blocks * 256) tables(i);
+        return;
+    }
     const int64_t units = (int64_t)(count ? *count : n) * 2 * pieces;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    for (int64_t u = blockIdx.x - table_blocks; u < units; u += gridDim.x - table_blocks) {
         const int64_t i = u / (2 * pieces);
         const int a = src[i], b = dst[i];
         if (a < 0 || b < 0 || a >= P || b >= P) continue;
@@ -253,31 +265,38 @@ PageShape page_shape(const Pool &p)
     return g;
 }
 
+template <class Tables>
 hipError_t launch_copy(const Pool &pool, const int32_t *src, const int32_t *dst, int n, const int32_t *count,
-                       hipStream_t stream)
+                       const Tables &tables, int64_t entries, hipStream_t stream)
 {
-    if (n == 0 || pool.Hkv == 0 || pool.D == 0) return hipSuccess;
-    const PageShape g = page_shape(pool);
-    const int64_t pieces = (g.vecs * g.rows + 1023) / 1024;
-    const int64_t units = (int64_t)n * 2 * pieces;
-    const unsigned blocks = (unsigned)(units < 16384 ? units : 16384);
+    const unsigned table_blocks = (unsigned)(entries < 256 * 4096 ? (entries + 255) / 256 : 4096);
+    if (pool.Hkv == 0 || pool.D == 0) n = 0;
+    PageShape g = {};
+    g.vec_bytes = 16;
+    if (n > 0) g = page_shape(pool);
+    const int64_t pieces = n > 0 ? (g.vecs * g.rows + 1023) / 1024 : 0, units = (int64_t)n * 2 * pieces;
+    const unsigned blocks = (unsigned)(units < 16384 ? units : 16384) + table_blocks;
+    if (blocks == 0) return hipSuccess;
+#define CFP32_COPY(V) \
+    cache_copy_kernel<V><<<blocks, 256, 0, stream>>>(g, src, dst, n, count, pool.P, pieces, tables, entries, table_blocks)
     switch (g.vec_bytes) {
-    case 16: cache_copy_kernel<uint4><<<blocks, 256, 0, stream>>>(g, src, dst, n, count, pool.P, pieces); break;
-    case 8: cache_copy_kernel<uint2><<<blocks, 256, 0, stream>>>(g, src, dst, n, count, pool.P, pieces); break;
-    case 4: cache_copy_kernel<uint32_t><<<blocks, 256, 0, stream>>>(g, src, dst, n, count, pool.P, pieces); break;
-    default: cache_copy_kernel<uint16_t><<<blocks, 256, 0, stream>>>(g, src, dst, n, count, pool.P, pieces); break;
+    case 16: CFP32_COPY(uint4); break;
+    case 8: CFP32_COPY(uint2); break;
+    case 4: CFP32_COPY(uint32_t); break;
+    default: CFP32_COPY(uint16_t); break;
     }
+#undef CFP32_COPY
     return hipGetLastError();
 }
 
 // Children's tables, and the counts of the pages they share.
-__global__ __launch_bounds__(256) void cache_fork_tables_kernel(const int32_t *table, int64_t ld, const int32_t *lens_out,
-                                                                const int32_t *parents, const int32_t *dst,
-                                                                int32_t *table_out, int64_t ld_out, int32_t *refs_out,
-                                                                int S, int W, int C, int P, int lg)
-{
-    const int64_t n = (int64_t)C * W;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+struct ForkTables {
+    const int32_t *table, *lens_out, *parents, *dst;
+    int32_t *table_out, *refs_out;
+    int64_t ld, ld_out;
+    int W, P, lg;
+    __device__ __forceinline__ void operator()(int64_t i) const
+    {
         const int64_t c = i / W, j = i - c * W;
         const int whole = lens_out[c] >> lg;
         int e = -1;
@@ -289,7 +308,21 @@ __global__ __launch_bounds__(256) void cache_fork_tables_kernel(const int32_t *t
         }
         table_out[c * ld_out + j] = e;
     }
-}
+};
+
+// Tables after a compaction.
+struct MovedTables {
+    const int32_t *table, *map;
+    int32_t *table_out;
+    int64_t ld, ld_out;
+    int W, P;
+    __device__ __forceinline__ void operator()(int64_t i) const
+    {
+        const int64_t s = i / W, j = i - s * W;
+        const int e = table[s * ld + j];
+        table_out[s * ld_out + j] = e >= 0 && e < P ? map[e] : e;
+    }
+};
 
 // ---- Writing tokens --------------------------------------------------------------
 
@@ -310,8 +343,6 @@ __global__ __launch_bounds__(256) void cache_append_kernel(HeadsView k, HeadsVie
                                                            const int32_t *lens, int32_t *lens_out, Pool pool,
                                                            const int32_t *table, int64_t ld, int S, int W, int T)
 {
-    typedef float in_t __attribute__((ext_vector_type(E)));
-    typedef Out out_t __attribute__((ext_vector_type(E)));
     const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
     for (int64_t s = first; s < S; s += step) lens_out[s] = lens[s] + (cu[s + 1] - cu[s]);
     const int per = pool.D / E;
@@ -328,10 +359,26 @@ __global__ __launch_bounds__(256) void cache_append_kernel(HeadsView k, HeadsVie
         const int page = table[s * ld + j];
         if (page < 0 || page >= pool.P) continue;
         const int64_t o = pos & (((int64_t)1 << pool.page_log2) - 1);
+        // In pieces of 16 bytes at most, which is what the pointers are aligned to.
         auto put = [&](const HeadsView &x, const PagesView &to) {
-            const in_t a = *reinterpret_cast<const in_t *>((const float *)x.data + t * x.tok + h * x.head + d);
-            *reinterpret_cast<out_t *>((Out *)to.data + page * to.page + h * to.head + o * to.tok + d) =
-                __builtin_convertvector(a, out_t);
+            constexpr int IN = E < 4 ? E : 4, OUT = E < 16 / (int)sizeof(Out) ? E : 16 / (int)sizeof(Out);
+            typedef float in_piece __attribute__((ext_vector_type(IN)));
+            typedef Out out_piece __attribute__((ext_vector_type(OUT)));
+            float a[E];
+#pragma unroll
+            for (int e = 0; e < E; e += IN) {
+                const in_piece p = *reinterpret_cast<const in_piece *>((const float *)x.data + t * x.tok + h * x.head + d + e);
+#pragma unroll
+                for (int u = 0; u < IN; ++u) a[e + u] = p[u];
+            }
+            Out *out = (Out *)to.data + page * to.page + h * to.head + o * to.tok + d;
+#pragma unroll
+            for (int e = 0; e < E; e += OUT) {
+                out_piece p;
+#pragma unroll
+                for (int u = 0; u < OUT; ++u) p[u] = (Out)a[e + u];
+                *reinterpret_cast<out_piece *>(out + e) = p;
+            }
         };
         put(k, pool.k);
         put(v, pool.v);
@@ -355,6 +402,23 @@ __global__ __launch_bounds__(256) void cache_free_kernel(const int32_t *rows, in
         const int e = rows[r * ld + (i - r * W)];
         if (e >= 0 && e < P) atomicSub(&refs_out[e], 1);
     }
+}
+
+// The same of a small pool in one launch: what is given up is counted in LDS.
+constexpr int kSmallPool = 16384;
+__global__ __launch_bounds__(kPlanThreads) void cache_free_small_kernel(const int32_t *rows, int64_t ld, const int32_t *refs,
+                                                                        int32_t *refs_out, int R, int W, int P)
+{
+    __shared__ int gone[kSmallPool];
+    for (int i = threadIdx.x; i < P; i += kPlanThreads) gone[i] = 0;
+    __syncthreads();
+    const int n = R * W;
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+        const int r = i / W, e = rows[r * ld + (i - r * W)];
+        if (e >= 0 && e < P) atomicAdd(&gone[e], 1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < P; i += kPlanThreads) refs_out[i] = refs[i] - gone[i];
 }
 
 // map[p]: where page p goes (itself unless it moves); src/dst: the moves; *moves: how many.
@@ -401,18 +465,6 @@ __global__ __launch_bounds__(kPlanThreads) void cache_compact_plan_kernel(const 
     }
 }
 
-__global__ __launch_bounds__(256) void cache_remap_kernel(const int32_t *table, int64_t ld, const int32_t *refs_out,
-                                                          const int32_t *map, const int32_t *live, int32_t *table_out,
-                                                          int64_t ld_out, int S, int W, int P)
-{
-    const int64_t n = (int64_t)S * W;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t s = i / W, j = i - s * W;
-        const int e = table[s * ld + j];
-        table_out[s * ld_out + j] = e >= 0 && e < P ? map[e] : e;
-    }
-}
-
 unsigned grid_for(int64_t n) { return (unsigned)(n <= 0 ? 1 : (n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192); }
 
 }  // namespace
@@ -434,16 +486,19 @@ hipError_t launch_cache_append(const HeadsView &k, const HeadsView &v, const int
     const int64_t in = (int64_t)((uintptr_t)k.data | (uintptr_t)v.data) | 4 * (k.tok | k.head | v.tok | v.head);
     const int64_t to = (int64_t)((uintptr_t)pool.k.data | (uintptr_t)pool.v.data) |
                        eb * (pool.k.page | pool.k.head | pool.k.tok | pool.v.page | pool.v.head | pool.v.tok);
-    const bool wide = pool.D % 4 == 0 && in % 16 == 0 && to % (4 * eb) == 0;
-    const int64_t n = (int64_t)T * pool.Hkv * (pool.D / (wide ? 4 : 1));
+    // Elements of a thread: 32 bytes of FP32 in, and 16 or 32 out.
+    const bool wide = pool.D % 8 == 0 && in % 16 == 0 && to % 16 == 0, four = pool.D % 4 == 0 && in % 16 == 0 && to % (4 * eb) == 0;
+    const int64_t n = (int64_t)T * pool.Hkv * (pool.D / (wide ? 8 : four ? 4 : 1));
     const unsigned blocks = grid_for(n > S ? n : S);
 #define CFP32_APPEND(OUT, E) \
     cache_append_kernel<OUT, E><<<blocks, 256, 0, stream>>>(k, v, cu, lens, lens_out, pool, table, ld, S, W, T)
     if (pool.elem_bytes == 2) {
-        if (wide) CFP32_APPEND(_Float16, 4);
+        if (wide) CFP32_APPEND(_Float16, 8);
+        else if (four) CFP32_APPEND(_Float16, 4);
         else CFP32_APPEND(_Float16, 1);
     } else {
-        if (wide) CFP32_APPEND(float, 4);
+        if (wide) CFP32_APPEND(float, 8);
+        else if (four) CFP32_APPEND(float, 4);
         else CFP32_APPEND(float, 1);
     }
 #undef CFP32_APPEND
@@ -452,7 +507,7 @@ hipError_t launch_cache_append(const HeadsView &k, const HeadsView &v, const int
 
 hipError_t launch_cache_copy_pages(const Pool &pool, const int32_t *src, const int32_t *dst, int n, hipStream_t stream)
 {
-    return launch_copy(pool, src, dst, n, nullptr, stream);
+    return launch_copy(pool, src, dst, n, nullptr, NoTables{}, 0, stream);
 }
 
 hipError_t launch_cache_fork(const Pool &pool, const int32_t *table, int64_t ld, const int32_t *lens,
@@ -465,17 +520,17 @@ hipError_t launch_cache_fork(const Pool &pool, const int32_t *table, int64_t ld,
                                                            S, W, C, pool.P, pool.page_log2, src, dst);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || C == 0) return e;
-    cache_fork_tables_kernel<<<grid_for((int64_t)C * W), 256, 0, stream>>>(table, ld, lens_out, parents, dst, table_out,
-                                                                           ld_out, refs_out, S, W, C, pool.P,
-                                                                           pool.page_log2);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    return launch_copy(pool, src, dst, C, nullptr, stream);
+    const ForkTables tables = {table, lens_out, parents, dst, table_out, refs_out, ld, ld_out, W, pool.P, pool.page_log2};
+    return launch_copy(pool, src, dst, C, nullptr, tables, (int64_t)C * W, stream);
 }
 
 hipError_t launch_cache_free(const int32_t *rows, int64_t ld, const int32_t *refs, int32_t *refs_out, int R, int W,
                              int P, hipStream_t stream)
 {
+    if (P <= kSmallPool && (int64_t)R * W <= 65536) {
+        cache_free_small_kernel<<<1, kPlanThreads, 0, stream>>>(rows, ld, refs, refs_out, R, W, P);
+        return hipGetLastError();
+    }
     if (refs != refs_out) {
         cache_counts_kernel<<<(P + 255) / 256, 256, 0, stream>>>(refs, refs_out, P);
         const hipError_t e = hipGetLastError();
@@ -494,13 +549,8 @@ hipError_t launch_cache_compact(const Pool &pool, const int32_t *table, int64_t 
     cache_compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(refs, refs_out, live, pool.P, map, src, dst, moves);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if ((int64_t)S * W > 0) {
-        cache_remap_kernel<<<grid_for((int64_t)S * W), 256, 0, stream>>>(table, ld, refs_out, map, live, table_out,
-                                                                         ld_out, S, W, pool.P);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return launch_copy(pool, src, dst, pool.P / 2, moves, stream);
+    const MovedTables tables = {table, map, table_out, ld, ld_out, W, pool.P};
+    return launch_copy(pool, src, dst, pool.P / 2, moves, tables, (int64_t)S * W, stream);
 }
 
 }  // namespace cfp32
