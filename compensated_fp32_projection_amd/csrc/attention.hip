@@ -25,7 +25,6 @@ namespace cfp32 {
 
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kRows = 16;
 
 // Where a block's keys are: packed rows, ...
@@ -89,9 +88,10 @@ __device__ __forceinline__ void load_row(const char *p, int at, int n, T (&x)[N]
     }
 }
 
+template <int DP, int NW>
 struct Joined {
-    float o[kWaves][kRows][kAttnMaxDim + 4];
-    float m[kWaves][kRows], l[kWaves][kRows];
+    float o[NW][kRows][DP + 4];
+    float m[NW][kRows], l[NW][kRows];
     int unfinished[kRows];
 };
 
@@ -99,11 +99,11 @@ template <int DP>
 constexpr int row_step() { return DP == 128 ? 32 : 64; }  // keys a wave takes at a time
 
 // One wave's share of 16 rows: this lane's row q sees the first `limit` keys;
-// the wave takes keys [kb, hi), row_step at a time, kWaves steps further each
+// the wave takes keys [kb, hi), row_step at a time, NW steps further each
 // time.  FEW: there is one step, of which blocks of 16 keys may be missing.
-template <class T, int DP, bool WIDE, bool FEW, class Keys>
+template <class T, int DP, bool WIDE, int NW, bool FEW, class Keys>
 __device__ __forceinline__ void attend_share(const float *q, bool q_wide, int D, int limit, float scale, int kb, int hi, Keys keys,
-                                             Joined &to)
+                                             Joined<DP, NW> &to)
 {
     constexpr bool F16 = sizeof(T) == 2;
     constexpr int kStep = row_step<DP>(), NB = kStep / 16;
@@ -155,7 +155,7 @@ __device__ __forceinline__ void attend_share(const float *q, bool q_wide, int D,
         pages(kb, page);
         load_k(kb);
         load_v(kb);
-        if (!FEW) pages(kb + kWaves * kStep, next);
+        if (!FEW) pages(kb + NW * kStep, next);
 
         // The row, as the right operand of the score products.
         float f = scale * kLog2e;
@@ -204,13 +204,13 @@ __device__ __forceinline__ void attend_share(const float *q, bool q_wide, int D,
                     }
                 }
             }
-            const int nb = kb + kWaves * kStep;
+            const int nb = kb + NW * kStep;
             const bool more = !FEW && nb < hi;
             if (more) {
                 // The next step's pages are known; ask for those after it first.
 #pragma unroll
                 for (int b = 0; b < NB; ++b) page[b] = next[b];
-                if (nb + kWaves * kStep < hi) pages(nb + kWaves * kStep, next);
+                if (nb + NW * kStep < hi) pages(nb + NW * kStep, next);
                 load_k(nb);
             }
             float mx = -INFINITY;
@@ -276,34 +276,33 @@ __device__ __forceinline__ void attend_share(const float *q, bool q_wide, int D,
 // at a time), dealt to its waves in steps, or, if they make no more than a
 // step of each, in equal shares of whole blocks of 16 (37 keys x 64: 7.0 ->
 // 5.7 us, all four waves at work).
-template <class T, int DP, bool WIDE, class Keys>
+template <class T, int DP, bool WIDE, int NW, class Keys>
 __device__ __forceinline__ void attend_rows(const float *q, bool q_wide, int D, int limit, float scale, int lo, int hi, Keys keys,
-                                            Joined &to)
+                                            Joined<DP, NW> &to)
 {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (hi - lo <= kWaves * row_step<DP>()) {
-        const int share = (hi - lo + 16 * kWaves - 1) / (16 * kWaves) * 16, kb = lo + wave * share, end = min(hi, kb + share);
-        attend_share<T, DP, WIDE, true>(q, q_wide, D, min(limit, end), scale, kb, end, keys, to);
+    if (hi - lo <= NW * row_step<DP>()) {
+        const int share = (hi - lo + 16 * NW - 1) / (16 * NW) * 16, kb = lo + wave * share, end = min(hi, kb + share);
+        attend_share<T, DP, WIDE, NW, true>(q, q_wide, D, min(limit, end), scale, kb, end, keys, to);
     } else {
-        attend_share<T, DP, WIDE, false>(q, q_wide, D, min(limit, hi), scale, lo + wave * row_step<DP>(), hi, keys, to);
+        attend_share<T, DP, WIDE, NW, false>(q, q_wide, D, min(limit, hi), scale, lo + wave * row_step<DP>(), hi, keys, to);
     }
 }
 
-// The waves' sums of row threadIdx.x / 16 joined: m, l and this thread's DP /
-// 16 values (unnormalised).
-template <int DP>
-__device__ __forceinline__ void join_rows(const Joined &from, float &m, float &l, float (&x)[DP / 16])
+// The waves' sums of a row joined: m, l and DP / 16 values from d0 on
+// (unnormalised).
+template <int DP, int NW>
+__device__ __forceinline__ void join_rows(const Joined<DP, NW> &from, int row, int d0, float &m, float &l, float (&x)[DP / 16])
 {
     constexpr int NV = DP / 16;
-    const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * NV;
     m = from.m[0][row];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, from.m[w][row]);
+    for (int w = 1; w < NW; ++w) m = fmaxf(m, from.m[w][row]);
     l = 0.0f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) x[c] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < NW; ++w) {
         const float mw = from.m[w][row], f = mw == -INFINITY ? 0.0f : exp2_raw(mw - m);
         l = fmaf(f, from.l[w][row], l);
 #pragma unroll
@@ -313,13 +312,13 @@ __device__ __forceinline__ void join_rows(const Joined &from, float &m, float &l
 
 // A row's sums, of what this block has seen: into its slot, or (all there is)
 // as its result.  Results that are not finite are marked.
-template <int DP>
-__device__ __forceinline__ void leave_row(Joined &sh, const Partials &to, int64_t slot, float *out, int D, bool live)
+template <int DP, int NW>
+__device__ __forceinline__ void leave_row(Joined<DP, NW> &sh, const Partials &to, int64_t slot, float *out, int D, bool live)
 {
-    float m, l, x[DP / 16];
-    join_rows<DP>(sh, m, l, x);
     if (!live) return;
     const int row = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (DP / 16);
+    float m, l, x[DP / 16];
+    join_rows(sh, row, d0, m, l, x);
     if (to.o) {
         if ((threadIdx.x & 15) == 0) {
             to.m[slot] = m;
@@ -350,10 +349,10 @@ __device__ __forceinline__ void part_range(int lo, int hi, int part, int parts, 
     b = lo + (int)min((int64_t)n, (int64_t)(part + 1) * per * unit);
 }
 
-template <class T, int DP, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs a, Partials to)
+template <class T, int DP, bool WIDE, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void prompt_rows_kernel(PromptArgs a, Partials to)
 {
-    __shared__ Joined sh;
+    __shared__ Joined<DP, NW> sh;
     constexpr int kUnit = row_step<DP>();
     // The rows that see most first.  Heads vary fastest: blocks go round the
     // eight XCDs, so a head's keys are read by few of them.
@@ -367,24 +366,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs 
     const int64_t r0 = (id - start) * kRows;
     const int live = (int)min((int64_t)kRows, n - r0);
     const int64_t r = r0 + min((int)(threadIdx.x & 15), live - 1);
-    const int i = (int)(r / g), h = kh * g + (int)(r - (int64_t)i * g);
+    const int i = (int)over(r, g), h = kh * g + (int)(r - (int64_t)i * g);
     const PackedKeys keys = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                              (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                              a.k.tok * (int64_t)sizeof(T), a.v.tok * (int64_t)sizeof(T)};
     int lo, hi;
-    part_range(0, sq.limit((int)((r0 + live - 1) / g)), part, to.slots, kUnit, lo, hi);
-    attend_rows<T, DP, WIDE>((const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head,
+    part_range(0, sq.limit((int)over(r0 + live - 1, g)), part, to.slots, kUnit, lo, hi);
+    attend_rows<T, DP, WIDE, NW>((const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head,
                              rows_wide(a.q.data, a.q.tok | a.q.head, a.D), a.D, sq.limit(i), a.scale, lo, hi, keys, sh);
     if (threadIdx.x < kRows) sh.unfinished[threadIdx.x] = 0;
     __syncthreads();
-    const int row = threadIdx.x >> 4, ri = (int)((r0 + row) / g), rh = kh * g + (int)(r0 + row - (int64_t)ri * g);
-    leave_row<DP>(sh, to, ((int64_t)(sq.q0 + ri) * a.Hq + rh) * to.slots + part,
+    const int row = threadIdx.x >> 4, ri = (int)over(r0 + row, g), rh = kh * g + (int)(r0 + row - (int64_t)ri * g);
+    leave_row(sh, to, ((int64_t)(sq.q0 + ri) * a.Hq + rh) * to.slots + part,
                   a.out + (sq.q0 + ri) * a.out_tok + rh * a.out_head, a.D, row < live);
     if (to.o) return;
     __syncthreads();
-    for (int w = threadIdx.x >> 6; w < live; w += kWaves)
+    for (int w = threadIdx.x >> 6; w < live; w += NW)
         if (sh.unfinished[w]) {
-            const int wi = (int)((r0 + w) / g);
+            const int wi = (int)over(r0 + w, g);
             attend_prompt_row<T>(a, sq, wi, kh * g + (int)(r0 + w - (int64_t)wi * g));
         }
 }
@@ -396,14 +395,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_rows_kernel(PromptArgs 
 struct DecodeParts {
     int shared, own, shared_groups, own_groups;
     int own_from;  // the first key that is not shared
+    bool eight;    // waves
     Partials to;  // slots: shared + own; null o: straight to the output
 };
 
-template <class T, int DP, bool WIDE>
-__global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs a, DecodeParts c)
+template <class T, int DP, bool WIDE, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void decode_rows_kernel(DecodeArgs a, DecodeParts c)
 {
-    __shared__ Joined sh;
-    constexpr int kUnit = kWaves * row_step<DP>();
+    __shared__ Joined<DP, NW> sh;
+    constexpr int kUnit = NW * row_step<DP>();
     const int g = a.Hq / a.Hkv, kh = blockIdx.y;
     const int shared_len = c.own_from;
     int id = blockIdx.x;
@@ -415,7 +415,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs 
     const int64_t end = common ? (int64_t)a.B * g : (int64_t)(group / c.own_groups + 1) * g;
     const int live = (int)min((int64_t)kRows, end - r0);
     const int64_t r = r0 + min((int)(threadIdx.x & 15), live - 1);
-    const int64_t b = r / g;
+    const int64_t b = over(r, g);
     const int h = kh * g + (int)(r - b * g);
     const int n = decode_length(a, (int)b);
     int lo, hi;
@@ -434,20 +434,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void decode_rows_kernel(DecodeArgs 
                             a.k.page * (int64_t)sizeof(T), a.v.page * (int64_t)sizeof(T),
                             a.k.tok * (int64_t)sizeof(T), a.v.tok * (int64_t)sizeof(T),
                             a.table + (common ? 0 : b * a.ld_table), a.page_log2, a.P, 0x7FFFFFFF};
-    attend_rows<T, DP, WIDE>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, common ? min(n, shared_len) : n, a.scale, lo, hi, keys,
+    attend_rows<T, DP, WIDE, NW>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, common ? min(n, shared_len) : n, a.scale, lo, hi, keys,
                              sh);
     if (threadIdx.x < kRows) sh.unfinished[threadIdx.x] = 0;
     __syncthreads();
     const int row = threadIdx.x >> 4;
-    const int64_t rb = (r0 + row) / g;
+    const int64_t rb = over(r0 + row, g);
     const int rh = kh * g + (int)(r0 + row - rb * g);
-    leave_row<DP>(sh, c.to, (rb * a.Hq + rh) * c.to.slots + (common ? part : c.to.slots - c.own + part),
+    leave_row(sh, c.to, (rb * a.Hq + rh) * c.to.slots + (common ? part : c.to.slots - c.own + part),
                   a.out + rb * a.out_seq + rh * a.out_head, a.D, row < live);
     if (c.to.o) return;
     __syncthreads();
-    for (int w = threadIdx.x >> 6; w < live; w += kWaves)
+    for (int w = threadIdx.x >> 6; w < live; w += NW)
         if (sh.unfinished[w]) {
-            const int64_t wb = (r0 + w) / g;
+            const int64_t wb = over(r0 + w, g);
             attend_decode_row<T>(a, wb, kh * g + (int)(r0 + w - wb * g));
         }
 }
@@ -576,25 +576,31 @@ bool wide(const void *p, int64_t strides, int D, bool f16)
 
 }  // namespace
 
-#define CFP32_BY_TYPE(KERNEL, F16, D, WIDE, GRID, BLOCK, ...)                                           \
-    do {                                                                                              \
-        if (F16) {                                                                                    \
-            if ((D) <= 64) {                                                                          \
-                if (WIDE) KERNEL<_Float16, 64, true><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);        \
-                else KERNEL<_Float16, 64, false><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);            \
-            } else {                                                                                  \
-                if (WIDE) KERNEL<_Float16, 128, true><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);       \
-                else KERNEL<_Float16, 128, false><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);           \
-            }                                                                                         \
-        } else {                                                                                      \
-            if ((D) <= 64) {                                                                          \
-                if (WIDE) KERNEL<float, 64, true><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);           \
-                else KERNEL<float, 64, false><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);               \
-            } else {                                                                                  \
-                if (WIDE) KERNEL<float, 128, true><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);          \
-                else KERNEL<float, 128, false><<<GRID, BLOCK, 0, stream>>>(__VA_ARGS__);              \
-            }                                                                                         \
-        }                                                                                             \
+// KERNEL<type, padded D, WIDE, waves>
+#define CFP32_BY_WAVES(KERNEL, T, DP, WIDE, EIGHT, GRID, ...)                                        \
+    do {                                                                                             \
+        if (EIGHT) KERNEL<T, DP, WIDE, 8><<<GRID, 512, 0, stream>>>(__VA_ARGS__);                    \
+        else KERNEL<T, DP, WIDE, 4><<<GRID, 256, 0, stream>>>(__VA_ARGS__);                          \
+    } while (0)
+#define CFP32_BY_TYPE(KERNEL, F16, D, WIDE, EIGHT, GRID, ...)                                        \
+    do {                                                                                             \
+        if (F16) {                                                                                   \
+            if ((D) <= 64) {                                                                         \
+                if (WIDE) CFP32_BY_WAVES(KERNEL, _Float16, 64, true, EIGHT, GRID, __VA_ARGS__);      \
+                else CFP32_BY_WAVES(KERNEL, _Float16, 64, false, EIGHT, GRID, __VA_ARGS__);          \
+            } else {                                                                                 \
+                if (WIDE) CFP32_BY_WAVES(KERNEL, _Float16, 128, true, EIGHT, GRID, __VA_ARGS__);     \
+                else CFP32_BY_WAVES(KERNEL, _Float16, 128, false, EIGHT, GRID, __VA_ARGS__);         \
+            }                                                                                        \
+        } else {                                                                                     \
+            if ((D) <= 64) {                                                                         \
+                if (WIDE) CFP32_BY_WAVES(KERNEL, float, 64, true, EIGHT, GRID, __VA_ARGS__);         \
+                else CFP32_BY_WAVES(KERNEL, float, 64, false, EIGHT, GRID, __VA_ARGS__);             \
+            } else {                                                                                 \
+                if (WIDE) CFP32_BY_WAVES(KERNEL, float, 128, true, EIGHT, GRID, __VA_ARGS__);        \
+                else CFP32_BY_WAVES(KERNEL, float, 128, false, EIGHT, GRID, __VA_ARGS__);            \
+            }                                                                                        \
+        }                                                                                            \
     } while (0)
 
 size_t partial_bytes(int64_t rows, int slots, int dim) { return slots > 1 ? (size_t)rows * slots * (dim + 2) * 4 : 0; }
@@ -644,10 +650,16 @@ int key_parts(int64_t keys, int64_t unit, int64_t blocks, int64_t target)
 }
 int64_t wave_step(int64_t D) { return D <= 64 ? 64 : 32; }
 
+// Blocks of eight waves where that makes their keys one step instead of two
+// (400 x 12 x 64 FP32 14.4 -> 12.5 us, 130 keys x 32/8 x 128 FP16 11.2 -> 9.3);
+// with more keys than that, or fewer, four are as good or better (500 x 16/2 x
+// 128 FP16 20 against 26 us).
+bool eight_waves(int64_t keys, int64_t D) { return keys > 4 * wave_step(D) && keys <= 8 * wave_step(D); }
+
 // How many parts the keys of a short prompt make: by the average sequence's.
 int prompt_parts(int64_t S, int64_t Tk, int64_t blocks, int64_t D)
 {
-    return key_parts(ceil_div(Tk, S), kWaves * wave_step(D), blocks, kPromptBlocks);
+    return key_parts(ceil_div(Tk, S), 4 * wave_step(D), blocks, kPromptBlocks);
 }
 
 // Which kernel a prompt goes through, by estimates in microseconds beyond what
@@ -696,9 +708,10 @@ hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStre
     const bool can = a.Tk > 0 && (!a.kv_f16 || (w && a.k.tok < ((int64_t)1 << 31) && a.v.tok < ((int64_t)1 << 31)));
     if (can && prefer_tiles(a, units)) return launch_prompt_tile(a, workspace, stream);
     Partials to = {nullptr, nullptr, nullptr, prompt_parts(a.S, a.Tk, units * a.Hkv, a.D), padded(a.D)};
+    const bool eight = eight_waves(ceil_div(a.Tk, (int64_t)a.S * to.slots), a.D);
     place_partials(to, rows, workspace);
     const dim3 grid((unsigned)(units * a.Hkv), (unsigned)to.slots);
-    CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, w, grid, 64 * kWaves, a, to);
+    CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, w, eight, grid, a, to);
     const hipError_t e = hipGetLastError();
     return e != hipSuccess || !to.o ? e : launch_join(a, to, stream);
 }
@@ -714,7 +727,7 @@ DecodeParts decode_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t 
                          int &tiled)
 {
     DecodeParts c = {};
-    const int64_t g = Hq / Hkv, unit = kWaves * wave_step(D);
+    const int64_t g = Hq / Hkv, unit = 4 * wave_step(D);
     const int64_t n_shared = B > 1 ? shared_pages << lg : 0, n_own = (W << lg) - n_shared;
     c.shared_groups = (int)ceil_div(B * g, kRows);
     c.own_groups = (int)ceil_div(g, kRows);
@@ -726,6 +739,7 @@ DecodeParts decode_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t 
     }
     if (n_own > 0) c.own = key_parts(n_own, unit, B * c.own_groups * Hkv, kDecodeBlocks);
     if (tiled + c.shared + c.own == 0) c.own = 1;
+    c.eight = c.shared == 0 && c.own == 1 && eight_waves(n_own, D);
     c.to.slots = tiled + c.shared + c.own;
     if (tiled && c.to.slots == 1) c.to.slots = 2;  // always by way of slots; the second is an empty part
     if (tiled && c.own == 0) c.own = c.to.slots - tiled;
@@ -767,9 +781,12 @@ hipError_t launch_attention_decode(const DecodeArgs &a, void *workspace, hipStre
         const hipError_t e = launch_decode_tile(a, c.to, tiled, stream);
         if (e != hipSuccess) return e;
     }
-    const dim3 grid((unsigned)blocks, (unsigned)a.Hkv);
-    CFP32_BY_TYPE(decode_rows_kernel, a.kv_f16, a.D, w, grid, 64 * kWaves, a, c);
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipSuccess;
+    if (blocks) {  // none where every key is shared and goes through tiles
+        const dim3 grid((unsigned)blocks, (unsigned)a.Hkv);
+        CFP32_BY_TYPE(decode_rows_kernel, a.kv_f16, a.D, w, c.eight, grid, a, c);
+        e = hipGetLastError();
+    }
     return e != hipSuccess || !c.to.o ? e : launch_join(a, c.to, stream);
 }
 

@@ -15,6 +15,13 @@ __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp
 // steps leave the sums as they are.
 constexpr float kLazy = 4.0f;
 
+// a / b for 0 <= a, in 32 bits where they do (a 64-bit division costs a
+// thread half a microsecond).
+__device__ __forceinline__ int64_t over(int64_t a, int b)
+{
+    return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // The sequence that owns unit `id` of a packed batch, where sequence s starts
 // at unit cu[s] * mul / div + s (so sequences of n tokens own up to
 // ceil(n * mul / div) units, and some units belong to none).

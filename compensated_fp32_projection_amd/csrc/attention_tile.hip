@@ -485,9 +485,9 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     if (id < start || r0 >= n) return;
     const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
-    const int i = (int)(r / g), h = kh * g + (int)(r - (int64_t)i * g);
+    const int i = (int)over(r, g), h = kh * g + (int)(r - (int64_t)i * g);
     const bool rows = first < n;
-    const int keys = sq.limit((int)((min(r0 + kBlockRows, n) - 1) / g));
+    const int keys = sq.limit((int)over(min(r0 + kBlockRows, n) - 1, g));
     const int limit = sq.limit(i);
     const float *q = (const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head;
     const bool q_wide = rows_wide(a.q.data, a.q.tok | a.q.head, a.D);
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     redo = (redo | redo >> 32) & 0xFFFFFFFFull;
     for (; redo; redo &= redo - 1) {
         const int64_t rr = first + __builtin_ctzll(redo);
-        const int ri = (int)(rr / g);
+        const int ri = (int)over(rr, g);
         attend_prompt_row<T>(a, sq, ri, kh * g + (int)(rr - (int64_t)ri * g));
     }
 }
@@ -550,7 +550,7 @@ __global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Parti
     const int64_t n = (int64_t)a.B * g, r0 = (int64_t)(blockIdx.x / parts / a.Hkv) * 128;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
-    const int64_t b = r / g;
+    const int64_t b = over(r, g);
     const int h = kh * g + (int)(r - b * g);
     const int shared = a.shared_pages << a.page_log2;
     const int limit = min(decode_length(a, (int)b), shared);
