@@ -188,6 +188,12 @@ struct PageShape {
     int vec_bytes;
 };
 
+typedef uint32_t vec4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t vec2_t __attribute__((ext_vector_type(2)));
+
+// Non-temporal: what is moved is not read again soon, and as ordinary loads
+// and stores it went through the L2s at two thirds of the speed (compaction
+// of 1024 pages of 256 KiB 37 -> 25 us, fork of 256 35 -> 29).
 template <class V>
 __device__ __forceinline__ void copy_piece(const PageShape &g, int src, int dst, int64_t piece, int64_t pieces)
 {
@@ -206,12 +212,12 @@ __device__ __forceinline__ void copy_piece(const PageShape &g, int src, int dst,
         if (u < total) {
             const int64_t r = g.rows == 1 ? 0 : u / g.vecs, i = u - r * g.vecs;
             off[e] = (g.rows == 1 ? 0 : r / g.n2 * t.s1 + r % g.n2 * t.s2) + i * (int64_t)sizeof(V);
-            x[e] = *reinterpret_cast<const V *>(from + off[e]);
+            x[e] = __builtin_nontemporal_load(reinterpret_cast<const V *>(from + off[e]));
         }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (off[e] >= 0) *reinterpret_cast<V *>(to + off[e]) = x[e];
+        if (off[e] >= 0) __builtin_nontemporal_store(x[e], reinterpret_cast<V *>(to + off[e]));
 }
 
 // Table entries to be made beside the copies, by the first blocks of their
@@ -280,8 +286,8 @@ hipError_t launch_copy(const Pool &pool, const int32_t *src, const int32_t *dst,
 #define CFP32_COPY(V) \
     cache_copy_kernel<V><<<blocks, 256, 0, stream>>>(g, src, dst, n, count, pool.P, pieces, tables, entries, table_blocks)
     switch (g.vec_bytes) {
-    case 16: CFP32_COPY(uint4); break;
-    case 8: CFP32_COPY(uint2); break;
+    case 16: CFP32_COPY(vec4_t); break;
+    case 8: CFP32_COPY(vec2_t); break;
     case 4: CFP32_COPY(uint32_t); break;
     default: CFP32_COPY(uint16_t); break;
     }
@@ -359,7 +365,8 @@ __global__ __launch_bounds__(256) void cache_append_kernel(HeadsView k, HeadsVie
         const int page = table[s * ld + j];
         if (page < 0 || page >= pool.P) continue;
         const int64_t o = pos & (((int64_t)1 << pool.page_log2) - 1);
-        // In pieces of 16 bytes at most, which is what the pointers are aligned to.
+        // In pieces of 16 bytes at most, which is what the pointers are aligned
+        // to; non-temporal (4 x 2048 tokens 29 -> 26 us).
         auto put = [&](const HeadsView &x, const PagesView &to) {
             constexpr int IN = E < 4 ? E : 4, OUT = E < 16 / (int)sizeof(Out) ? E : 16 / (int)sizeof(Out);
             typedef float in_piece __attribute__((ext_vector_type(IN)));
@@ -367,7 +374,7 @@ __global__ __launch_bounds__(256) void cache_append_kernel(HeadsView k, HeadsVie
             float a[E];
 #pragma unroll
             for (int e = 0; e < E; e += IN) {
-                const in_piece p = *reinterpret_cast<const in_piece *>((const float *)x.data + t * x.tok + h * x.head + d + e);
+                const in_piece p = __builtin_nontemporal_load(reinterpret_cast<const in_piece *>((const float *)x.data + t * x.tok + h * x.head + d + e));
 #pragma unroll
                 for (int u = 0; u < IN; ++u) a[e + u] = p[u];
             }
@@ -377,7 +384,7 @@ __global__ __launch_bounds__(256) void cache_append_kernel(HeadsView k, HeadsVie
                 out_piece p;
 #pragma unroll
                 for (int u = 0; u < OUT; ++u) p[u] = (Out)a[e + u];
-                *reinterpret_cast<out_piece *>(out + e) = p;
+                __builtin_nontemporal_store(p, reinterpret_cast<out_piece *>(out + e));
             }
         };
         put(k, pool.k);
