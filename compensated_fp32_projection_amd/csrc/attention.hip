@@ -718,9 +718,18 @@ hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStre
 
 namespace {
 
-// More rows than this share a prefix: its keys go through attention_tile.hip's
-// kernel (if the pages allow).
-constexpr int64_t kTileRows = 32;
+// Which kernel takes the keys that all sequences share: estimates in
+// microseconds, of this one by its groups of 16 rows, of attention_tile.hip's
+// by its blocks of 128.  Measured, this against that, FP16 pages: 32 x 32/8 x
+// 128 behind 1280 / 5120 / 20480 keys 33 / 50 / 112 against 35 / 39 / 58 us; 12
+// of these 18 / 33 / 63 against 27 / 31 / 46; 10 x 16/2 x 128 behind 5120 /
+// 20480 / 61440 18 / 34 / 67 against 29 / 34 / 47; 16 x 14/2 x 64 behind the
+// same 16 / 29 / 52 against 23 / 26 / 38.
+bool prefer_tiles(int64_t rows, int64_t Hkv, int64_t D, int64_t keys)
+{
+    const double k = 1e-3 * (double)keys * Hkv, groups = (double)ceil_div(rows, kRows), blocks = (double)ceil_div(rows, 128);
+    return D <= 64 ? 0.05 * groups * k > 10 + 0.13 * blocks * k : 0.1 * groups * k > 13 + 0.16 * blocks * k;
+}
 
 // `tiled`: the shared keys are cut for the other kernel, and c.shared is 0.
 DecodeParts decode_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int lg, int64_t shared_pages, bool tiles,
@@ -734,7 +743,7 @@ DecodeParts decode_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t 
     c.own_from = (int)n_shared;
     tiled = 0;
     if (n_shared) {
-        if (tiles && B * g > kTileRows) tiled = decode_tile_parts(B, Hq, Hkv, n_shared, lg);
+        if (tiles && prefer_tiles(B * g, Hkv, D, n_shared)) tiled = decode_tile_parts(B, Hq, Hkv, n_shared, lg);
         else c.shared = key_parts(n_shared, unit, c.shared_groups * Hkv, kDecodeBlocks);
     }
     if (n_own > 0) c.own = key_parts(n_own, unit, B * c.own_groups * Hkv, kDecodeBlocks);

@@ -233,3 +233,76 @@ def test_long_shared_prefix_keeps_its_precision():
     lens = np.full(B, n + 5, np.int32)
     want, bound = ref.decode(q, k, v, table, lens)
     check(decode_call(dev(q), dev(k), dev(v), table, lens, shared_pages=n // page), want, bound)
+
+
+LONG_DECODES = [
+    # lens, shared pages, page, Hq, Hkv, D: many rows behind a long prefix
+    ([5952 + 3 * i for i in range(20)], 93, 64, 64, 8, 128),
+    ([6030 + i for i in range(40)], 6000, 1, 32, 8, 128),                     # a page for each token
+    ([6000, 6400, 6401, 3, 0, 5120, 7000, 1000, 6399, 64] * 2, 400, 16, 64, 8, 80),  # lengths that end inside the prefix
+    ([6144] * 20, 24, 256, 64, 8, 128),                                       # nothing beyond the prefix
+    ([12100 + 7 * i for i in range(30)], 378, 32, 14, 2, 64),
+]
+
+
+@pytest.mark.parametrize("case", LONG_DECODES, ids=lambda c: f"{len(c[0])}x{max(c[0])}s{c[1]}p{c[2]}h{c[3]}-{c[4]}d{c[5]}")
+def test_long_shared_prefixes(case):
+    lens, shared, page, Hq, Hkv, D = case
+    note(f"tiles decode {len(lens)}x{max(lens)} shared {shared} of {page} {Hq}/{Hkv} x {D}")
+    q, k, v, table, lens = decode_make(sum(lens) + D, lens, shared, page, Hq, Hkv, D, "f16")
+    got = decode_call(dev(q), dev(k), dev(v), table, lens, shared_pages=shared)
+    g = Hq // Hkv
+    for j in (0, Hkv - 1):
+        hs = slice(j * g, j * g + g)
+        want, bound = ref.decode(q[:, hs], k[:, j:j + 1], v[:, j:j + 1], table, lens)
+        check(got[:, hs], want, bound, f"K/V head {j}")
+
+
+def test_bad_pages_and_values_in_a_long_shared_prefix():
+    lens = [5000 + 300 * (i % 8) for i in range(24)]
+    Hq, Hkv, page, shared = 64, 8, 64, 96
+    q, k, v, table, lens = decode_make(43, lens, shared, page, Hq, Hkv, 128, "f16")
+    hs = slice(8, 16)
+    want, bound = ref.decode(q[:, hs], k[:, 1:2], v[:, 1:2], table, lens)
+    note("tiles bad pages in a long prefix")
+
+    def run(t):
+        return decode_call(dev(q), dev(k), dev(v), t, lens, shared_pages=shared)[:, hs]
+
+    t = table.copy()
+    t[:, 90] = -7
+    got, hit = run(t), lens > 90 * page
+    assert hit.any() and not hit.all() and np.isnan(got[hit]).all()
+    check(got[~hit], want[~hit], bound[~hit], "rows that do not reach the page")
+    v[table[0, 85], :, 10, 5] = np.inf
+    v[table[0, 95]] = np.nan
+    got, see, lost = run(table), lens > 85 * page + 10, lens > 95 * page
+    assert np.isnan(got[lost]).all() and (got[see & ~lost][..., 5] == np.inf).all()
+    keep = np.arange(128) != 5
+    rest = see & ~lost
+    check(got[rest][..., keep], want[rest][..., keep], bound[rest][..., keep], "beside the infinity")
+    check(got[~see], want[~see], bound[~see], "rows that do not see it")
+
+
+def test_long_shared_prefix_repeats():
+    """The same bits every time, on a side stream with its own workspace, and from a graph as sequences grow."""
+    q, k, v, table, lens = (dev(x) for x in decode_make(44, [6200] * 20, 90, 64, 64, 8, 128, "f16", unused=0))
+    note("tiles decode repeats")
+    a = cf.attention_decode(q, k, v, table, lens, shared_pages=90)
+    torch.cuda.synchronize()
+    side, ws = torch.cuda.Stream(), cf.Workspace()
+    assert torch.equal(a, cf.attention_decode(q, k, v, table, lens, shared_pages=90, stream=side, workspace=ws))
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            cf.attention_decode(q, k, v, table, lens, shared_pages=90, out=out, workspace=ws, stream=side)
+    torch.cuda.synchronize()
+    for r in range(3):
+        lens -= 100
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, cf.attention_decode(q, k, v, table, lens, shared_pages=90)), f"replay {r}"
