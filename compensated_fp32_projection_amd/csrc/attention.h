@@ -57,6 +57,18 @@ struct Partials {
     float *m, *l;
     int slots, dim;
 };
+// How the keys of a decode are cut: the shared ones into `shared` parts (0:
+// none are shared), each sequence's others into `own`, of equal lengths (in
+// whole steps of all waves).  Row groups: 16 rows of the batch's for the
+// shared keys, 16 of a sequence's heads for its own.
+struct DecodeParts {
+    int shared, own, shared_groups, own_groups;
+    int own_from;  // the first key that is not shared
+    bool eight;    // waves
+    int tiles;     // shared parts that attention_tile.hip's kernel takes (then `shared` is 0): slots [0, tiles)
+    Partials to;   // slots: tiles + shared + own; null o: straight to the output
+};
+
 size_t partial_bytes(int64_t rows, int slots, int dim);
 void place_partials(Partials &to, int64_t rows, void *at);
 hipError_t launch_join(const PromptArgs &a, const Partials &from, hipStream_t stream);
@@ -67,10 +79,11 @@ hipError_t launch_join(const DecodeArgs &a, const Partials &from, hipStream_t st
 size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
 hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream);
 
-// The shared keys of a decode with FP16 pages that allow 16-byte loads, in
-// `parts` parts: slots [0, parts).
+// How many parts the shared keys of a decode make there, and the launch of
+// all of a decode whose shared keys go there (FP16 pages that allow 16-byte
+// loads, a token's stride below 2^32 bytes).
 int decode_tile_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t keys, int page_log2);
-hipError_t launch_decode_tile(const DecodeArgs &a, const Partials &to, int parts, hipStream_t stream);
+hipError_t launch_decode_tile(const DecodeArgs &a, const DecodeParts &c, hipStream_t stream);
 
 size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int page_log2,
                                   int64_t shared_pages, bool kv_f16);

@@ -4,6 +4,8 @@
 #include "attention.h"
 #include "device_common.h"
 
+#define CFP32_LDS __attribute__((address_space(3)))
+
 namespace cfp32 {
 
 constexpr float kLog2e = 1.44269504088896340736f;

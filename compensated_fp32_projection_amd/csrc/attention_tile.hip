@@ -25,9 +25,8 @@
 //     not touch the output sums.
 #include <type_traits>
 
-#include "attention_device.h"
+#include "attention_rows.h"
 
-#define CFP32_LDS __attribute__((address_space(3)))
 #define CFP32_GLOBAL __attribute__((address_space(1)))
 #define CFP32_CONSTANT __attribute__((address_space(4)))
 
@@ -142,7 +141,7 @@ struct WaveRows {
 // Keys of tiles [t0, t1), at least one, for this lane's row q, which sees the
 // first `limit` keys.  Tiles go in pairs (one body of code for each pair of
 // buffers): after an odd number, one that no row sees.
-template <int DP, int PL, int NW, class Source>
+template <int DP, int PL, int NW, int R, class Source>
 __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D, int limit, float scale, int t0, int t1,
                                              const Source &src, uint4 *k0, uint4 *k1, uint4 *v0, uint4 *v1, WaveRows<DP> &to)
 {
@@ -293,7 +292,6 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
     // the next with the row (SCORES).  Fragments (4 registers) go through a
     // ring of R, each requested R - 2 ahead of its use; in between,
     // also(n) is called for n = 0, 1, ... 2 LOADS - 1 (the next loads).
-    constexpr int R = 7;
     constexpr int NV = 4 * DB * PL, NK = 2 * KK * PL;
     auto products = [&](const uint4 *vb, const uint4 *kb, auto with_values, auto with_scores, auto also) {
         constexpr bool VALUES = decltype(with_values)::value, SCORES = decltype(with_scores)::value;
@@ -499,12 +497,12 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     } else if constexpr (PL == 2) {
         const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
         const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot, t1 - 1};
-        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW, 7>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                                   (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                                   a.k.tok * 2, a.v.tok * 2, sq.nk - 1, a.D / 8};
-        attend_tiles<DP, PL, NW>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW, 7>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     }
     if (!rows) return;
     const bool live = first + (lane & 31) < n;
@@ -538,16 +536,38 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
 
 // ---- A prefix that all sequences of a decode share -----------------------------------
 
-// 128 rows (sequences x heads of a K/V head) against one part of the shared
-// keys, into slot `part`.
+// The first blocks take 128 rows (sequences x heads of a K/V head) against one
+// part of the shared keys each, into slot `part`; the others
+// (attention_rows.h) the rows of a sequence against a part of its own keys.
+// The former are bounded by their products, the latter by memory: with one
+// of the former to a CU and the latter beside them 32 x 32/8 x 128 behind 65536
+// keys takes 123 us, in two launches of two blocks to a CU 131, and 20 behind
+// 20480 44 against 54 (mixed evenly 151 and 57: some CUs then get three of the
+// long blocks).
 template <int DP>
-__global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Partials to, int parts)
+__global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, DecodeParts c, unsigned tile_blocks)
 {
     __shared__ uint4 k0[kTile * DP / 8], k1[kTile * DP / 8], v0[kTile * DP / 8], v1[kTile * DP / 8];
     __shared__ int ids[kPageIds];
     __shared__ int first_bad;
-    const int g = a.Hq / a.Hkv, part = blockIdx.x % parts, kh = blockIdx.x / parts % a.Hkv;
-    const int64_t n = (int64_t)a.B * g, r0 = (int64_t)(blockIdx.x / parts / a.Hkv) * 128;
+    const unsigned id = blockIdx.x;
+    if (id >= tile_blocks) {
+        static_assert(sizeof k0 >= 4 * Joined<DP, 4>::kWave && sizeof ids >= (8 + 1) * 4 * kRows, "its sums fit");
+        Joined<DP, 4> sh;
+        sh.o[0] = (CFP32_LDS float *)k0;
+        sh.o[1] = (CFP32_LDS float *)k1;
+        sh.o[2] = (CFP32_LDS float *)v0;
+        sh.o[3] = (CFP32_LDS float *)v1;
+        sh.m = (CFP32_LDS float *)ids;
+        sh.l = sh.m + 4 * kRows;
+        sh.unfinished = (CFP32_LDS int *)(sh.l + 4 * kRows);
+        const int other = (int)(id - tile_blocks);
+        decode_rows<_Float16, DP, true, 4, true>(a, c, other / a.Hkv, other % a.Hkv, sh);
+        return;
+    }
+    const Partials &to = c.to;
+    const int parts = c.tiles, g = a.Hq / a.Hkv, part = id % parts, kh = id / parts % a.Hkv;
+    const int64_t n = (int64_t)a.B * g, r0 = (int64_t)(id / parts / a.Hkv) * 128;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
     const int64_t b = over(r, g);
@@ -573,7 +593,7 @@ __global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Parti
         const PagedSource src = {(const char *)((const _Float16 *)a.k.data + kh * a.k.head),
                                  (const char *)((const _Float16 *)a.v.data + kh * a.v.head), a.k.page * 2, a.v.page * 2,
                                  (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), ids, j0, last, a.D / 8, a.page_log2};
-        attend_tiles<DP, 1, 4>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, limit, a.scale,
+        attend_tiles<DP, 1, 4, DP == 128 ? 5 : 7>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, limit, a.scale,
                                t0, t1, src, k0, k1, v0, v1, w);
         if (limit > first_bad) w.l = NAN;
     } else {
@@ -736,7 +756,7 @@ hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t 
 int decode_tile_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t keys, int page_log2)
 {
     const int64_t blocks = (B * (Hq / Hkv) + 127) / 128 * Hkv, tiles = (keys + kTile - 1) / kTile;
-    int64_t parts = 512 / blocks;  // two blocks to a CU
+    int64_t parts = 256 / blocks;  // one block to a CU, and room for the sequences' own keys beside it
     if (parts > (tiles + 3) / 4) parts = (tiles + 3) / 4;
     if (parts < 1) parts = 1;
     // A part's page ids (and two tiles' more, by rounding) fit the block's list.
@@ -745,12 +765,13 @@ int decode_tile_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t keys, int page
     return (int)(parts > least ? parts : least);
 }
 
-hipError_t launch_decode_tile(const DecodeArgs &a, const Partials &to, int parts, hipStream_t stream)
+hipError_t launch_decode_tile(const DecodeArgs &a, const DecodeParts &c, hipStream_t stream)
 {
-    const int64_t blocks = ((int64_t)a.B * (a.Hq / a.Hkv) + 127) / 128 * a.Hkv * parts;
+    const int64_t tiles = ((int64_t)a.B * (a.Hq / a.Hkv) + 127) / 128 * a.Hkv * c.tiles;
+    const int64_t blocks = tiles + (int64_t)a.B * c.own_groups * c.own * a.Hkv;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    if (a.D <= 64) decode_tile_kernel<64><<<(unsigned)blocks, 256, 0, stream>>>(a, to, parts);
-    else decode_tile_kernel<128><<<(unsigned)blocks, 256, 0, stream>>>(a, to, parts);
+    if (a.D <= 64) decode_tile_kernel<64><<<(unsigned)blocks, 256, 0, stream>>>(a, c, (unsigned)tiles);
+    else decode_tile_kernel<128><<<(unsigned)blocks, 256, 0, stream>>>(a, c, (unsigned)tiles);
     return hipGetLastError();
 }
 

@@ -291,7 +291,9 @@ def test_long_shared_prefix_repeats():
     a = cf.attention_decode(q, k, v, table, lens, shared_pages=90)
     torch.cuda.synchronize()
     side, ws = torch.cuda.Stream(), cf.Workspace()
-    assert torch.equal(a, cf.attention_decode(q, k, v, table, lens, shared_pages=90, stream=side, workspace=ws))
+    b = cf.attention_decode(q, k, v, table, lens, shared_pages=90, stream=side, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
     out = torch.empty_like(q)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
