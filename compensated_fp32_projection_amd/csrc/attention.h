@@ -75,7 +75,7 @@ hipError_t launch_join(const PromptArgs &a, const Partials &from, hipStream_t st
 hipError_t launch_join(const DecodeArgs &a, const Partials &from, hipStream_t stream);
 
 // The form for many rows (attention_tile.hip); FP16 K and V have to allow
-// 16-byte loads, and a token's stride to be below 2^32 bytes.
+// 16-byte loads, and a token's stride to be below 2^26 bytes.
 size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
 hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream);
 

@@ -319,7 +319,7 @@ hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStre
     const int64_t units = (int64_t)a.Tq * g / kRows + a.S, rows = (int64_t)a.Tq * a.Hq;
     if (units > 0x7FFFFFFF / a.Hkv || rows > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
     const bool w = wide(a.k.data, a.k.tok | a.k.head, a.D, a.kv_f16) && wide(a.v.data, a.v.tok | a.v.head, a.D, a.kv_f16);
-    const bool can = a.Tk > 0 && (!a.kv_f16 || (w && a.k.tok < ((int64_t)1 << 31) && a.v.tok < ((int64_t)1 << 31)));
+    const bool can = a.Tk > 0 && (!a.kv_f16 || (w && a.k.tok < ((int64_t)1 << 25) && a.v.tok < ((int64_t)1 << 25)));
     if (can && prefer_tiles(a, units)) return launch_prompt_tile(a, workspace, stream);
     Partials to = {nullptr, nullptr, nullptr, prompt_parts(a.S, a.Tk, units * a.Hkv, a.D), padded(a.D)};
     const bool eight = eight_waves(ceil_div(a.Tk, (int64_t)a.S * to.slots), a.D);

@@ -58,19 +58,21 @@ __host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2
 
 // ---- Where a tile's rows are ------------------------------------------------------
 
-// Rows row0 + lr of a tile (row0 the same for the wave), 16-byte chunk `chunk`.
-// page(): what has to be looked up for that, before the loads of several rows.
+// Row row0 + lr of a tile (row0 the same for the wave), 16-byte chunk `chunk`:
+// where it is, as an address of the wave's and a 32-bit offset.
 struct PlaneSource {
+    static constexpr bool kWaveBase = true;
     const char *tiles;      // of this head and sequence
     const int32_t *shifts;
     int last;               // a tile beyond the last repeats it: no row sees it
     __device__ __forceinline__ int page(int, int, int) const { return 0; }
     template <int DP>
-    __device__ __forceinline__ const char *at(int value, int plane, int tile, int row0, int lr, int chunk, int) const
+    __device__ __forceinline__ const char *base(int value, int plane, int tile, int row0) const
     {
-        const char *from = tiles + (int64_t)min(tile, last) * tile_bytes<DP>(2) + (value * 2 + plane) * (kTile * DP * 2);
-        return from + row0 * (DP * 2) + (uint32_t)(lr * (DP * 2) + chunk * 16);
+        return tiles + (int64_t)min(tile, last) * tile_bytes<DP>(2) + ((value * 2 + plane) * kTile + row0) * (DP * 2);
     }
+    template <int DP>
+    __device__ __forceinline__ uint32_t offset(int, int, int, int lr, int chunk) const { return lr * (DP * 2) + chunk * 16; }
     // A scalar load: a vector load would be waited for behind the tiles on their way.
     __device__ __forceinline__ int shift(int value, int tile) const
     {
@@ -79,23 +81,31 @@ struct PlaneSource {
 };
 
 struct PackedSource {
+    static constexpr bool kWaveBase = true;
     const char *k, *v;      // key 0
-    int64_t k_tok, v_tok;   // bytes, below 2^32
+    uint32_t k_tok, v_tok;  // bytes, below 2^26: a tile's rows are within 2^32 of each other
     int last, chunks;       // a key or chunk beyond the last repeats one: it meets a weight or an element of 0
     __device__ __forceinline__ int page(int, int, int) const { return 0; }
     template <int DP>
-    __device__ __forceinline__ const char *at(int value, int, int tile, int row0, int lr, int chunk, int) const
+    __device__ __forceinline__ const char *base(int value, int, int tile, int) const
     {
-        const uint32_t j = (uint32_t)min(tile * kTile + row0 + lr, last);
-        const char *base = (value ? v : k) + (uint64_t)j * (uint32_t)(value ? v_tok : k_tok);
-        return base + (chunk < chunks ? chunk : 0) * 16;
+        const int64_t j0 = min(tile, last / kTile) * kTile;
+        return value ? v + j0 * v_tok : k + j0 * k_tok;
+    }
+    template <int DP>
+    __device__ __forceinline__ uint32_t offset(int value, int tile, int row0, int lr, int chunk) const
+    {
+        const uint32_t row = min(row0 + lr, last - min(tile, last / kTile) * kTile);
+        return row * (value ? v_tok : k_tok) + (chunk < chunks ? chunk : 0) * 16;
     }
     __device__ __forceinline__ int shift(int, int) const { return 0; }
 };
 
 constexpr int kPageIds = 2048;  // pages of a block's keys
 
+// A row has the address of its page, looked up (page) before the loads of several rows.
 struct PagedSource {
+    static constexpr bool kWaveBase = false;
     const char *k, *v;      // the head in page 0
     int64_t k_page, v_page;
     uint32_t k_tok, v_tok;  // bytes
@@ -106,7 +116,7 @@ struct PagedSource {
         return ids[(min(tile * kTile + row0 + lr, last) >> lg) - (first >> lg)];
     }
     template <int DP>
-    __device__ __forceinline__ const char *at(int value, int, int tile, int row0, int lr, int chunk, int page) const
+    __device__ __forceinline__ const char *at(int value, int tile, int row0, int lr, int chunk, int page) const
     {
         const int j = min(tile * kTile + row0 + lr, last);
         const uint32_t o = j & ((1 << lg) - 1);
@@ -168,8 +178,16 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
         asm("" : "+v"(from_lane));  // the addresses are made again each time: kept, they would cost the products registers
         const int lr = from_lane / CH;
         const int c = (from_lane % CH) ^ (value ? v_swizzle(lr) ^ v_swizzle(i * (64 / CH)) : k_swizzle(lr) ^ k_swizzle(i * (64 / CH)));
-        __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)src.template at<DP>(value, p, tile, row0, lr, c, at_page),
-                                         (CFP32_LDS void *)(buf + p * PLANE + piece * 64), 16, 0, 0);
+        CFP32_LDS void *to_lds = (CFP32_LDS void *)(buf + p * PLANE + piece * 64);
+        if constexpr (Source::kWaveBase) {
+            // (A global load to LDS would make the compiler wait for every read of LDS before it uses one.)
+            const char *base = src.template base<DP>(value, p, tile, row0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void *)base, 0, -1, 0x00020000), to_lds, 16,
+                                                     src.template offset<DP>(value, tile, row0, lr, c), 0, 0, 0);
+        } else {
+            __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)src.template at<DP>(value, tile, row0, lr, c, at_page),
+                                             to_lds, 16, 0, 0);
+        }
     };
     t1 += (t1 - t0) & 1;
     if (wave < 4) {
@@ -501,7 +519,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                                   (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
-                                  a.k.tok * 2, a.v.tok * 2, sq.nk - 1, a.D / 8};
+                                  (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), sq.nk - 1, a.D / 8};
         attend_tiles<DP, PL, NW, 7>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     }
     if (!rows) return;
