@@ -72,12 +72,7 @@ template <class T>
 __device__ __forceinline__ void redo_row(const DecodeArgs &a, int64_t i, int h) { attend_decode_row<T>(a, i, h); }
 __device__ __forceinline__ bool prompt_row(const PromptArgs &a, int64_t i, Sequence &sq)
 {
-    int lo = 0, hi = a.S;  // the largest s < S with cu_q[s] <= i
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if (a.cu_q[mid] <= i) lo = mid;
-        else hi = mid;
-    }
+    const int lo = find_last(a.S, i, [&](int s) { return (int64_t)a.cu_q[s]; });
     sq = sequence(a, lo);
     return i >= sq.q0 && i < sq.q0 + sq.nq;
 }

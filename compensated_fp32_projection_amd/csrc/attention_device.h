@@ -24,19 +24,32 @@ __device__ __forceinline__ int64_t over(int64_t a, int b)
     return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
+// The largest s < S with start(s) <= id (0 if none), by all lanes of a wave:
+// 64 starts at a time (one after the other, three lookups took 1.5 us).
+template <class Start>
+__device__ __forceinline__ int find_last(int S, int64_t id, Start start)
+{
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = S;  // it is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 63) / 64, at = lane * step;
+        const uint64_t below = __ballot(at < n && start(lo + at) <= id);
+        const int k = below ? 63 - __builtin_clzll(below) : 0;
+        lo += k * step;
+        n = min(step, n - k * step);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // The sequence that owns unit `id` of a packed batch, where sequence s starts
 // at unit cu[s] * mul / div + s (so sequences of n tokens own up to
 // ceil(n * mul / div) units, and some units belong to none).
 __device__ __forceinline__ int find_unit(const int32_t *cu, int S, int mul, int div, int64_t id, int64_t &start)
 {
-    int lo = 0, hi = S;
-    while (hi - lo > 1) {
-        const int mid = lo + (hi - lo) / 2;
-        if ((int64_t)cu[mid] * mul / div + mid <= id) lo = mid;
-        else hi = mid;
-    }
-    start = (int64_t)cu[lo] * mul / div + lo;
-    return lo;
+    auto at = [&](int s) { return (int64_t)cu[s] * mul / div + s; };
+    const int s = find_last(S, id, at);
+    start = at(s);
+    return s;
 }
 
 // A sequence of a packed batch: rows [q0, q0 + nq) and keys [k0, k0 + nk),

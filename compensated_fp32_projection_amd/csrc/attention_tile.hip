@@ -126,7 +126,7 @@ struct PagedSource {
     __device__ __forceinline__ int shift(int, int) const { return 0; }
 };
 
-// Two weights as high and low FP16 parts (to nearest even; p - high is exact).
+// Two values as high and low FP16 parts (to nearest even; p - high is exact).
 // The difference takes the FP16 operand as it is, which the compiler does not
 // find by itself (it converts back first).  Only that is written out: what
 // reads an exponential's result too early is for the compiler to see.
@@ -139,6 +139,14 @@ __device__ __forceinline__ void split_pair(float p0, float p1, uint32_t &hi, uin
     lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{r0, r1}, half2_t));
 }
 
+// A wave's rows on their way between memory and registers: [32 rows][64 bytes]
+// of LDS, chunks of 16 bytes XORed with the row.
+__device__ __forceinline__ CFP32_LDS char *stage_of(int wave, uint4 *a, uint4 *b)
+{
+    return (CFP32_LDS char *)(wave < 4 ? a : b) + (wave & 3) * 2048;
+}
+__device__ __forceinline__ int stage_at(int row, int chunk) { return row * 64 + (chunk ^ ((row >> 2) & 3)) * 16; }
+
 // ---- The rows of a wave -------------------------------------------------------------
 
 template <int DP>
@@ -148,11 +156,11 @@ struct WaveRows {
     int scale;              // o is at 2^scale
 };
 
-// Keys of tiles [t0, t1), at least one, for this lane's row q, which sees the
-// first `limit` keys.  Tiles go in pairs (one body of code for each pair of
+// Keys of tiles [t0, t1), at least one, for the wave's rows q_row(0 .. 31); this
+// lane's sees the first `limit` keys.  Tiles go in pairs (one body of code for each pair of
 // buffers): after an odd number, one that no row sees.
-template <int DP, int PL, int NW, int R, class Source>
-__device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D, int limit, float scale, int t0, int t1,
+template <int DP, int PL, int NW, int R, class Source, class Row>
+__device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int limit, float scale, int t0, int t1,
                                              const Source &src, uint4 *k0, uint4 *k1, uint4 *v0, uint4 *v1, WaveRows<DP> &to)
 {
     constexpr int CH = DP / 8;         // 16-byte chunks of a row
@@ -199,34 +207,54 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
     half8_t qh[KK], ql[KK];
     float f = fabsf(scale) * kLog2e;  // the sign goes into the row
     {
-        float mx = 0.0f;
-        int e2;
-        {
-            float x[KK][8];
-            if (q_wide) {
+        float x[KK][8], mx = 0.0f;
+        if (q_wide) {
+            // Four lanes to 64 bytes of a row, and to their places through LDS
+            // (a lane for itself, 16 bytes of 64 rows at a time, spent 4 us).
+            CFP32_LDS char *stage = stage_of(wave, v0, v1);
+            const float *qa = q_row(lane >> 2), *qb = q_row(16 + (lane >> 2));
+            float y[KK][2][4];
 #pragma unroll
-                for (int i = 0; i < KK; ++i) load_floats<8, true>(q, 16 * i + 8 * half, D, x[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < KK; ++i) load_floats<8, false>(q, 16 * i + 8 * half, D, x[i]);
+            for (int i = 0; i < KK; ++i) {
+                load_floats<4, true>(qa, 16 * i + 4 * (lane & 3), D, y[i][0]);
+                load_floats<4, true>(qb, 16 * i + 4 * (lane & 3), D, y[i][1]);
             }
 #pragma unroll
-            for (int i = 0; i < KK; ++i)
+            for (int i = 0; i < KK; ++i) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float ax = fabsf(x[i][e]);
-                    mx = fmaxf(mx, ax < INFINITY ? ax : 0.0f);
+                for (int s = 0; s < 2; ++s)
+                    *(CFP32_LDS floatx4_t *)(stage + stage_at(16 * s + (lane >> 2), lane & 3)) =
+                        floatx4_t{y[i][s][0], y[i][s][1], y[i][s][2], y[i][s][3]};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const floatx4_t z = *(CFP32_LDS floatx4_t *)(stage + stage_at(col, 2 * half + s));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][4 * s + e] = z[e];
                 }
-            mx = fmaxf(mx, __shfl_xor(mx, 32));
-            e2 = top_shift(mx);
+            }
+        } else {
+            const float *q = q_row(col);
 #pragma unroll
-            for (int i = 0; i < KK; ++i)
+            for (int i = 0; i < KK; ++i) load_floats<8, false>(q, 16 * i + 8 * half, D, x[i]);
+        }
+        // (A row that is not finite has no finite result, whatever its scale.)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    _Float16 h, w;
-                    split_scaled(scale < 0.0f ? -x[i][e] : x[i][e], e2, h, w);
-                    qh[i][e] = h, ql[i][e] = w;
-                }
+        for (int i = 0; i < KK; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[i][e]));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const int e2 = top_shift(mx);
+#pragma unroll
+        for (int i = 0; i < KK; ++i) {
+            uint32_t h[4], w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float p0 = __builtin_amdgcn_ldexpf(scale < 0.0f ? -x[i][2 * e] : x[i][2 * e], e2);
+                const float p1 = __builtin_amdgcn_ldexpf(scale < 0.0f ? -x[i][2 * e + 1] : x[i][2 * e + 1], e2);
+                split_pair(p0, p1, h[e], w[e]);
+            }
+            qh[i] = __builtin_bit_cast(half8_t, uint4_t{h[0], h[1], h[2], h[3]});
+            ql[i] = __builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]});
         }
         f = __builtin_amdgcn_ldexpf(f, -e2);
     }
@@ -431,16 +459,39 @@ __device__ __forceinline__ void attend_tiles(const float *q, bool q_wide, int D,
     to.scale = kTopWeight + (cv == kNoValues ? 0 : PL == 2 ? cv : 0);
 }
 
-// Four consecutive values; `wide`: the address is a multiple of 16 bytes and all four are there.
-__device__ __forceinline__ void store4(float *out, const float (&y)[4], int n, bool wide)
+// A wave's 32 rows y(b, 4 c + e) (laid out as o) to row_to(0 .. 31) (null: no
+// such row), the first D values of each, through LDS: four lanes to 64 bytes
+// of a row.  `wide`: rows allow 16-byte stores.
+template <int DP, class Value, class Row>
+__device__ __forceinline__ void store_rows(CFP32_LDS char *stage, Value y, Row row_to, int D, bool wide)
 {
-    if (wide && n >= 4) {
-        *reinterpret_cast<floatx4_t *>(out) = floatx4_t{y[0], y[1], y[2], y[3]};
-        return;
-    }
+    const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+    float *to[2] = {row_to(lane >> 2), row_to(16 + (lane >> 2))};
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < n) out[e] = y[e];
+    for (int b = 0; b < DP / 32; ++b)
+#pragma unroll
+        for (int c2 = 0; c2 < 4; c2 += 2) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                floatx4_t x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = y(b, 4 * (c2 + c) + e);
+                *(CFP32_LDS floatx4_t *)(stage + stage_at(col, 2 * c + half)) = x;
+            }
+            const int d = 32 * b + 8 * c2 + 4 * (lane & 3);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const floatx4_t x = *(CFP32_LDS floatx4_t *)(stage + stage_at(16 * s + (lane >> 2), lane & 3));
+                if (!to[s]) continue;
+                if (wide && d + 4 <= D) {
+                    *reinterpret_cast<floatx4_t *>(to[s] + d) = x;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (d + e < D) to[s][d + e] = x[e];
+                }
+            }
+        }
 }
 
 template <int DP>
@@ -453,26 +504,22 @@ __device__ __forceinline__ void no_rows(WaveRows<DP> &w)
         for (int e = 0; e < 16; ++e) w.o[b][e] = 0.0f;
 }
 
-// A wave's rows into their slots.
-template <int DP>
-__device__ __forceinline__ void leave_rows(const WaveRows<DP> &w, const Partials &to, int64_t slot, bool live)
+// A wave's rows into their slots (slot_of(row) < 0: no such row).
+template <int DP, class Slot>
+__device__ __forceinline__ void leave_rows(const WaveRows<DP> &w, const Partials &to, Slot slot_of, CFP32_LDS char *stage)
 {
-    const int half = (threadIdx.x & 63) >> 5;
-    if (!live) return;
-    if (half == 0) {
+    const int lane = threadIdx.x & 63;
+    const int64_t slot = slot_of(lane & 31);
+    if (lane < 32 && slot >= 0) {
         to.m[slot] = w.m;
         to.l[slot] = __builtin_amdgcn_ldexpf(w.l, -kTopWeight);
     }
-    if (w.l == 0.0f) return;
-#pragma unroll
-    for (int b = 0; b < DP / 32; ++b)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            floatx4_t y;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = __builtin_amdgcn_ldexpf(w.o[b][4 * c + e], -w.scale);
-            *reinterpret_cast<floatx4_t *>(to.o + slot * DP + 32 * b + 8 * c + 4 * half) = y;
-        }
+    if (!__any(w.l != 0.0f)) return;
+    store_rows<DP>(stage, [&](int b, int r) { return __builtin_amdgcn_ldexpf(w.o[b][r], -w.scale); },
+                   [&](int row) {
+                       const int64_t s = slot_of(row);
+                       return s < 0 ? (float *)nullptr : to.o + s * DP;
+                   }, DP, true);
 }
 
 // Tiles [0, n) in parts of an even number.
@@ -499,13 +546,17 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     const Sequence sq = sequence(a, sid);
     const int64_t n = (int64_t)sq.nq * g, r0 = (id - start) * kBlockRows;
     if (id < start || r0 >= n) return;
-    const int lane = threadIdx.x & 63, half = lane >> 5, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
-    const int i = (int)over(r, g), h = kh * g + (int)(r - (int64_t)i * g);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t first = r0 + wave * kWaveRows;
+    const int own = (int)over(min(first + (lane & 31), n - 1), g);  // this lane's row of the sequence
     const bool rows = first < n;
     const int keys = sq.limit((int)over(min(r0 + kBlockRows, n) - 1, g));
-    const int limit = sq.limit(i);
-    const float *q = (const float *)a.q.data + (sq.q0 + i) * a.q.tok + h * a.q.head;
+    const int limit = sq.limit(own);
+    // Row of the wave -> token, head.
+    auto q_row = [&](int row) {
+        const int64_t r = min(first + row, n - 1), i = over(r, g);
+        return (const float *)a.q.data + (sq.q0 + i) * a.q.tok + (kh * g + (r - i * g)) * a.q.head;
+    };
     const bool q_wide = rows_wide(a.q.data, a.q.tok | a.q.head, a.D);
     WaveRows<DP> w;
     int t0, t1;
@@ -515,34 +566,43 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     } else if constexpr (PL == 2) {
         const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
         const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot, t1 - 1};
-        attend_tiles<DP, PL, NW, 7>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW, 7>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                                   (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                                   (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), sq.nk - 1, a.D / 8};
-        attend_tiles<DP, PL, NW, 7>(q, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW, 7>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     }
     if (!rows) return;
-    const bool live = first + (lane & 31) < n;
-    if (to.o) return leave_rows<DP>(w, to, ((int64_t)(sq.q0 + i) * a.Hq + h) * to.slots + part, live);
-    // l is summed at 2^kTopWeight, o at 2^scale.
-    const float inv = w.l == 0.0f ? 0.0f : __builtin_amdgcn_ldexpf(1.0f / w.l, kTopWeight);
-    float *out = a.out + (sq.q0 + i) * a.out_tok + h * a.out_head;
-    const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)((a.out_tok | a.out_head) * 4)) & 15) == 0;
-    bool odd = false;
+    // K's buffers have been read by now (V's last may be in use).
+    CFP32_LDS char *stage = stage_of(wave, k0, k1);
+    if (to.o)
+        return leave_rows<DP>(w, to, [&](int row) -> int64_t {
+            const int64_t r = first + row, i = over(r, g);
+            return r < n ? ((sq.q0 + i) * a.Hq + kh * g + (r - i * g)) * to.slots + part : -1;
+        }, stage);
+    // l is summed at 2^kTopWeight, o at 2^scale: one factor where that is no
+    // extreme power of two.
+    const float inv = w.l == 0.0f ? 0.0f : 1.0f / w.l;
+    const int shift = kTopWeight - w.scale;
+    const bool once = PL == 1 || (shift > -60 && shift < 60);
+    const float factor = __builtin_amdgcn_ldexpf(inv, once ? shift : 0);
+    const int then = once ? 0 : shift;
+    float finite = 0.0f;  // NaN once a result is not
 #pragma unroll
     for (int b = 0; b < DP / 32; ++b)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int d = 32 * b + 8 * c + 4 * half;
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[e] = __builtin_amdgcn_ldexpf(w.o[b][4 * c + e] * inv, -w.scale);
-                odd |= d + e < a.D && !(fabsf(y[e]) < INFINITY);
-            }
-            if (live) store4(out + d, y, a.D - d, wide);
+        for (int r = 0; r < 16; ++r) {
+            w.o[b][r] *= factor;
+            if (then) w.o[b][r] = __builtin_amdgcn_ldexpf(w.o[b][r], then);
+            finite = fmaf(w.o[b][r], 0.0f, finite);
         }
+    const bool live = first + (lane & 31) < n, odd = finite != finite;
+    store_rows<DP>(stage, [&](int b, int r) { return w.o[b][r]; },
+                   [&](int row) {
+                       const int64_t r = first + row, i = over(r, g);
+                       return r < n ? a.out + (sq.q0 + i) * a.out_tok + (kh * g + (r - i * g)) * a.out_head : (float *)nullptr;
+                   }, a.D, ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)((a.out_tok | a.out_head) * 4)) & 15) == 0);
     uint64_t redo = __ballot(odd && live);
     redo = (redo | redo >> 32) & 0xFFFFFFFFull;
     for (; redo; redo &= redo - 1) {
@@ -587,9 +647,7 @@ __global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Decod
     const int parts = c.tiles, g = a.Hq / a.Hkv, part = id % parts, kh = id / parts % a.Hkv;
     const int64_t n = (int64_t)a.B * g, r0 = (int64_t)(id / parts / a.Hkv) * 128;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t first = r0 + wave * kWaveRows, r = min(first + (lane & 31), n - 1);
-    const int64_t b = over(r, g);
-    const int h = kh * g + (int)(r - b * g);
+    const int64_t first = r0 + wave * kWaveRows, b = over(min(first + (lane & 31), n - 1), g);
     const int shared = a.shared_pages << a.page_log2;
     const int limit = min(decode_length(a, (int)b), shared);
     int t0, t1;
@@ -611,13 +669,19 @@ __global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Decod
         const PagedSource src = {(const char *)((const _Float16 *)a.k.data + kh * a.k.head),
                                  (const char *)((const _Float16 *)a.v.data + kh * a.v.head), a.k.page * 2, a.v.page * 2,
                                  (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), ids, j0, last, a.D / 8, a.page_log2};
-        attend_tiles<DP, 1, 4, DP == 128 ? 5 : 7>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, limit, a.scale,
+        attend_tiles<DP, 1, 4, DP == 128 ? 5 : 7>([&](int row) {
+            const int64_t r = min(first + row, n - 1), s = over(r, g);
+            return a.q + s * a.q_seq + (kh * g + (r - s * g)) * a.q_head;
+        }, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, limit, a.scale,
                                t0, t1, src, k0, k1, v0, v1, w);
         if (limit > first_bad) w.l = NAN;
     } else {
         no_rows<DP>(w);
     }
-    leave_rows<DP>(w, to, (b * a.Hq + h) * to.slots + part, first + (lane & 31) < n);
+    leave_rows<DP>(w, to, [&](int row) -> int64_t {
+        const int64_t r = first + row, s = over(r, g);
+        return r < n ? (s * a.Hq + kh * g + (r - s * g)) * to.slots + part : -1;
+    }, stage_of(wave, k0, k1));
 }
 
 // FP32 K and V of one tile and head as two FP16 planes each.
@@ -703,15 +767,17 @@ int64_t plane_bytes(int64_t slots, int64_t Hkv, int64_t D)
     return (n + 255) & ~(int64_t)255;
 }
 
-// Where blocks of 128 rows are few, their keys make parts, up to kTileBlocks
-// blocks, of at least kPartTiles tiles for the average sequence: 1500 x 12 x
-// 64 FP32 (144 blocks) 55 -> 46 us; with 200 to 256 blocks two parts cost more
-// than they gave (1000 x 32/8 x 128 FP16 43 -> 53 us), and so did parts of
-// four tiles (4 x 300 x 12 x 64 FP16 after 100 each 16 -> 25 us).
-constexpr int64_t kTileBlocks = 320, kPartTiles = 8;
+// Where blocks of 128 rows are few, their keys make parts of at least
+// kPartTiles tiles for the average sequence, up to 512 blocks for long ones
+// (2048 x 12 x 64 FP32, 204 blocks: 68 -> 60 us), up to 320 for shorter (1500 x
+// 12 x 64, 144 blocks: 55 -> 46; with 200 to 256 blocks of 1000 keys two parts
+// cost more than they gave: x 32/8 x 128 FP16 43 -> 53 us; and so did parts of
+// four tiles: 4 x 300 x 12 x 64 FP16 after 100 each 16 -> 25 us).
+constexpr int64_t kTileBlocks = 512, kPartTiles = 8;
 int tile_parts(int64_t S, int64_t Tk, int64_t blocks)
 {
-    const int64_t most = (Tk / S + kPartTiles * kTile - 1) / (kPartTiles * kTile), want = kTileBlocks / blocks;
+    const int64_t most = (Tk / S + kPartTiles * kTile - 1) / (kPartTiles * kTile);
+    const int64_t want = (Tk / S >= 24 * kTile ? kTileBlocks : 320) / blocks;
     return (int)(want <= 1 || most <= 1 ? 1 : most < want ? most : want);
 }
 
