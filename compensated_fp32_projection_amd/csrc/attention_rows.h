@@ -3,7 +3,7 @@
 //
 // A block of four waves works on 16 rows (tokens x heads of one K/V head, so
 // grouped heads share what is read); its keys are dealt to the waves in steps
-// of kStep, and the waves' sums are joined in LDS.  Everything a wave
+// of 32 or 64, and the waves' sums are joined in LDS.  Everything a wave
 // multiplies goes from memory straight into the registers the matrix
 // instructions read:
 //   * scores as S^T = K Q^T, so that a lane holds scores of one row (column
@@ -33,7 +33,6 @@ constexpr int kRows = 16;
 struct PackedKeys {
     const char *k, *v;       // key 0 of the head
     int64_t k_tok, v_tok;    // bytes
-    __device__ __forceinline__ int page_of(int) { return 0; }
     __device__ __forceinline__ int page_step(int) { return 0; }
     __device__ __forceinline__ const char *key(int j, int) const { return k + j * k_tok; }
     __device__ __forceinline__ const char *value(int j, int) const { return v + j * v_tok; }

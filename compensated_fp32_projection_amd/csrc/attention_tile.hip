@@ -3,8 +3,8 @@
 //
 // A block's waves hold 32 rows each (tokens x heads of one K/V head: grouped
 // heads are rows like others) and go through the keys 64 at a time.  A tile
-// of K and V comes from memory straight into LDS (global_load_lds, 16 bytes a
-// lane) while the tile before it is multiplied; one barrier to a tile.
+// of K and V comes from memory straight into LDS (16 bytes a lane) while the
+// tile before it is multiplied.
 //   * Products: v_mfma_f32_32x32x16_f16 with FP32 sums.  An FP32 operand is
 //     scaled by a power of two to the top of FP16's range and split into two
 //     FP16 parts of 22 bits together (rows on the way in, weights as they are
@@ -23,6 +23,11 @@
 //     64 bytes) so that four rows do.
 //   * The running maximum is followed lazily (kLazy), so that most tiles do
 //     not touch the output sums.
+// Bound by the matrix units' power where there is enough to do: 8192 x 32/8 x
+// 128 FP32, causal, takes 1.29 ms, 1275 TFLOP/s of products (three for one)
+// with the units busy 78% of a clock that falls to 1.5 GHz.  8 x 750 of these
+// with FP16 keys take 126 us, 650 TFLOP/s (two for one): blocks of 32 to 1024
+// keys spend much of their time on their first tile and their last stores.
 #include <type_traits>
 
 #include "attention_rows.h"

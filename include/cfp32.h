@@ -384,11 +384,15 @@ CFP32_API size_t cfp32_attention_prompt_workspace_bytes(int64_t S, int64_t Tk, i
  * continues a cached prefix).  out = softmax(scale q K^T) V over the keys a
  * row sees; a row that sees none is 0.  What a row does not see does not
  * reach it, NaN and infinities included; an infinite or NaN value of V that
- * a row sees reaches it as IEEE arithmetic has it, an infinite or NaN entry
- * of a key or query as NaN.  Rows of out outside all sequences are not written.
- * FP32 K and V: values below 2^-24 of the largest in a 64-key tile of a head
- * keep fewer bits than FP32 holds (their error is below 2^-39 of that
- * largest). */
+ * a row sees reaches it as IEEE arithmetic has it, and so does an infinite or
+ * NaN score.  Rows of out outside all sequences are not written.
+ * (A score of -infinity weighs 0, and a row all of whose scores are -infinity
+ * is 0.)
+ * FP32 K and V of long prompts are multiplied as two FP16 parts each, 22 bits
+ * at one power-of-two scale for a head's 64 keys: values below 2^-24 of the
+ * largest in such a group keep fewer bits (their error is below 2^-39 of that
+ * largest), and the error of a group's values of V may reach 2^-35 of the
+ * largest in the groups before it. */
 CFP32_API cfp32_status cfp32_attention_prompt(const float *q, int64_t q_tok, int64_t q_head,
                                     const void *k, int64_t k_tok, int64_t k_head,
                                     const void *v, int64_t v_tok, int64_t v_head, int kv_type,
