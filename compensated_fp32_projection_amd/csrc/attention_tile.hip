@@ -819,8 +819,14 @@ hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t 
     // Eight waves multiply and make weights at the same time; four give more
     // and shorter blocks.  Two blocks of four to a CU and not more: four
     // (1024 x 32/8 x 128 FP16 52 -> 43 us, FP32 77 -> 66; 8192: 903 -> 955 and
-    // 1321 -> 1572).
-    const bool eight = blocks > 512;
+    // 1321 -> 1572).  Where two of them fit a CU's LDS together, also for up
+    // to four and for short sequences, whose blocks are mostly beginning and
+    // end (eight against four: 2 x 4000 x 12 x 64 FP16 138 / 125, 16 x 1000 of
+    // these 105 / 91, 200 x 40 92 / 49, 8 x 750 x 32/8 x 128 136 / 128, 6 x
+    // 1400 218 / 229, 4 x 2000 275 / 287, FP32 4 x 4000 x 32/8 x 64 778 / 814;
+    // where they do not fit, 8 x 750 x 32/8 x 128 FP32 189 / 227).
+    const bool together = a.kv_f16 || a.D <= 64;
+    const bool eight = blocks > 512 && (!together || (blocks > 1024 && a.Tk / a.S > 1100));
 #define CFP32_PROMPT(T, DP, NW)                                                                                       \
     prompt_tile_kernel<T, DP, NW><<<dim3((unsigned)(((int64_t)a.Tq * g / (NW * kWaveRows) + a.S) * a.Hkv),             \
                                          (unsigned)to.slots), 64 * NW, 0, stream>>>(a, planes, to)
