@@ -26,8 +26,8 @@
 // Bound by the matrix units' power where there is enough to do: 8192 x 32/8 x
 // 128 FP32, causal, takes 1.29 ms, 1275 TFLOP/s of products (three for one)
 // with the units busy 78% of a clock that falls to 1.5 GHz.  8 x 750 of these
-// with FP16 keys take 126 us, 650 TFLOP/s (two for one): blocks of 32 to 1024
-// keys spend much of their time on their first tile and their last stores.
+// with FP16 keys take 121 us, 675 TFLOP/s (two for one): blocks of up to 18
+// tiles spend much of their time on their first one and their last stores.
 #include <type_traits>
 
 #include "attention_rows.h"
