@@ -264,7 +264,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
         f = __builtin_amdgcn_ldexpf(f, -e2);
     }
     float m = -INFINITY, l = 0.0f;
-    int cv = kNoValues;  // values are summed at 2^(kTopWeight + cv)
+    int cv = kNoValues;  // values are summed at 2^(kTopWeight + cv); kNoValues: none yet
     floatx16_t o[DB];
 #pragma unroll
     for (int b = 0; b < DB; ++b)
@@ -298,28 +298,43 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
         for (int r = 1; r < 16; ++r) mx = fmaxf(mx, fmaxf(s[0][r], s[1][r]));
         mx *= ft;  // ft >= 0
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        int up = 0;  // this tile's values beside the sums' scale
-        if (PL == 2) {
-            const int ev = v_shift == kNoValues ? cv : v_shift;
-            up = ev < cv ? 1 : min(ev - cv, 60);  // 2^(kTopWeight - 60): nothing in FP16
-            if (ev < cv) {
-                // A step of room: values a little larger do not move the scale again.
-                const int next = ev - 1;
-                const float c = cv == kNoValues ? 1.0f : __builtin_amdgcn_ldexpf(1.0f, max(next - cv, -200));
-#pragma unroll
-                for (int b = 0; b < DB; ++b) o[b] *= c;
-                cv = next;
+        // The sums' scale follows what the row sums, weight times value: at
+        // 2^-cv beside the weights' 2^-m, it is lowered only by a tile that
+        // weighs more with its values than all before it (lazily, as m is).
+        // A tile that the row does not see, or gives no weight, leaves it.
+        // m and cv are integers, so what the sums are multiplied by is exact.
+        const float mn = fmaxf(m, PL == 2 ? ceilf(mx) : mx), from = mn == -INFINITY ? 0.0f : mn;
+        const int ev = v_shift == kNoValues ? cv : v_shift;
+        const float held = (m - from) - (float)cv;  // in powers of two beside `from`: what was summed, and what comes
+        const float comes = PL == 1 || v_shift == kNoValues ? -INFINITY : (mx - from) - (float)ev;
+        if (__any(mx > m + kLazy || (PL == 2 && comes > held + kLazy))) {
+            l *= mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
+            float c;
+            if (PL == 2) {
+                const float top = fmaxf(held, ceilf(comes));
+                cv = top > -(float)kNoValues ? -(int)top : kNoValues;
+                c = exp2_raw(held + (float)cv);
+            } else {
+                c = mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
             }
-        }
-        if (__any(mx > m + kLazy)) {
-            const float mn = fmaxf(m, mx);
-            const float c = mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
             m = mn;
-            l *= c;
 #pragma unroll
             for (int b = 0; b < DB; ++b) o[b] *= c;
         }
-        const float base = (float)(kTopWeight - up) - (m == -INFINITY ? 0.0f : m);
+        const float top_m = m == -INFINITY ? 0.0f : m;
+        const int up = PL == 2 ? (v_shift == kNoValues ? 0 : v_shift - cv) : 0;  // this tile's values beside the sums' scale
+        // Where this tile's values are that much smaller, its weights for
+        // them may leave FP32's range: their sum is then taken by itself.
+        const bool apart = PL == 2 && __any(up > 90);
+        if (apart) {
+            float add = 0.0f;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) add += exp2_raw(fmaf(s[b][r], ft, (float)kTopWeight - top_m));
+            l += add;
+        }
+        const float base = (float)(kTopWeight - up) - top_m;
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -337,7 +352,8 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             __builtin_amdgcn_sched_barrier(0);  // eight at a time: more would need registers the products hold
         }
         const float add = sum[0] + sum[1];
-        l = PL == 2 ? fmaf(add, __builtin_amdgcn_ldexpf(1.0f, up), l) : l + add;
+        if (PL == 1) l += add;
+        else if (!apart) l = fmaf(add, __builtin_amdgcn_ldexpf(1.0f, up), l);
     };
     // The products of a phase: V of one tile with its weights (VALUES), K of
     // the next with the row (SCORES).  Fragments (4 registers) go through a

@@ -391,8 +391,7 @@ CFP32_API size_t cfp32_attention_prompt_workspace_bytes(int64_t S, int64_t Tk, i
  * FP32 K and V of long prompts are multiplied as two FP16 parts each, 22 bits
  * at one power-of-two scale for a head's 64 keys: values below 2^-24 of the
  * largest in such a group keep fewer bits (their error is below 2^-39 of that
- * largest), and the error of a group's values of V may reach 2^-35 of the
- * largest in the groups before it. */
+ * largest). */
 CFP32_API cfp32_status cfp32_attention_prompt(const float *q, int64_t q_tok, int64_t q_head,
                                     const void *k, int64_t k_tok, int64_t k_head,
                                     const void *v, int64_t v_tok, int64_t v_head, int kv_type,

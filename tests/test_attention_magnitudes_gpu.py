@@ -1,0 +1,68 @@
+"""GPU tests of long prompts (64-key tiles) whose K and V differ in magnitude
+from token to token: a row's result is FP32-grade whatever the keys it does not
+see, or gives no weight, hold (definition in FP64, tolerance derived in
+attention_reference.py)."""
+import numpy as np
+import pytest
+
+from gpu_helpers import note
+from test_attention_prompt_gpu import call, dev, make, starts
+from test_attention_tiles_gpu import compare
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = {
+    # sequences, Hq, Hkv, D, head compared
+    "four_waves": ([1100], 12, 12, 64, 7),
+    "parts": ([1500], 12, 12, 64, 3),                                          # keys in parts, joined
+    "eight_waves": ([290, 310, 270, 300, 305, 295, 340, 290], 32, 8, 128, 5),
+    "odd_dim": ([900, 700], 16, 8, 80, 6),
+}
+
+
+def run(shape, seed, change, causal=True):
+    """A prompt of that shape whose q, k, v of every sequence went through `change`, against the definition."""
+    lens, Hq, Hkv, D, head = SHAPES[shape]
+    q, k, v = make(seed, lens, lens, Hq, Hkv, D, "f32")
+    cu = starts(lens)
+    for a, b in zip(cu[:-1], cu[1:]):
+        change(q[a:b], k[a:b], v[a:b])
+    compare(call(dev(q), dev(k), dev(v), cu, cu, causal=causal), q, k, v, cu, cu, [head], causal=causal)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_tiles_of_rising_values(shape):
+    """Rows that see the first tile only, before tiles of 2^200 times its values."""
+    note(f"rising values {shape}")
+
+    def change(q, k, v):
+        v[:64] *= np.float32(1e-30)
+        v[64:] *= np.float32(1e30)
+
+    run(shape, 51, change)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_tiles_of_large_values_without_weight(shape, causal):
+    """Large values whose keys weigh nothing, before small ones."""
+    note(f"large weightless tiles {shape} causal={causal}")
+
+    def change(q, k, v):
+        np.abs(q, out=q)
+        k[:64] = -40
+        v[:64] *= np.float32(1e30)
+        v[64:] *= np.float32(1e-30)
+
+    run(shape, 52, change, causal)
+
+
+def test_values_fall_and_rise_between_tiles():
+    """Magnitudes over all of FP32's range from tile to tile."""
+    note("values fall and rise")
+    f = np.float32(10.0) ** np.random.default_rng(53).integers(-34, 35, 17).astype(np.float32)
+
+    def change(q, k, v):
+        v *= np.resize(f.repeat(64), len(v))[:, None, None]
+
+    run("four_waves", 53, change)
