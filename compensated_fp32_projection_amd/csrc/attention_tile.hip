@@ -47,16 +47,24 @@ typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 constexpr int kTile = 64;       // keys of a tile
 constexpr int kWaveRows = 32;
 constexpr int kTopWeight = 11;  // weights are multiplied at 2^kTopWeight: up to 2^(kTopWeight + kLazy) = 2^15
-constexpr int kNoValues = 1 << 20;  // shift of a tile whose values are all zero
+constexpr int kNoValues = 1 << 20;  // shift of a tile or key whose values are all zero
+constexpr int kKeyShifts = 1 << 21; // shift of K: the tile's keys have shifts of their own
 
 // Planes of FP32 K and V, cut in two: for each K/V head and tile [K hi, K lo,
 // V hi, V lo][64][DP] FP16, zeros beyond the sequence and beyond D, and the
-// shifts of K and V.
+// shifts of K and V.  One shift for 64 keys leaves each its bits as long as
+// their largest magnitudes are within 1 / kSpread of each other: an element is
+// then off by no more than 2^-22 of itself or 2^-27 of its key's largest.
+// Tiles whose keys differ by more, of which a row may see the small ones
+// alone, or weigh them alone, have a shift for each key.  key_shifts ([K,
+// V][64]) has every key's, also those of a tile that are alike.
 struct Planes {
     char *tiles;
-    int32_t *shifts;
+    int32_t *shifts, *key_shifts;
     int64_t slots;  // tiles of a head: sequence s starts at cu_k[s] / 64 + s
 };
+
+constexpr float kSpread = 0x1p-12f;
 
 template <int DP>
 __host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2 * planes * kTile * DP * 2; }
@@ -68,7 +76,7 @@ __host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2
 struct PlaneSource {
     static constexpr bool kWaveBase = true;
     const char *tiles;      // of this head and sequence
-    const int32_t *shifts;
+    const int32_t *shifts, *key_shifts;
     int last;               // a tile beyond the last repeats it: no row sees it
     __device__ __forceinline__ int page(int, int, int) const { return 0; }
     template <int DP>
@@ -82,6 +90,23 @@ struct PlaneSource {
     __device__ __forceinline__ int shift(int value, int tile) const
     {
         return ((const CFP32_CONSTANT int32_t *)shifts)[2 * min(tile, last) + value];
+    }
+    // No tile from t0 on has keys with shifts of their own, and those of V are
+    // within 60 of each other (weights at one tile's scale are then within
+    // FP32's range at another's).
+    __device__ __forceinline__ bool alike(int t0) const
+    {
+        bool other = false;
+        const int first = shift(1, t0);
+        for (int t = t0 + (threadIdx.x & 63); t <= last; t += 64) {
+            const int2 s = *reinterpret_cast<const int2 *>(shifts + 2 * t);
+            other |= s.x == kKeyShifts || (s.y != kNoValues && abs(s.y - first) > 30);
+        }
+        return !__any(other);
+    }
+    __device__ __forceinline__ const int32_t *shifts_of(int value, int tile) const
+    {
+        return key_shifts + (2 * min(tile, last) + value) * kTile;
     }
 };
 
@@ -164,7 +189,12 @@ struct WaveRows {
 // Keys of tiles [t0, t1), at least one, for the wave's rows q_row(0 .. 31); this
 // lane's sees the first `limit` keys.  Tiles go in pairs (one body of code for each pair of
 // buffers): after an odd number, one that no row sees.
-template <int DP, int PL, int NW, int R, class Source, class Row>
+// EACH: K and V have a scale for each key, for what one scale for 64 keys, or
+// tiles whose scales are alike, does not hold.  A body of its own, chosen once
+// for a block (a test in each tile cost the usual inputs 3 to 5%); 8192 x 32/8 x
+// 128 whose blocks all take it 2.26 ms against 1.34, 1000 x 12 x 64 57 us
+// against 36.
+template <int DP, int PL, int NW, int R, bool EACH, class Source, class Row>
 __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int limit, float scale, int t0, int t1,
                                              const Source &src, uint4 *k0, uint4 *k1, uint4 *v0, uint4 *v1, WaveRows<DP> &to)
 {
@@ -279,62 +309,93 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
 
     floatx16_t s[2];
     half8_t ph[4], pl[4];
-    auto weights = [&](int tile, int k_shift, int v_shift) {
-        const int j0 = tile * kTile;
-        float ft = PL == 2 ? __builtin_amdgcn_ldexpf(f, -k_shift) : f;
-        if (__any(j0 + kTile > limit)) {
-            const int n = limit - j0 - 4 * half;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float x = s[b][r] * ft;
-                    s[b][r] = 32 * b + 8 * (r / 4) + r % 4 < n ? x : -INFINITY;
-                }
-            ft = 1.0f;
-        }
-        float mx = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, fmaxf(s[0][r], s[1][r]));
-        mx *= ft;  // ft >= 0
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        // The sums' scale follows what the row sums, weight times value: at
-        // 2^-cv beside the weights' 2^-m, it is lowered only by a tile that
-        // weighs more with its values than all before it (lazily, as m is).
-        // A tile that the row does not see, or gives no weight, leaves it.
-        // m and cv are integers, so what the sums are multiplied by is exact.
-        const float mn = fmaxf(m, PL == 2 ? ceilf(mx) : mx), from = mn == -INFINITY ? 0.0f : mn;
-        const int ev = v_shift == kNoValues ? cv : v_shift;
-        const float held = (m - from) - (float)cv;  // in powers of two beside `from`: what was summed, and what comes
-        const float comes = PL == 1 || v_shift == kNoValues ? -INFINITY : (mx - from) - (float)ev;
+    // The running maximum after a tile whose largest score is mx, and the
+    // sums' scale after its largest weight times value, `comes` beside the
+    // maximum (in powers of two, FP32 V): at 2^-cv beside the weights' 2^-m,
+    // it is lowered only by a tile that weighs more with its values than all
+    // before it (lazily, as m is).  A tile that the row does not see, or gives
+    // no weight, leaves it.  m and cv are integers there, so what the sums are
+    // multiplied by is exact.
+    auto above = [&](float mx) { return fmaxf(m, PL == 2 ? ceilf(mx) : mx); };
+    auto follow = [&](float mx, float mn, float comes) {
+        const float held = (m - (mn == -INFINITY ? 0.0f : mn)) - (float)cv;  // what was summed, as `comes`
         if (__any(mx > m + kLazy || (PL == 2 && comes > held + kLazy))) {
-            l *= mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
-            float c;
+            const float d = mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
+            float c = d;
             if (PL == 2) {
                 const float top = fmaxf(held, ceilf(comes));
                 cv = top > -(float)kNoValues ? -(int)top : kNoValues;
                 c = exp2_raw(held + (float)cv);
-            } else {
-                c = mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
             }
             m = mn;
+            l *= d;
 #pragma unroll
             for (int b = 0; b < DB; ++b) o[b] *= c;
         }
-        const float top_m = m == -INFINITY ? 0.0f : m;
-        const int up = PL == 2 ? (v_shift == kNoValues ? 0 : v_shift - cv) : 0;  // this tile's values beside the sums' scale
-        // Where this tile's values are that much smaller, its weights for
-        // them may leave FP32's range: their sum is then taken by itself.
-        const bool apart = PL == 2 && __any(up > 90);
-        if (apart) {
-            float add = 0.0f;
+    };
+    auto zero_if_none = [](float x) { return x == -INFINITY ? 0.0f : x; };
+    auto weights = [&](int tile, int k_shift, int v_shift) {
+        const int j0 = tile * kTile, n = limit - j0 - 4 * half;
+        float ft = f, base;
+        int up = 0;  // this tile's values beside the sums' scale
+        if constexpr (EACH) {
+            // Key by key, and the weights' sum by itself: those for the values may leave FP32's range.
+            auto by_key = [&](int value, auto change) {
+                const CFP32_GLOBAL int32_t *shifts = (const CFP32_GLOBAL int32_t *)src.shifts_of(value, tile) + 4 * half;
+                asm("" : "+v"(shifts));  // read again each time, four at a time: kept, they would need registers
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) add += exp2_raw(fmaf(s[b][r], ft, (float)kTopWeight - top_m));
-            l += add;
+                    for (int r = 0; r < 16; ++r) {
+                        const int key = 32 * b + 8 * (r / 4) + r % 4;
+                        s[b][r] = change(s[b][r], key, shifts[key]);
+                        if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+                    }
+            };
+            float mx = -INFINITY, comes = -INFINITY;
+            by_key(0, [&](float x, int key, int shift) {
+                x *= __builtin_amdgcn_ldexpf(f, -shift);
+                x = key < n ? x : -INFINITY;
+                mx = fmaxf(mx, x);
+                return x;
+            });
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float mn = above(mx), from = zero_if_none(mn);
+            by_key(1, [&](float x, int, int shift) {
+                comes = fmaxf(comes, (x - from) - (float)shift);
+                return x;
+            });
+            follow(mx, mn, fmaxf(comes, __shfl_xor(comes, 32)));
+            const float top = zero_if_none(m);
+            by_key(1, [&](float x, int, int shift) {
+                x -= top;
+                l += exp2_raw(x + (float)kTopWeight);
+                return x - (float)shift;
+            });
+            ft = 1.0f;
+            base = (float)(kTopWeight + cv);
+        } else {
+            if (PL == 2) ft = __builtin_amdgcn_ldexpf(f, -k_shift);
+            if (__any(j0 + kTile > limit)) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float x = s[b][r] * ft;
+                        s[b][r] = 32 * b + 8 * (r / 4) + r % 4 < n ? x : -INFINITY;
+                    }
+                ft = 1.0f;
+            }
+            float mx = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+            for (int r = 1; r < 16; ++r) mx = fmaxf(mx, fmaxf(s[0][r], s[1][r]));
+            mx *= ft;  // ft >= 0
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float mn = above(mx);
+            follow(mx, mn, v_shift == kNoValues ? -INFINITY : (mx - zero_if_none(mn)) - (float)v_shift);
+            if (PL == 2) up = v_shift == kNoValues ? 0 : v_shift - cv;
+            base = (float)(kTopWeight - up) - zero_if_none(m);
         }
-        const float base = (float)(kTopWeight - up) - top_m;
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -352,8 +413,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             __builtin_amdgcn_sched_barrier(0);  // eight at a time: more would need registers the products hold
         }
         const float add = sum[0] + sum[1];
-        if (PL == 1) l += add;
-        else if (!apart) l = fmaf(add, __builtin_amdgcn_ldexpf(1.0f, up), l);
+        if (!EACH) l = PL == 2 ? fmaf(add, __builtin_amdgcn_ldexpf(1.0f, up), l) : l + add;
     };
     // The products of a phase: V of one tile with its weights (VALUES), K of
     // the next with the row (SCORES).  Fragments (4 registers) go through a
@@ -586,13 +646,15 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
         no_rows<DP>(w);
     } else if constexpr (PL == 2) {
         const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
-        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot, t1 - 1};
-        attend_tiles<DP, PL, NW, 7>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot,
+                                 planes.key_shifts + 2 * kTile * slot, t1 - 1};
+        if (src.alike(t0)) attend_tiles<DP, PL, NW, 7, false>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        else attend_tiles<DP, PL, NW, 5, true>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                                   (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                                   (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), sq.nk - 1, a.D / 8};
-        attend_tiles<DP, PL, NW, 7>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW, 7, false>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     }
     if (!rows) return;
     // K's buffers have been read by now (V's last may be in use).
@@ -690,7 +752,7 @@ __global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Decod
         const PagedSource src = {(const char *)((const _Float16 *)a.k.data + kh * a.k.head),
                                  (const char *)((const _Float16 *)a.v.data + kh * a.v.head), a.k.page * 2, a.v.page * 2,
                                  (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), ids, j0, last, a.D / 8, a.page_log2};
-        attend_tiles<DP, 1, 4, DP == 128 ? 5 : 7>([&](int row) {
+        attend_tiles<DP, 1, 4, DP == 128 ? 5 : 7, false>([&](int row) {
             const int64_t r = min(first + row, n - 1), s = over(r, g);
             return a.q + s * a.q_seq + (kh * g + (r - s * g)) * a.q_head;
         }, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, limit, a.scale,
@@ -705,12 +767,27 @@ __global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Decod
     }, stage_of(wave, k0, k1));
 }
 
+// The largest x >= 0 of each N (8 or 16) neighbouring lanes, to all of them:
+// lanes exchanged by quad_perm 1 0 3 2 and 2 3 0 1, halves and rows mirrored.
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float x)
+{
+    return fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true)));
+}
+template <int N>
+__device__ __forceinline__ float max_of_lanes(float x)
+{
+    static_assert(N == 8 || N == 16, "half a row of lanes, or a row");
+    x = max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(x)));
+    return N == 16 ? max_dpp<0x140>(x) : x;
+}
+
 // FP32 K and V of one tile and head as two FP16 planes each.
 template <int DP>
 __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes planes)
 {
     constexpr int CH = DP / 8, PER = kTile * CH / 256;
-    __shared__ float most[2][4];
+    __shared__ float most[2][4], least[2][4];
     const int kh = blockIdx.y;
     int64_t start;
     const int sid = find_unit(a.cu_k, a.S, 1, kTile, blockIdx.x, start);
@@ -721,7 +798,7 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
     const bool wide = a.D % 4 == 0 &&
                       ((reinterpret_cast<uintptr_t>(a.k.data) | reinterpret_cast<uintptr_t>(a.v.data) |
                         (uintptr_t)((a.k.tok | a.k.head | a.v.tok | a.v.head) * 4)) & 15) == 0;
-    float x[2][PER][8], mx[2] = {0.0f, 0.0f};
+    float x[2][PER][8], key_mx[2][PER];  // of the key's CH lanes
 #pragma unroll
     for (int value = 0; value < 2; ++value)
 #pragma unroll
@@ -730,6 +807,7 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
             const HeadsView &t = value ? a.v : a.k;
             const float *p = (const float *)t.data + (sq.k0 + j0 + row) * t.tok + kh * t.head + d;
             const bool there = j0 + row < sq.nk;
+            float mx = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
                 if (wide) {
@@ -744,26 +822,49 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const float ax = fabsf(x[value][i][e + u]);
-                    mx[value] = fmaxf(mx[value], ax < INFINITY ? ax : 0.0f);
+                    mx = fmaxf(mx, ax < INFINITY ? ax : 0.0f);
                 }
             }
+            key_mx[value][i] = max_of_lanes<CH>(mx);
         }
 #pragma unroll
     for (int value = 0; value < 2; ++value) {
+        float hi = 0.0f, lo = INFINITY;  // of the keys that are not zero
 #pragma unroll
-        for (int o = 32; o; o >>= 1) mx[value] = fmaxf(mx[value], __shfl_xor(mx[value], o));
-        if ((threadIdx.x & 63) == 0) most[value][threadIdx.x >> 6] = mx[value];
+        for (int i = 0; i < PER; ++i) {
+            hi = fmaxf(hi, key_mx[value][i]);
+            lo = fminf(lo, key_mx[value][i] > 0.0f ? key_mx[value][i] : INFINITY);
+        }
+#pragma unroll
+        for (int o = 32; o >= CH; o >>= 1) {
+            hi = fmaxf(hi, __shfl_xor(hi, o));
+            lo = fminf(lo, __shfl_xor(lo, o));
+        }
+        if ((threadIdx.x & 63) == 0) {
+            most[value][threadIdx.x >> 6] = hi;
+            least[value][threadIdx.x >> 6] = lo;
+        }
     }
     __syncthreads();
+    float top[2];
+    bool each = false;
+#pragma unroll
+    for (int value = 0; value < 2; ++value) {
+        top[value] = fmaxf(fmaxf(most[value][0], most[value][1]), fmaxf(most[value][2], most[value][3]));
+        each |= fminf(fminf(least[value][0], least[value][1]), fminf(least[value][2], least[value][3])) < top[value] * kSpread;
+    }
     char *tile = planes.tiles + slot * tile_bytes<DP>(2);
 #pragma unroll
     for (int value = 0; value < 2; ++value) {
-        const float top = fmaxf(fmaxf(most[value][0], most[value][1]), fmaxf(most[value][2], most[value][3]));
-        const int e2 = top_shift(top);
-        if (threadIdx.x == 0) planes.shifts[2 * slot + value] = value && top == 0.0f ? kNoValues : e2;
+        const int all = top_shift(top[value]);
+        if (threadIdx.x == 0)
+            planes.shifts[2 * slot + value] = each ? (value ? 0 : kKeyShifts) : value && top[1] == 0.0f ? kNoValues : all;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int at = threadIdx.x + 256 * i;
+            const int e2 = each ? top_shift(key_mx[value][i]) : all;
+            if (at % CH == 0)
+                planes.key_shifts[(2 * slot + value) * kTile + at / CH] = value && key_mx[1][i] == 0.0f ? kNoValues : e2;
             half8_t hi, lo;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -784,7 +885,7 @@ namespace {
 
 int64_t plane_bytes(int64_t slots, int64_t Hkv, int64_t D)
 {
-    const int64_t n = slots * Hkv * ((D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)) + 8);
+    const int64_t n = slots * Hkv * ((D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)) + 8 * (1 + kTile));
     return (n + 255) & ~(int64_t)255;
 }
 
@@ -820,6 +921,7 @@ hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t 
         planes.slots = a.Tk / kTile + a.S;
         planes.tiles = ws;
         planes.shifts = (int32_t *)(ws + planes.slots * a.Hkv * (a.D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)));
+        planes.key_shifts = planes.shifts + 2 * planes.slots * a.Hkv;
         ws += plane_bytes(planes.slots, a.Hkv, a.D);
         if (planes.slots > 0x7FFFFFFF || a.Hkv > 65535) return hipErrorInvalidConfiguration;
         const dim3 grid((unsigned)planes.slots, (unsigned)a.Hkv);

@@ -388,10 +388,13 @@ CFP32_API size_t cfp32_attention_prompt_workspace_bytes(int64_t S, int64_t Tk, i
  * NaN score.  Rows of out outside all sequences are not written.
  * (A score of -infinity weighs 0, and a row all of whose scores are -infinity
  * is 0.)
- * FP32 K and V of long prompts are multiplied as two FP16 parts each, 22 bits
- * at one power-of-two scale for a head's 64 keys: values below 2^-24 of the
- * largest in such a group keep fewer bits (their error is below 2^-39 of that
- * largest). */
+ * Operands cut into two FP16 parts keep 22 bits: a value of q is off by no more
+ * than 2^-22 of itself or 2^-39 of its row's largest, one of FP32 K and V (long
+ * prompts) than 2^-22 of itself or 2^-27 of the largest of its token and head,
+ * and a weight (long prompts, shared prefixes) than 2^-22 of itself or 2^-36 of
+ * the row's largest (with FP32 V: largest product of a weight and the largest
+ * value of 64 tokens).  Tokens that a row does not see, or gives no weight,
+ * cost it no bits, whatever their magnitude. */
 CFP32_API cfp32_status cfp32_attention_prompt(const float *q, int64_t q_tok, int64_t q_head,
                                     const void *k, int64_t k_tok, int64_t k_head,
                                     const void *v, int64_t v_tok, int64_t v_head, int kv_type,

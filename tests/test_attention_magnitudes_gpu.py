@@ -66,3 +66,59 @@ def test_values_fall_and_rise_between_tiles():
         v *= np.resize(f.repeat(64), len(v))[:, None, None]
 
     run("four_waves", 53, change)
+
+
+@pytest.mark.parametrize("factor", [1e6, 1e8, 1e12, 1e30])
+@pytest.mark.parametrize("what", ["key", "value"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_one_large_token(shape, what, factor):
+    """One token's keys or values multiplied: the rows before it do not see it."""
+    note(f"one large {what} x {factor} {shape}")
+
+    def change(q, k, v):
+        (k if what == "key" else v)[180] *= np.float32(factor)
+
+    run(shape, 54, change)
+
+
+@pytest.mark.parametrize("what", ["key", "value"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_one_small_token(shape, what):
+    """One token's keys or values next to nothing; one row sees it alone."""
+    note(f"one small {what} {shape}")
+
+    def change(q, k, v):
+        (k if what == "key" else v)[0] *= np.float32(1e-20)
+
+    run(shape, 55, change)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_large_tokens_without_weight(shape, causal):
+    """Every second token has large values, and keys (some of them large) that give it no weight."""
+    note(f"large weightless tokens {shape} causal={causal}")
+
+    def change(q, k, v):
+        np.abs(q, out=q)
+        k[1::4] = -40
+        k[3::4] = -1e15
+        v[1::2] *= np.float32(1e20)
+
+    run(shape, 56, change, causal)
+
+
+def test_tokens_of_every_magnitude():
+    """Values over all of FP32's range from token to token, and keys of different magnitudes."""
+    note("tokens of every magnitude")
+    rng = np.random.default_rng(57)
+
+    def change(q, k, v):
+        n = len(v)
+        v *= np.float32(10.0) ** rng.integers(-34, 35, n).astype(np.float32)[:, None, None]
+        k *= np.float32(10.0) ** rng.integers(-9, 1, n).astype(np.float32)[:, None, None]
+        v[rng.integers(0, n, n // 9)] = 0
+        k[rng.integers(0, n, n // 9)] = 0
+
+    run("four_waves", 57, change)
+    run("eight_waves", 58, change)
