@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, Partials from, int64_
     }
     if (!out) return;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    bool odd = !(fabsf(l) < INFINITY);
+    bool odd = !(fabsf(l) < INFINITY) || l == 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float y = o[e] * inv;

@@ -317,7 +317,8 @@ __device__ __forceinline__ void join_rows(const Joined<DP, NW> &from, int row, i
 }
 
 // A row's sums, of what this block has seen: into its slot, or (all there is)
-// as its result.  Results that are not finite are marked.
+// as its result.  Results that are not finite are marked, and rows of no
+// weight: they see nothing, or scores that are too low in powers of two only.
 template <bool SLOTS, int DP, int NW>
 __device__ __forceinline__ void leave_row(const Joined<DP, NW> &sh, const Partials &to, int64_t slot, float *out, int D, bool live)
 {
@@ -342,7 +343,7 @@ __device__ __forceinline__ void leave_row(const Joined<DP, NW> &sh, const Partia
         const float y = x[e] * inv;
         if (d0 + e < D) {
             out[d0 + e] = y;
-            if (!(fabsf(y) < INFINITY)) sh.unfinished[row] = 1;
+            if (!(fabsf(y) < INFINITY) || l == 0.0f) sh.unfinished[row] = 1;
         }
     }
 }

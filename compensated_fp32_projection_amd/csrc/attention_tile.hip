@@ -354,9 +354,9 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             };
             float mx = -INFINITY, comes = -INFINITY;
             by_key(0, [&](float x, int key, int shift) {
-                x *= __builtin_amdgcn_ldexpf(f, -shift);
-                x = key < n ? x : -INFINITY;
-                mx = fmaxf(mx, x);
+                const float fk = __builtin_amdgcn_ldexpf(f, -shift);
+                x = key < n ? x * fk : -INFINITY;
+                mx = fmaxf(mx, key < n && fk == INFINITY ? INFINITY : x);
                 return x;
             });
             mx = fmaxf(mx, __shfl_xor(mx, 32));
@@ -376,6 +376,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             base = (float)(kTopWeight + cv);
         } else {
             if (PL == 2) ft = __builtin_amdgcn_ldexpf(f, -k_shift);
+            const bool far = ft == INFINITY;
             if (__any(j0 + kTile > limit)) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -389,7 +390,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             float mx = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
             for (int r = 1; r < 16; ++r) mx = fmaxf(mx, fmaxf(s[0][r], s[1][r]));
-            mx *= ft;  // ft >= 0
+            mx = far ? INFINITY : mx * ft;  // ft >= 0
             mx = fmaxf(mx, __shfl_xor(mx, 32));
             const float mn = above(mx);
             follow(mx, mn, v_shift == kNoValues ? -INFINITY : (mx - zero_if_none(mn)) - (float)v_shift);
@@ -536,7 +537,10 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
 #pragma unroll
     for (int b = 0; b < DB; ++b) to.o[b] = o[b];
     to.m = m;
-    to.l = l + __shfl_xor(l, 32);
+    // Scores (in powers of two) beyond FP32's range, the lowest of them for
+    // all keys included: whether they are finite as such is for the slow form.
+    l += __shfl_xor(l, 32);
+    to.l = m == INFINITY || (l == 0.0f && limit > t0 * kTile) ? NAN : l;
     to.scale = kTopWeight + (cv == kNoValues ? 0 : PL == 2 ? cv : 0);
 }
 
