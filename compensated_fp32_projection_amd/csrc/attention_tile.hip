@@ -91,18 +91,24 @@ struct PlaneSource {
     {
         return ((const CFP32_CONSTANT int32_t *)shifts)[2 * min(tile, last) + value];
     }
+    // Tile t0 + lane's shifts, asked for before what else a block begins with.
+    __device__ __forceinline__ int2 ask(int t0) const
+    {
+        return *reinterpret_cast<const int2 *>(shifts + 2 * min(t0 + (int)(threadIdx.x & 63), last));
+    }
     // No tile from t0 on has keys with shifts of their own, and those of V are
     // within 60 of each other (weights at one tile's scale are then within
     // FP32's range at another's).
-    __device__ __forceinline__ bool alike(int t0) const
+    __device__ __forceinline__ bool alike(int t0, int2 s) const
     {
+        const int first = __builtin_amdgcn_readfirstlane(s.y);
         bool other = false;
-        const int first = shift(1, t0);
-        for (int t = t0 + (threadIdx.x & 63); t <= last; t += 64) {
-            const int2 s = *reinterpret_cast<const int2 *>(shifts + 2 * t);
+        for (int t = t0;;) {
             other |= s.x == kKeyShifts || (s.y != kNoValues && abs(s.y - first) > 30);
+            t += 64;
+            if (t > last) return !__any(other);
+            s = ask(t);
         }
-        return !__any(other);
     }
     __device__ __forceinline__ const int32_t *shifts_of(int value, int tile) const
     {
@@ -189,12 +195,7 @@ struct WaveRows {
 // Keys of tiles [t0, t1), at least one, for the wave's rows q_row(0 .. 31); this
 // lane's sees the first `limit` keys.  Tiles go in pairs (one body of code for each pair of
 // buffers): after an odd number, one that no row sees.
-// EACH: K and V have a scale for each key, for what one scale for 64 keys, or
-// tiles whose scales are alike, does not hold.  A body of its own, chosen once
-// for a block (a test in each tile cost the usual inputs 3 to 5%); 8192 x 32/8 x
-// 128 whose blocks all take it 2.26 ms against 1.34, 1000 x 12 x 64 57 us
-// against 36.
-template <int DP, int PL, int NW, int R, bool EACH, class Source, class Row>
+template <int DP, int PL, int NW, int R, class Source, class Row>
 __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int limit, float scale, int t0, int t1,
                                              const Source &src, uint4 *k0, uint4 *k1, uint4 *v0, uint4 *v1, WaveRows<DP> &to)
 {
@@ -233,45 +234,48 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
         }
     };
     t1 += (t1 - t0) & 1;
+    int2 shifts = {};
+    if constexpr (PL == 2) shifts = src.ask(t0);
     if (wave < 4) {
 #pragma unroll
         for (int n = 0; n < LOADS; ++n) fetch(0, t0, k0, n, page(t0, n));
     }
 
+    float x[KK][8];  // the row's values 16 i + 8 half ..
+    if (q_wide) {
+        // Four lanes to 64 bytes of a row, and to their places through LDS
+        // (a lane for itself, 16 bytes of 64 rows at a time, spent 4 us).
+        CFP32_LDS char *stage = stage_of(wave, v0, v1);
+        const float *qa = q_row(lane >> 2), *qb = q_row(16 + (lane >> 2));
+        float y[KK][2][4];
+#pragma unroll
+        for (int i = 0; i < KK; ++i) {
+            load_floats<4, true>(qa, 16 * i + 4 * (lane & 3), D, y[i][0]);
+            load_floats<4, true>(qb, 16 * i + 4 * (lane & 3), D, y[i][1]);
+        }
+#pragma unroll
+        for (int i = 0; i < KK; ++i) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                *(CFP32_LDS floatx4_t *)(stage + stage_at(16 * s + (lane >> 2), lane & 3)) =
+                    floatx4_t{y[i][s][0], y[i][s][1], y[i][s][2], y[i][s][3]};
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const floatx4_t z = *(CFP32_LDS floatx4_t *)(stage + stage_at(col, 2 * half + s));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][4 * s + e] = z[e];
+            }
+        }
+    } else {
+        const float *q = q_row(col);
+#pragma unroll
+        for (int i = 0; i < KK; ++i) load_floats<8, false>(q, 16 * i + 8 * half, D, x[i]);
+    }
     // The row, at 2^e2, as the right operand of the scores.
     half8_t qh[KK], ql[KK];
     float f = fabsf(scale) * kLog2e;  // the sign goes into the row
-    {
-        float x[KK][8], mx = 0.0f;
-        if (q_wide) {
-            // Four lanes to 64 bytes of a row, and to their places through LDS
-            // (a lane for itself, 16 bytes of 64 rows at a time, spent 4 us).
-            CFP32_LDS char *stage = stage_of(wave, v0, v1);
-            const float *qa = q_row(lane >> 2), *qb = q_row(16 + (lane >> 2));
-            float y[KK][2][4];
-#pragma unroll
-            for (int i = 0; i < KK; ++i) {
-                load_floats<4, true>(qa, 16 * i + 4 * (lane & 3), D, y[i][0]);
-                load_floats<4, true>(qb, 16 * i + 4 * (lane & 3), D, y[i][1]);
-            }
-#pragma unroll
-            for (int i = 0; i < KK; ++i) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    *(CFP32_LDS floatx4_t *)(stage + stage_at(16 * s + (lane >> 2), lane & 3)) =
-                        floatx4_t{y[i][s][0], y[i][s][1], y[i][s][2], y[i][s][3]};
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const floatx4_t z = *(CFP32_LDS floatx4_t *)(stage + stage_at(col, 2 * half + s));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][4 * s + e] = z[e];
-                }
-            }
-        } else {
-            const float *q = q_row(col);
-#pragma unroll
-            for (int i = 0; i < KK; ++i) load_floats<8, false>(q, 16 * i + 8 * half, D, x[i]);
-        }
+    auto split_row = [&] {
+        float mx = 0.0f;
         // (A row that is not finite has no finite result, whatever its scale.)
 #pragma unroll
         for (int i = 0; i < KK; ++i)
@@ -292,7 +296,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             ql[i] = __builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]});
         }
         f = __builtin_amdgcn_ldexpf(f, -e2);
-    }
+    };
     float m = -INFINITY, l = 0.0f;
     int cv = kNoValues;  // values are summed at 2^(kTopWeight + cv); kNoValues: none yet
     floatx16_t o[DB];
@@ -334,14 +338,22 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
         }
     };
     auto zero_if_none = [](float x) { return x == -INFINITY ? 0.0f : x; };
-    auto weights = [&](int tile, int k_shift, int v_shift) {
+    // `each`: K and V have a scale for each key, for what one scale for 64 keys,
+    // or tiles whose scales are alike, does not hold.  A loop of its own, chosen
+    // once for a block from shifts asked for before the row (a test in each
+    // tile cost the usual inputs 3 to 5%, the shifts asked for by themselves 1
+    // to 3%); 8192 x 32/8 x 128 whose blocks all take it 2.26 ms against 1.34,
+    // 1000 x 12 x 64 57 us against 36.
+    auto weights = [&](int tile, int k_shift, int v_shift, auto each) {
+        constexpr bool EACH = decltype(each)::value;
         const int j0 = tile * kTile, n = limit - j0 - 4 * half;
         float ft = f, base;
         int up = 0;  // this tile's values beside the sums' scale
         if constexpr (EACH) {
             // Key by key, and the weights' sum by itself: those for the values may leave FP32's range.
             auto by_key = [&](int value, auto change) {
-                const CFP32_GLOBAL int32_t *shifts = (const CFP32_GLOBAL int32_t *)src.shifts_of(value, tile) + 4 * half;
+                const CFP32_GLOBAL int32_t *shifts = nullptr;
+                if constexpr (PL == 2) shifts = (const CFP32_GLOBAL int32_t *)src.shifts_of(value, tile) + 4 * half;
                 asm("" : "+v"(shifts));  // read again each time, four at a time: kept, they would need registers
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
@@ -496,7 +508,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
     // at which read is then plain to the compiler, which would wait otherwise.
     // All waves go through all tiles (those of the block's last row): the
     // barriers hold them that long anyway.
-    auto run = [&](auto group) {
+    auto run = [&](auto group, auto each) {
         constexpr bool second = decltype(group)::value;
         int t = t0;
         // K(u), V(u - 1); beyond the last tile, where no one reads them, the last again.
@@ -509,7 +521,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
         // Weights of tile t, its values, the next one's scores (unless it is the last).
         auto step = [&](uint4 *k_now, uint4 *k_next, uint4 *v_now, uint4 *v_next, auto last) {
             constexpr bool more = !decltype(last)::value;
-            weights(t, src.shift(0, t), src.shift(1, t));
+            weights(t, src.shift(0, t), src.shift(1, t), each);
             if (!second) drain();
             if (!second || more) sync();
             if constexpr (more) {
@@ -530,10 +542,25 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
         step(k0, k1, v0, v1, no);
         step(k1, k0, v1, v0, yes);
     };
-    drain();
-    sync();
-    if (NW == 8 && wave >= 4) run(yes);
-    else run(no);
+    auto run_groups = [&](auto each) {
+        split_row();
+        drain();
+        sync();
+        if (NW == 8 && wave >= 4) run(yes, each);
+        else run(no, each);
+    };
+    if constexpr (PL == 2) {
+        if (src.alike(t0, shifts)) {
+            run_groups(no);
+        } else {
+            // (The row is split in both places, so that what one loop has no
+            // registers for is not spilled in the other.)
+            asm volatile("" ::: "memory");
+            run_groups(yes);
+        }
+    } else {
+        run_groups(no);
+    }
 #pragma unroll
     for (int b = 0; b < DB; ++b) to.o[b] = o[b];
     to.m = m;
@@ -652,13 +679,12 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
         const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
         const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot,
                                  planes.key_shifts + 2 * kTile * slot, t1 - 1};
-        if (src.alike(t0)) attend_tiles<DP, PL, NW, 7, false>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
-        else attend_tiles<DP, PL, NW, 5, true>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW, 7>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
                                   (const char *)((const T *)a.v.data + sq.k0 * a.v.tok + kh * a.v.head),
                                   (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), sq.nk - 1, a.D / 8};
-        attend_tiles<DP, PL, NW, 7, false>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
+        attend_tiles<DP, PL, NW, 7>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     }
     if (!rows) return;
     // K's buffers have been read by now (V's last may be in use).
@@ -756,7 +782,7 @@ __global__ __launch_bounds__(256, 2) void decode_tile_kernel(DecodeArgs a, Decod
         const PagedSource src = {(const char *)((const _Float16 *)a.k.data + kh * a.k.head),
                                  (const char *)((const _Float16 *)a.v.data + kh * a.v.head), a.k.page * 2, a.v.page * 2,
                                  (uint32_t)(a.k.tok * 2), (uint32_t)(a.v.tok * 2), ids, j0, last, a.D / 8, a.page_log2};
-        attend_tiles<DP, 1, 4, DP == 128 ? 5 : 7, false>([&](int row) {
+        attend_tiles<DP, 1, 4, DP == 128 ? 5 : 7>([&](int row) {
             const int64_t r = min(first + row, n - 1), s = over(r, g);
             return a.q + s * a.q_seq + (kh * g + (r - s * g)) * a.q_head;
         }, rows_wide(a.q, a.q_seq | a.q_head, a.D), a.D, limit, a.scale,
