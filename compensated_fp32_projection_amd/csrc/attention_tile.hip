@@ -273,7 +273,8 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
     }
     // The row, at 2^e2, as the right operand of the scores.
     half8_t qh[KK], ql[KK];
-    float f = fabsf(scale) * kLog2e;  // the sign goes into the row
+    const float f = fabsf(scale) * kLog2e;  // the sign goes into the row
+    int e2;  // (scores are taken back from the row's and the keys' shifts at once: one after the other may leave FP32's range)
     auto split_row = [&] {
         float mx = 0.0f;
         // (A row that is not finite has no finite result, whatever its scale.)
@@ -282,7 +283,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
 #pragma unroll
             for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[i][e]));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
-        const int e2 = top_shift(mx);
+        e2 = top_shift(mx);
 #pragma unroll
         for (int i = 0; i < KK; ++i) {
             uint32_t h[4], w[4];
@@ -295,7 +296,6 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             qh[i] = __builtin_bit_cast(half8_t, uint4_t{h[0], h[1], h[2], h[3]});
             ql[i] = __builtin_bit_cast(half8_t, uint4_t{w[0], w[1], w[2], w[3]});
         }
-        f = __builtin_amdgcn_ldexpf(f, -e2);
     };
     float m = -INFINITY, l = 0.0f;
     int cv = kNoValues;  // values are summed at 2^(kTopWeight + cv); kNoValues: none yet
@@ -347,7 +347,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
     auto weights = [&](int tile, int k_shift, int v_shift, auto each) {
         constexpr bool EACH = decltype(each)::value;
         const int j0 = tile * kTile, n = limit - j0 - 4 * half;
-        float ft = f, base;
+        float ft, base;
         int up = 0;  // this tile's values beside the sums' scale
         if constexpr (EACH) {
             // Key by key, and the weights' sum by itself: those for the values may leave FP32's range.
@@ -366,7 +366,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             };
             float mx = -INFINITY, comes = -INFINITY;
             by_key(0, [&](float x, int key, int shift) {
-                const float fk = __builtin_amdgcn_ldexpf(f, -shift);
+                const float fk = __builtin_amdgcn_ldexpf(f, -e2 - shift);
                 x = key < n ? x * fk : -INFINITY;
                 mx = fmaxf(mx, key < n && fk == INFINITY ? INFINITY : x);
                 return x;
@@ -387,7 +387,7 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             ft = 1.0f;
             base = (float)(kTopWeight + cv);
         } else {
-            if (PL == 2) ft = __builtin_amdgcn_ldexpf(f, -k_shift);
+            ft = __builtin_amdgcn_ldexpf(f, -e2 - (PL == 2 ? k_shift : 0));
             const bool far = ft == INFINITY;
             if (__any(j0 + kTile > limit)) {
 #pragma unroll

@@ -54,3 +54,16 @@ def test_scores_near_the_largest_finite_value(form, sign):
     k[7, :, 3] = -2.6e19 if sign < 0 else 3.2e19
     got = call(dev(q), dev(k), dev(v), cu, cu, scale=1.0)[7:, 0]
     assert (np.abs(got - v[7, 0]) <= 2.0 ** -23 * np.abs(v[7, 0])).all()
+
+
+@pytest.mark.parametrize("sq,sk", [(2e-38, 2e37), (1e-39, 1e38), (1e37, 2e-38)])
+def test_products_of_the_smallest_and_largest(sq, sk):
+    """Rows near FP32's smallest normal value (and below) against keys near its largest."""
+    note(f"smallest and largest {sq} {sk}")
+    q, k, v = make(64, [1100], [1100], 12, 12, 64, "f32")
+    k = np.clip(k, -3, 3)
+    q, k = q * np.float32(sq), k * np.float32(sk)
+    cu = starts([1100])
+    got = call(dev(q), dev(k), dev(v), cu, cu)
+    want, bound, _ = ref.prompt(q[:, 4:5], k[:, 4:5], v[:, 4:5], cu, cu)
+    check(got[:, 4:5], want, bound)

@@ -16,8 +16,11 @@ SHAPES = {
     "four_waves": ([1100], 12, 12, 64, 7),
     "parts": ([1500], 12, 12, 64, 3),                                          # keys in parts, joined
     "eight_waves": ([290, 310, 270, 300, 305, 295, 340, 290], 32, 8, 128, 5),
+    "seventy_tiles": ([4500], 4, 4, 64, 2),
     "odd_dim": ([900, 700], 16, 8, 80, 6),
 }
+
+FORMS = ["four_waves", "parts", "eight_waves", "odd_dim"]
 
 
 def run(shape, seed, change, causal=True):
@@ -30,7 +33,7 @@ def run(shape, seed, change, causal=True):
     compare(call(dev(q), dev(k), dev(v), cu, cu, causal=causal), q, k, v, cu, cu, [head], causal=causal)
 
 
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", FORMS)
 def test_tiles_of_rising_values(shape):
     """Rows that see the first tile only, before tiles of 2^200 times its values."""
     note(f"rising values {shape}")
@@ -43,7 +46,7 @@ def test_tiles_of_rising_values(shape):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", FORMS)
 def test_tiles_of_large_values_without_weight(shape, causal):
     """Large values whose keys weigh nothing, before small ones."""
     note(f"large weightless tiles {shape} causal={causal}")
@@ -68,9 +71,20 @@ def test_values_fall_and_rise_between_tiles():
     run("four_waves", 53, change)
 
 
+@pytest.mark.parametrize("what", ["key", "value"])
+def test_one_large_token_far_on(what):
+    """In the seventieth tile."""
+    note(f"one large {what} far on")
+
+    def change(q, k, v):
+        (k if what == "key" else v)[4450] *= np.float32(1e12)
+
+    run("seventy_tiles", 59, change)
+
+
 @pytest.mark.parametrize("factor", [1e6, 1e8, 1e12, 1e30])
 @pytest.mark.parametrize("what", ["key", "value"])
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", FORMS)
 def test_one_large_token(shape, what, factor):
     """One token's keys or values multiplied: the rows before it do not see it."""
     note(f"one large {what} x {factor} {shape}")
@@ -82,7 +96,7 @@ def test_one_large_token(shape, what, factor):
 
 
 @pytest.mark.parametrize("what", ["key", "value"])
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", FORMS)
 def test_one_small_token(shape, what):
     """One token's keys or values next to nothing; one row sees it alone."""
     note(f"one small {what} {shape}")
@@ -94,7 +108,7 @@ def test_one_small_token(shape, what):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("shape", FORMS)
 def test_large_tokens_without_weight(shape, causal):
     """Every second token has large values, and keys (some of them large) that give it no weight."""
     note(f"large weightless tokens {shape} causal={causal}")
