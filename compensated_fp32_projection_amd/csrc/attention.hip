@@ -117,8 +117,9 @@ __global__ __launch_bounds__(256) void join_kernel(Args a, Partials from, int64_
             li = from.l[s0 + i];
         }
         l = fmaf(f, li, l);
-        if (li == 0.0f) f = 0.0f;  // nothing was written there
-        uint64_t used = __ballot(f != 0.0f);
+        // Nothing was written where li is 0; what is has to be read also where
+        // f is 0, for the NaN of an infinite value.
+        uint64_t used = __ballot(li != 0.0f);
         while (used) {
             constexpr int U = 8;  // loads in flight
             float w[U], x[U][E];

@@ -67,3 +67,24 @@ def test_products_of_the_smallest_and_largest(sq, sk):
     got = call(dev(q), dev(k), dev(v), cu, cu)
     want, bound, _ = ref.prompt(q[:, 4:5], k[:, 4:5], v[:, 4:5], cu, cu)
     check(got[:, 4:5], want, bound)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+@pytest.mark.parametrize("kv", ["f32", "f16"])
+def test_values_in_parts_of_little_weight(kv, bad):
+    """A value that is not finite among keys whose weights underflow beside
+    another part's: 0 times it is NaN."""
+    note(f"parts of little weight {bad} {kv}")
+    q, k, v, table, lens = decode_make(63, [2000, 1990], 0, 16, 1, 1, 64, kv)
+    want, bound = ref.decode(q, k, v, table, lens)
+    q[:] = np.abs(q)
+    for b in range(2):
+        for j in range(100, 120):
+            k[table[b, j], 0, 3] = 40
+    v[table[0, 1], 0, 2, 5] = bad
+    want, bound = ref.decode(q, k, v, table, lens)
+    got = decode_call(dev(q), dev(k), dev(v), table, lens)
+    keep = np.arange(64) != 5
+    assert not np.isfinite(got[0, 0, 5])
+    check(got[0, 0, keep], want[0, 0, keep], bound[0, 0, keep], "beside it")
+    check(got[1], want[1], bound[1], "the other sequence")
