@@ -50,42 +50,49 @@ constexpr int kTopWeight = 11;  // weights are multiplied at 2^kTopWeight: up to
 constexpr int kNoValues = 1 << 20;  // shift of a tile or key whose values are all zero
 constexpr int kKeyShifts = 1 << 21; // shift of K: the tile's keys have shifts of their own
 
-// Planes of FP32 K and V, cut in two: for each K/V head and tile [K hi, K lo,
-// V hi, V lo][64][DP] FP16, zeros beyond the sequence and beyond D, and the
-// shifts of K and V.  One shift for 64 keys leaves each its bits as long as
-// their largest magnitudes are within 1 / kSpread of each other: an element is
-// then off by no more than 2^-22 of itself or 2^-27 of its key's largest.
-// Tiles whose keys differ by more, of which a row may see the small ones
-// alone, or weigh them alone, have a shift for each key.  key_shifts ([K,
-// V][64]) has every key's, also those of a tile that are alike.
+// FP32 K and V, cut in two: of each K/V head and key, in the order of the packed
+// keys, [K hi, K lo, V hi, V lo][DP] FP16, zeros beyond D; each sequence's tiles
+// begin with its first key, and what its last one holds beyond its end are the
+// next sequence's keys, or zeros behind the last.  And the shifts of K and V of
+// each tile (sequence s's begin at cu_k[s] / 64 + s).  One shift for 64 keys
+// leaves each its bits as long as their largest magnitudes are within 1 /
+// kSpread of each other: an element is then off by no more than 2^-22 of itself
+// or 2^-27 of its key's largest.  Tiles whose keys differ by more, of which a
+// row may see the small ones alone, or weigh them alone, have a shift for each
+// key.  key_shifts has every key's, also those of a tile that are alike.
 struct Planes {
-    char *tiles;
-    int32_t *shifts, *key_shifts;
-    int64_t slots;  // tiles of a head: sequence s starts at cu_k[s] / 64 + s
+    char *keys;                    // [Hkv][count]
+    int32_t *shifts, *key_shifts;  // [Hkv][slots][K, V], [Hkv][count][K, V]
+    int64_t count, slots;
 };
 
 constexpr float kSpread = 0x1p-12f;
 
-template <int DP>
-__host__ __device__ constexpr int64_t tile_bytes(int planes) { return (int64_t)2 * planes * kTile * DP * 2; }
+constexpr int plane_key_bytes(int dp) { return 4 * 2 * dp; }
 
 // ---- Where a tile's rows are ------------------------------------------------------
 
 // Row row0 + lr of a tile (row0 the same for the wave), 16-byte chunk `chunk`:
-// where it is, as an address of the wave's and a 32-bit offset.
+// where it is, as an address of the tile's, an offset of the wave's and one of
+// the lane's (32 bits each).
 struct PlaneSource {
     static constexpr bool kWaveBase = true;
-    const char *tiles;      // of this head and sequence
+    const char *keys;       // of this head and sequence
     const int32_t *shifts, *key_shifts;
     int last;               // a tile beyond the last repeats it: no row sees it
     __device__ __forceinline__ int page(int, int, int) const { return 0; }
     template <int DP>
-    __device__ __forceinline__ const char *base(int value, int plane, int tile, int row0) const
+    __device__ __forceinline__ const char *base(int, int tile) const
     {
-        return tiles + (int64_t)min(tile, last) * tile_bytes<DP>(2) + ((value * 2 + plane) * kTile + row0) * (DP * 2);
+        return keys + (int64_t)min(tile, last) * (kTile * plane_key_bytes(DP));
     }
     template <int DP>
-    __device__ __forceinline__ uint32_t offset(int, int, int, int lr, int chunk) const { return lr * (DP * 2) + chunk * 16; }
+    __device__ __forceinline__ uint32_t wave_offset(int value, int plane, int row0) const
+    {
+        return row0 * plane_key_bytes(DP) + (value * 2 + plane) * (DP * 2);
+    }
+    template <int DP>
+    __device__ __forceinline__ uint32_t offset(int, int, int, int lr, int chunk) const { return lr * plane_key_bytes(DP) + chunk * 16; }
     // A scalar load: a vector load would be waited for behind the tiles on their way.
     __device__ __forceinline__ int shift(int value, int tile) const
     {
@@ -110,10 +117,8 @@ struct PlaneSource {
             s = ask(t);
         }
     }
-    __device__ __forceinline__ const int32_t *shifts_of(int value, int tile) const
-    {
-        return key_shifts + (2 * min(tile, last) + value) * kTile;
-    }
+    // [64], K and V in turn
+    __device__ __forceinline__ const int32_t *shifts_of(int tile) const { return key_shifts + 2 * kTile * (int64_t)min(tile, last); }
 };
 
 struct PackedSource {
@@ -123,11 +128,13 @@ struct PackedSource {
     int last, chunks;       // a key or chunk beyond the last repeats one: it meets a weight or an element of 0
     __device__ __forceinline__ int page(int, int, int) const { return 0; }
     template <int DP>
-    __device__ __forceinline__ const char *base(int value, int, int tile, int) const
+    __device__ __forceinline__ const char *base(int value, int tile) const
     {
         const int64_t j0 = min(tile, last / kTile) * kTile;
         return value ? v + j0 * v_tok : k + j0 * k_tok;
     }
+    template <int DP>
+    __device__ __forceinline__ uint32_t wave_offset(int, int, int) const { return 0; }
     template <int DP>
     __device__ __forceinline__ uint32_t offset(int value, int tile, int row0, int lr, int chunk) const
     {
@@ -225,9 +232,10 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
         CFP32_LDS void *to_lds = (CFP32_LDS void *)(buf + p * PLANE + piece * 64);
         if constexpr (Source::kWaveBase) {
             // (A global load to LDS would make the compiler wait for every read of LDS before it uses one.)
-            const char *base = src.template base<DP>(value, p, tile, row0);
+            const char *base = src.template base<DP>(value, tile);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void *)base, 0, -1, 0x00020000), to_lds, 16,
-                                                     src.template offset<DP>(value, tile, row0, lr, c), 0, 0, 0);
+                                                     src.template offset<DP>(value, tile, row0, lr, c),
+                                                     src.template wave_offset<DP>(value, p, row0), 0, 0);
         } else {
             __builtin_amdgcn_global_load_lds((const CFP32_GLOBAL void *)src.template at<DP>(value, tile, row0, lr, c, at_page),
                                              to_lds, 16, 0, 0);
@@ -353,14 +361,14 @@ __device__ __forceinline__ void attend_tiles(Row q_row, bool q_wide, int D, int 
             // Key by key, and the weights' sum by itself: those for the values may leave FP32's range.
             auto by_key = [&](int value, auto change) {
                 const CFP32_GLOBAL int32_t *shifts = nullptr;
-                if constexpr (PL == 2) shifts = (const CFP32_GLOBAL int32_t *)src.shifts_of(value, tile) + 4 * half;
+                if constexpr (PL == 2) shifts = (const CFP32_GLOBAL int32_t *)src.shifts_of(tile) + 8 * half + value;
                 asm("" : "+v"(shifts));  // read again each time, four at a time: kept, they would need registers
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int key = 32 * b + 8 * (r / 4) + r % 4;
-                        s[b][r] = change(s[b][r], key, shifts[key]);
+                        s[b][r] = change(s[b][r], key, shifts[2 * key]);
                         if (r % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                     }
             };
@@ -676,9 +684,9 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_tile_kernel(PromptArgs a, P
     if (t0 >= t1) {
         no_rows<DP>(w);
     } else if constexpr (PL == 2) {
-        const int64_t slot = kh * planes.slots + sq.k0 / kTile + sid;
-        const PlaneSource src = {planes.tiles + slot * tile_bytes<DP>(2), planes.shifts + 2 * slot,
-                                 planes.key_shifts + 2 * kTile * slot, t1 - 1};
+        const int64_t key = kh * planes.count + sq.k0;
+        const PlaneSource src = {planes.keys + key * plane_key_bytes(DP), planes.shifts + 2 * (kh * planes.slots + sq.k0 / kTile + sid),
+                                 planes.key_shifts + 2 * key, t1 - 1};
         attend_tiles<DP, PL, NW, 7>(q_row, q_wide, a.D, limit, a.scale, t0, t1, src, k0, k1, v0, v1, w);
     } else {
         const PackedSource src = {(const char *)((const T *)a.k.data + sq.k0 * a.k.tok + kh * a.k.head),
@@ -824,7 +832,8 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
     const Sequence sq = sequence(a, sid);
     const int64_t j0 = (blockIdx.x - start) * kTile;
     if (blockIdx.x < start || j0 >= sq.nk) return;
-    const int64_t slot = kh * planes.slots + blockIdx.x;
+    const int64_t slot = kh * planes.slots + blockIdx.x, key0 = kh * planes.count + sq.k0 + j0;
+    const int64_t behind = min(max(a.cu_k[a.S], 0), a.Tk) - sq.k0 - j0;  // rows from here on are no sequence's
     const bool wide = a.D % 4 == 0 &&
                       ((reinterpret_cast<uintptr_t>(a.k.data) | reinterpret_cast<uintptr_t>(a.v.data) |
                         (uintptr_t)((a.k.tok | a.k.head | a.v.tok | a.v.head) * 4)) & 15) == 0;
@@ -883,7 +892,6 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
         top[value] = fmaxf(fmaxf(most[value][0], most[value][1]), fmaxf(most[value][2], most[value][3]));
         each |= fminf(fminf(least[value][0], least[value][1]), fminf(least[value][2], least[value][3])) < top[value] * kSpread;
     }
-    char *tile = planes.tiles + slot * tile_bytes<DP>(2);
 #pragma unroll
     for (int value = 0; value < 2; ++value) {
         const int all = top_shift(top[value]);
@@ -891,10 +899,11 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
             planes.shifts[2 * slot + value] = each ? (value ? 0 : kKeyShifts) : value && top[1] == 0.0f ? kNoValues : all;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int at = threadIdx.x + 256 * i;
+            const int at = threadIdx.x + 256 * i, row = at / CH;
+            if (j0 + row >= sq.nk && row < behind) continue;  // the next sequence's
             const int e2 = each ? top_shift(key_mx[value][i]) : all;
             if (at % CH == 0)
-                planes.key_shifts[(2 * slot + value) * kTile + at / CH] = value && key_mx[1][i] == 0.0f ? kNoValues : e2;
+                planes.key_shifts[2 * (key0 + row) + value] = value && key_mx[1][i] == 0.0f ? kNoValues : e2;
             half8_t hi, lo;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -902,9 +911,9 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
                 split_scaled(x[value][i][e], e2, h, w);
                 hi[e] = h, lo[e] = w;
             }
-            char *to = tile + (int64_t)value * 2 * kTile * DP * 2 + at * 16;
+            char *to = planes.keys + (key0 + row) * plane_key_bytes(DP) + value * 2 * (DP * 2) + at % CH * 16;
             *reinterpret_cast<half8_t *>(to) = hi;
-            *reinterpret_cast<half8_t *>(to + kTile * DP * 2) = lo;
+            *reinterpret_cast<half8_t *>(to + DP * 2) = lo;
         }
     }
 }
@@ -913,9 +922,12 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
 
 namespace {
 
-int64_t plane_bytes(int64_t slots, int64_t Hkv, int64_t D)
+// Of a packed batch's planes: how many keys (a tile may reach 63 beyond the last) and tiles there are, ...
+Planes planes_for(int64_t S, int64_t Tk) { return {nullptr, nullptr, nullptr, Tk + kTile, Tk / kTile + S}; }
+// ... and their bytes.
+int64_t plane_bytes(const Planes &p, int64_t Hkv, int64_t D)
 {
-    const int64_t n = slots * Hkv * ((D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)) + 8 * (1 + kTile));
+    const int64_t n = Hkv * (p.count * (plane_key_bytes(D <= 64 ? 64 : 128) + 8) + p.slots * 8);
     return (n + 255) & ~(int64_t)255;
 }
 
@@ -939,7 +951,7 @@ size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool
 {
     // Whatever the rows are, blocks of 128 of them and parts make no more than kTileBlocks.
     const size_t parts = tile_parts(S, Tk, 1) > 1 ? partial_bytes(kTileBlocks * 128 / 2, 2, D <= 64 ? 64 : 128) : 0;
-    return parts + (kv_f16 ? 0 : plane_bytes(Tk / kTile + S, Hkv, D));
+    return parts + (kv_f16 ? 0 : plane_bytes(planes_for(S, Tk), Hkv, D));
 }
 
 hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream)
@@ -948,11 +960,11 @@ hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t 
     Planes planes = {};
     char *ws = (char *)workspace;
     if (!a.kv_f16) {
-        planes.slots = a.Tk / kTile + a.S;
-        planes.tiles = ws;
-        planes.shifts = (int32_t *)(ws + planes.slots * a.Hkv * (a.D <= 64 ? tile_bytes<64>(2) : tile_bytes<128>(2)));
-        planes.key_shifts = planes.shifts + 2 * planes.slots * a.Hkv;
-        ws += plane_bytes(planes.slots, a.Hkv, a.D);
+        planes = planes_for(a.S, a.Tk);
+        planes.keys = ws;
+        planes.key_shifts = (int32_t *)(ws + planes.count * a.Hkv * plane_key_bytes(a.D <= 64 ? 64 : 128));
+        planes.shifts = planes.key_shifts + 2 * planes.count * a.Hkv;
+        ws += plane_bytes(planes, a.Hkv, a.D);
         if (planes.slots > 0x7FFFFFFF || a.Hkv > 65535) return hipErrorInvalidConfiguration;
         const dim3 grid((unsigned)planes.slots, (unsigned)a.Hkv);
         if (a.D <= 64) prompt_planes_kernel<64><<<grid, 256, 0, stream>>>(a, planes);
