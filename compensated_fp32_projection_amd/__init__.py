@@ -395,25 +395,26 @@ class Workspace:
     The library's kernels read and write the workspace asynchronously, in the
     order of the stream they are launched on, so one Workspace serves one
     stream at a time: calls on different streams that may overlap need one
-    each (the helpers' default keeps one per device and stream).  The buffer
-    is marked as used by every stream it is handed to (``record_stream``), so
-    when it grows, the caching allocator does not give the old buffer to
-    anyone else before the work queued on those streams is done."""
+    each (the helpers' default keeps one per device and stream).  A buffer is
+    memory of the stream it is first handed to, so that what the allocator
+    gave back for it is ordered with that stream's work, and is marked as used
+    by every stream it is handed to (``record_stream``), so when it grows, the
+    caching allocator does not give the old buffer to anyone else before the
+    work queued on those streams is done."""
 
     def __init__(self):
         self.buf = None
         self._lock = threading.Lock()
 
     def get(self, nbytes, device, stream=None):
-        torch = _torch()
         if nbytes == 0:
             return None
         with self._lock:
             if self.buf is None or self.buf.numel() < nbytes or self.buf.device != device:
-                self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+                self.buf = _empty(nbytes, _torch().uint8, device, stream)
             buf = self.buf
-        if stream is not None and hasattr(stream, "cuda_stream"):
-            buf.record_stream(stream)
+        if stream is not None:
+            buf.record_stream(_on(stream))
         return buf
 
 
