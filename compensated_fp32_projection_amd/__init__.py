@@ -543,19 +543,31 @@ def qkv_rotary(qkv, H: int, D: int, positions=None, theta: float = 10000.0, stre
 _helpers = None
 
 
+class _NoNative:
+    """In the place of the helpers' native form: declines every call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _native():
-    """The helpers' native form (csrc/helpers.cpp), bound to the loaded library."""
+    """The helpers' native form (csrc/helpers.cpp), bound to the loaded library;
+    where it was not built, the calls are made from Python."""
     global _helpers
     if _helpers is None:
         torch = _torch()
-        path = os.path.join(_HERE, "_helpers.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
-                               "`python -m compensated_fp32_projection_amd.build`")
         import importlib.util
-        spec = importlib.util.spec_from_file_location(__name__ + "._helpers", path)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
+        path = os.path.join(_HERE, "_helpers.so")
+        try:
+            spec = importlib.util.spec_from_file_location(__name__ + "._helpers", path)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+        except ImportError as e:
+            import warnings
+            warnings.warn(f"the native form of the attention and cache helpers is not there ({e}): their calls take "
+                          "10 to 15 us more of host time", RuntimeWarning, stacklevel=3)
+            _helpers = _NoNative()
+            return _helpers
         lib = load_library()
         names = ("cfp32_attention_prompt_workspace_bytes", "cfp32_attention_prompt",
                  "cfp32_attention_decode_workspace_bytes", "cfp32_attention_decode", "cfp32_cache_reserve",

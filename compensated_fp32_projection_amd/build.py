@@ -1,5 +1,7 @@
 """Build libcfp32.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
-the native tensor helpers (_helpers.so, host code) with g++.
+the native tensor helpers (_helpers.so, host code) with g++ where torch, the
+Python headers and g++ are there: the library needs none of them, and without
+the native form the helpers make their calls from Python.
 
     python -m compensated_fp32_projection_amd.build [--verbose] [--resource-usage]
 
@@ -19,11 +21,13 @@ import argparse
 import datetime
 import glob
 import hashlib
+import importlib.util
 import json
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -103,11 +107,20 @@ def write_build_info() -> dict:
     return info
 
 
+def helpers_lack() -> str | None:
+    """What is missing to build the native helpers, or None."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None
+
+
 def build_helpers(verbose: bool = False) -> str:
     """Compile the native form of the tensor helpers (csrc/helpers.cpp, host
     code only) against the installed torch; returns the module's path."""
-    import sysconfig
-
     import torch
     root = os.path.join(os.path.dirname(torch.__file__))
     tmp = HELPERS + ".tmp"
@@ -128,7 +141,8 @@ def build_helpers(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False, resource_usage: bool = False) -> str:
-    """Compile every HIP source into libcfp32.so, and the native helpers; returns the library path."""
+    """Compile every HIP source into libcfp32.so, and the native helpers where
+    they can be built; returns the library path."""
     tmp = LIB + ".tmp"
     cmd = [hipcc(), *FLAGS, *sources(), "-o", tmp]
     if resource_usage:
@@ -144,8 +158,14 @@ def build(verbose: bool = False, resource_usage: bool = False) -> str:
     if err.strip() and (verbose or resource_usage):
         print(err, file=sys.stderr)
     os.replace(tmp, LIB)
-    build_helpers(verbose)
+    if os.path.exists(HELPERS):  # they are bound to the calls of the library they were built beside
+        os.remove(HELPERS)
     write_build_info()
+    lack = helpers_lack()
+    if lack:
+        print(f"no {lack}: the native form of the tensor helpers is not built", file=sys.stderr)
+    else:
+        build_helpers(verbose)
     return LIB
 
 
