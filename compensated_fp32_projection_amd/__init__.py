@@ -89,6 +89,14 @@ def load_library():
         raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                            "`python -m compensated_fp32_projection_amd.build` (no CPU fallback exists)")
     lib = ctypes.CDLL(LIB_PATH)
+    # A call that uses a workspace launches several kernels over it, and calls
+    # of two threads on one stream may share the helpers' own: they are made
+    # with the interpreter's lock held (a few microseconds), as the helpers'
+    # native form makes them, so that one's launches do not fall between another's.
+    held = ctypes.PyDLL(LIB_PATH)
+    for name in ("cfp32_linear", "cfp32_linear_ex", "cfp32_linear_geglu", "cfp32_attention_prompt",
+                 "cfp32_attention_decode", "cfp32_cache_fork", "cfp32_cache_compact"):
+        setattr(lib, name, getattr(held, name))
     P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     lib.cfp32_status_string.argtypes = [I32]
     lib.cfp32_status_string.restype = ctypes.c_char_p
@@ -400,7 +408,8 @@ class Workspace:
     gave back for it is ordered with that stream's work, and is marked as used
     by every stream it is handed to (``record_stream``), so when it grows, the
     caching allocator does not give the old buffer to anyone else before the
-    work queued on those streams is done."""
+    work queued on those streams is done.  Threads that launch on one stream
+    may share one (their calls' kernels follow each other as a whole)."""
 
     def __init__(self):
         self.buf = None
@@ -574,20 +583,17 @@ def _native():
                  "cfp32_cache_append", "cfp32_cache_fork_workspace_bytes", "cfp32_cache_fork", "cfp32_cache_free",
                  "cfp32_cache_compact_workspace_bytes", "cfp32_cache_compact")
         mod.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
-                 torch._C._cuda_getCurrentRawStream, _scratch_address)
+                 torch._C._cuda_getCurrentRawStream, _scratch_buffer)
         _helpers = mod
     return _helpers
 
 
-def _scratch_address(need, index, raw):
-    """Address of the helpers' own workspace for the current stream `raw` of device `index`."""
+def _scratch_buffer(need, index, raw):
+    """The helpers' own workspace for the current stream `raw` of device
+    `index`, for the native form; None where it has to be allocated first."""
     ws = _default_ws.get((index, raw))
-    if ws is None or ws.buf is None or ws.buf.numel() < need:
-        torch = _torch()
-        device = torch.device("cuda", index)
-        return _default_workspace(device, torch.cuda.current_stream(device)).get(
-            need, device, torch.cuda.current_stream(device)).data_ptr()
-    return ws.buf.data_ptr()
+    buf = None if ws is None else ws.buf
+    return None if buf is None or buf.numel() < need else buf
 
 
 def _heads(t, dtypes, name, device):
@@ -657,11 +663,13 @@ def _empty(shape, dtype, device, stream):
 
 
 def _scratch(need, device, workspace, stream):
+    """(buffer, its address, stream handle) of a call; the buffer is held until
+    the call is made (another thread's may make the workspace grow meanwhile)."""
     st = _on(stream)
     if not need:
-        return None, _stream(st)
-    ws = (workspace or _default_workspace(device, st)).get(need, device, st)
-    return ws.data_ptr(), _stream(st)
+        return None, None, _stream(st)
+    buf = (workspace or _default_workspace(device, st)).get(need, device, st)
+    return buf, buf.data_ptr(), _stream(st)
 
 
 def attention_prompt(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None, out=None,
@@ -697,7 +705,7 @@ def attention_prompt(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float
     po = _heads(out, (torch.float32,), "out", dev)
     kv = KV_F16 if k.dtype == torch.float16 else KV_F32
     need = cfp32_attention_prompt_workspace_bytes(S, Tk, Hkv, D, kv)
-    ws, st = _scratch(need, dev, workspace, stream)
+    buf, ws, st = _scratch(need, dev, workspace, stream)
     _check(cfp32_attention_prompt(*pq, *pk, *pv, kv, cq, ck, *po, S, Tq, Tk, Hq, Hkv, D, 1 if causal else 0,
                                   D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention_prompt")
     return out
@@ -730,7 +738,7 @@ def attention_decode(q, k_pages, v_pages, table, lens, shared_pages: int = 0, sc
         raise ValueError("out has the wrong shape")
     po = _heads(out, (torch.float32,), "out", dev)
     need = cfp32_attention_decode_workspace_bytes(B, Hq, Hkv, D, W, page, shared_pages, kv)
-    ws, st = _scratch(need, dev, workspace, stream)
+    buf, ws, st = _scratch(need, dev, workspace, stream)
     _check(cfp32_attention_decode(*pq, *at, kv, P, page, pt, _ld(table), W, pl, shared_pages, *po, B, Hq, Hkv, D,
                                   D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention_decode")
     return out
@@ -826,7 +834,7 @@ def cache_fork(k_pages, v_pages, table, lens, refs, parents, missing=None, refs_
     if refs_out.shape != refs.shape or (missing is not None and not missing.numel()):
         raise ValueError("refs_out or missing has the wrong shape")
     need = cfp32_cache_fork_workspace_bytes(C)
-    ws, st = _scratch(need, dev, workspace, stream)
+    buf, ws, st = _scratch(need, dev, workspace, stream)
     _check(cfp32_cache_fork(*at, kv, P, page, Hkv, D, pt, _ld(table), pl, pr, pp, table_out.data_ptr(), W,
                             lens_out.data_ptr(), pro, pm, S, W, C, ws, need, st), "cfp32_cache_fork")
     return table_out, refs_out, lens_out
@@ -872,7 +880,7 @@ def cache_compact(k_pages, v_pages, table, refs, table_out=None, refs_out=None, 
         raise ValueError("table_out or refs_out has the wrong shape")
     live = _empty(1, torch.int32, dev, stream)
     need = cfp32_cache_compact_workspace_bytes(P)
-    ws, st = _scratch(need, dev, workspace, stream)
+    buf, ws, st = _scratch(need, dev, workspace, stream)
     _check(cfp32_cache_compact(*at, kv, P, page, Hkv, D, pt, _ld(table), pr, pto, _ld(table_out), pro,
                                live.data_ptr(), S, W, ws, need, st), "cfp32_cache_compact")
     return table_out, refs_out, live

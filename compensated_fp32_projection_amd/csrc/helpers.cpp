@@ -18,7 +18,10 @@ namespace {
 
 // The library's entry points (from the library that the package has loaded),
 // and two Python callables: the current raw stream of a device index, and the
-// address of the helpers' workspace of (bytes, device index, raw stream).
+// helpers' workspace of (bytes, device index, raw stream), None where it has to
+// be allocated first (which the Python form does).  From that callable's return
+// to the end of a call no other thread runs Python, and the buffer is held, so
+// two threads' launches over one workspace follow each other.
 struct Api {
     decltype(&cfp32_attention_prompt_workspace_bytes) prompt_ws;
     decltype(&cfp32_attention_prompt) prompt;
@@ -89,18 +92,22 @@ bool stream_of(c10::Device dev, void *&st, PyObject *&st_obj)
 }
 
 struct Call {
-    void *stream = nullptr, *ws = nullptr;
-    PyObject *st_obj = nullptr;
-    ~Call() { Py_XDECREF(st_obj); }
+    void *stream = nullptr, *ws = nullptr;  // ws null: refused by the C ABI where one is needed
+    PyObject *st_obj = nullptr, *buffer = nullptr;
+    ~Call()
+    {
+        Py_XDECREF(st_obj);
+        Py_XDECREF(buffer);
+    }
     bool ready(c10::Device dev, size_t need)
     {
         if (!stream_of(dev, stream, st_obj)) return false;
         if (!need) return true;
-        PyObject *r = PyObject_CallFunction(scratch, "niO", (Py_ssize_t)need, (int)dev.index(), st_obj);
-        if (!r) return false;
-        ws = PyLong_AsVoidPtr(r);
-        Py_DECREF(r);
-        return ws || !PyErr_Occurred();
+        buffer = PyObject_CallFunction(scratch, "niO", (Py_ssize_t)need, (int)dev.index(), st_obj);
+        if (!buffer) return false;
+        const at::Tensor *t = tensor(buffer);
+        if (t) ws = t->data_ptr();
+        return true;
     }
 };
 

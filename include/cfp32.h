@@ -56,7 +56,9 @@
  * - The library keeps no mutable state besides a per-device cache of the
  *   architecture check (and cfp32_linear_noalloc's scratch array and the
  *   cache of its address); calls from several threads are safe, except
- *   overlapping cfp32_linear_noalloc calls on one device.
+ *   overlapping cfp32_linear_noalloc calls on one device, and overlapping
+ *   calls with one workspace: a call may launch several kernels over it,
+ *   which must not be mixed with another call's, also on one stream.
  */
 #ifndef CFP32_H
 #define CFP32_H
