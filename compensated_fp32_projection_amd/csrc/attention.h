@@ -9,6 +9,10 @@
 namespace cfp32 {
 
 constexpr int kAttnMaxDim = 128;  // largest head size
+constexpr int kRows = 16;         // rows of a block of attention_rows.h
+constexpr int kTile = 64;         // keys of a tile of attention_tile.hip, ...
+constexpr int kWaveRows = 32;     // ... rows of a wave, ...
+constexpr int kPageIds = 2048;    // ... and pages of a block's keys
 
 // [tokens, heads, D] with unit stride along D: element strides of a token and a head.
 struct HeadsView {
@@ -46,9 +50,6 @@ struct DecodeArgs {
     float scale;
 };
 
-size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
-hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream);
-
 // What several blocks contribute to one row: unnormalised sums, their maxima
 // (in powers of two) and weights.  Part i of row r is entry r * slots + i.
 // Null o: one part, which goes straight to the output.
@@ -69,25 +70,58 @@ struct DecodeParts {
     Partials to;   // slots: tiles + shared + own; null o: straight to the output
 };
 
-size_t partial_bytes(int64_t rows, int slots, int dim);
-void place_partials(Partials &to, int64_t rows, void *at);
-hipError_t launch_join(const PromptArgs &a, const Partials &from, hipStream_t stream);
-hipError_t launch_join(const DecodeArgs &a, const Partials &from, hipStream_t stream);
+// Rows of up to this many parts are joined by a wave each, of more by a block.
+constexpr int kJoinByWave = 16;
+inline int64_t join_blocks(const Partials &from, int64_t rows) { return from.slots > kJoinByWave ? rows : (rows + 3) / 4; }
 
-// The form for many rows (attention_tile.hip); FP16 K and V have to allow
-// 16-byte loads, and a token's stride to be below 2^26 bytes.
-size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
-hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream);
+// FP32 K and V, cut in two: of each K/V head and key, in the order of the packed
+// keys, [K hi, K lo, V hi, V lo][DP] FP16, zeros beyond D; each sequence's tiles
+// begin with its first key, and what its last one holds beyond its end are the
+// next sequence's keys, or zeros behind the last.  And the shifts of K and V of
+// each tile (sequence s's begin at cu_k[s] / 64 + s).  One shift for 64 keys
+// leaves each its bits as long as their largest magnitudes are within 2^12 of
+// each other: an element is then off by no more than 2^-22 of itself or 2^-27
+// of its key's largest.  Tiles whose keys differ by more, of which a row may
+// see the small ones alone, or weigh them alone, have a shift for each key.
+// key_shifts has every key's, also those of a tile that are alike.
+struct Planes {
+    char *keys;                    // [Hkv][count]
+    int32_t *shifts, *key_shifts;  // [Hkv][slots][K, V], [Hkv][count][K, V]
+    int64_t count, slots;
+};
+constexpr int plane_key_bytes(int dp) { return 4 * 2 * dp; }
 
-// How many parts the shared keys of a decode make there, and the launch of
-// all of a decode whose shared keys go there (FP16 pages that allow 16-byte
-// loads, a token's stride below 2^32 bytes).
-int decode_tile_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t keys, int page_log2);
-hipError_t launch_decode_tile(const DecodeArgs &a, const DecodeParts &c, hipStream_t stream);
-
+// What attention_plans.hip decides about a call.  error: a grid that cannot be
+// launched.
+struct PromptPlan {
+    hipError_t error;
+    bool tiles;      // attention_tile.hip's kernel, else attention_rows.h's
+    bool wide;       // K and V allow 16-byte loads
+    bool eight;      // waves
+    int64_t blocks;  // of each part
+    Partials to;
+    Planes planes;   // FP32 K and V of tiles
+};
+struct DecodePlan {
+    hipError_t error;
+    bool wide;
+    DecodeParts parts;
+    int64_t blocks, tile_blocks;  // of each K/V head; with tiles, of all, and those for shared keys
+};
+PromptPlan plan_prompt(const PromptArgs &a, void *workspace);
+DecodePlan plan_decode(const DecodeArgs &a, void *workspace);
+size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16);
 size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int page_log2,
                                   int64_t shared_pages, bool kv_f16);
+
+hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream);
 hipError_t launch_attention_decode(const DecodeArgs &a, void *workspace, hipStream_t stream);
+
+// The forms for many rows (attention_tile.hip), without the join.  FP16 K and V
+// have to allow 16-byte loads, a token's stride to be below 2^26 bytes (pages:
+// 2^32).
+hipError_t launch_prompt_tile(const PromptArgs &a, const PromptPlan &p, hipStream_t stream);
+hipError_t launch_decode_tile(const DecodeArgs &a, const DecodePlan &p, hipStream_t stream);
 
 // A pool of K pages and of V pages.
 struct Pool {

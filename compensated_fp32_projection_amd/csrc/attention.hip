@@ -1,5 +1,5 @@
-// Launches of the attention calls: the kernels of few rows (attention_rows.h),
-// the joining of parts, and the choice between these and attention_tile.hip's.
+// Launches of the attention calls (as attention_plans.hip has them): the
+// kernels of few rows (attention_rows.h), and the joining of parts.
 #include "attention_rows.h"
 
 namespace cfp32 {
@@ -178,12 +178,6 @@ __global__ __launch_bounds__(64) void decode_no_pages_kernel(DecodeArgs a)
         for (int h = blockIdx.y; h < a.Hq; h += gridDim.y) attend_decode_row<float>(a, b, h);
 }
 
-bool wide(const void *p, int64_t strides, int D, bool f16)
-{
-    const int64_t eb = f16 ? 2 : 4;
-    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(strides * eb)) & 15) == 0 && D % (16 / eb) == 0;
-}
-
 }  // namespace
 
 // KERNEL<type, padded D, WIDE, waves>
@@ -213,27 +207,13 @@ bool wide(const void *p, int64_t strides, int D, bool f16)
         }                                                                                            \
     } while (0)
 
-size_t partial_bytes(int64_t rows, int slots, int dim) { return slots > 1 ? (size_t)rows * slots * (dim + 2) * 4 : 0; }
-
-void place_partials(Partials &to, int64_t rows, void *at)
-{
-    if (to.slots <= 1) return;
-    const int64_t n = rows * to.slots;
-    to.o = (float *)at;
-    to.m = to.o + n * to.dim;
-    to.l = to.m + n;
-}
-
 namespace {
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int padded(int64_t D) { return D <= 64 ? 64 : 128; }
 
 template <class Args>
 hipError_t join(const Args &a, const Partials &from, int64_t rows, hipStream_t stream)
 {
-    const bool four = from.slots > 16;
-    const unsigned blocks = (unsigned)(four ? rows : ceil_div(rows, 4));
+    const bool four = from.slots > kJoinByWave;
+    const unsigned blocks = (unsigned)join_blocks(from, rows);
 #define CFP32_JOIN(T, DP)                                                            \
     do {                                                                           \
         if (four) join_kernel<T, DP, 4><<<blocks, 256, 0, stream>>>(a, from, rows); \
@@ -250,156 +230,41 @@ hipError_t join(const Args &a, const Partials &from, int64_t rows, hipStream_t s
     return hipGetLastError();
 }
 
-// Parts are made until the grid has `target` blocks (of 4 waves), of a step
-// of all waves each (a little more than one makes no parts).
-constexpr int64_t kDecodeBlocks = 512, kPromptBlocks = 256;
-int key_parts(int64_t keys, int64_t unit, int64_t blocks, int64_t target)
-{
-    const int64_t most = 4 * keys <= 5 * unit ? 1 : ceil_div(keys, unit), want = target / (blocks ? blocks : 1);
-    return (int)(want <= 1 || most <= 1 ? 1 : most < want ? most : want);
-}
-int64_t wave_step(int64_t D) { return D <= 64 ? 64 : 32; }
-
-// Blocks of eight waves where that makes their keys one step instead of two
-// (400 x 12 x 64 FP32 14.4 -> 12.5 us, 130 keys x 32/8 x 128 FP16 11.2 -> 9.3);
-// with more keys than that, or fewer, four are as good or better (500 x 16/2 x
-// 128 FP16 20 against 26 us).
-bool eight_waves(int64_t keys, int64_t D) { return keys > 4 * wave_step(D) && keys <= 8 * wave_step(D); }
-
-// How many parts the keys of a short prompt make: by the average sequence's.
-int prompt_parts(int64_t S, int64_t Tk, int64_t blocks, int64_t D)
-{
-    return key_parts(ceil_div(Tk, S), 4 * wave_step(D), blocks, kPromptBlocks);
-}
-
-// Which kernel a prompt goes through, by estimates in microseconds beyond what
-// both have in common: here FP32 matrix products (45 TFLOP/s of the useful
-// ones, 75 with FP16 keys) and the blocks, there the way through the longest
-// sequence's tiles and what comes before (for FP32 K and V a pass over them).
-// Measured, 16 rows to a block against tiles: FP32 500 / 750 / 1000 x 12 x 64
-// 17 / 26 / 38 against 25 / 30 / 36 us, 300 / 500 x 32/8 x 128 26 / 48 against
-// 31 / 38; FP16 500 / 1500 x 12 x 64 13 / 38 against 17 / 34, 300 / 500 x 32/8 x
-// 128 20 / 33 against 21 / 25, 8 x 60 and 4 x 100 of these 19 and 17 against 14
-// and 14, 50 after 700 16 against 20.
-bool prefer_tiles(const PromptArgs &a, int64_t units)
-{
-    const double keys = (double)a.Tk / a.S, seen = a.causal ? keys - 0.5 * a.Tq / a.S : keys;
-    const double gflop = 4e-9 * a.D * a.Hq * a.Tq * (seen > 0 ? seen : 0), tiles = keys / 64;
-    const double rows_us = gflop * (a.kv_f16 ? 1e3 / 75 : 1e3 / 45) + 0.008 * units * a.Hkv;
-    const double tiles_us = a.kv_f16 ? (a.D <= 64 ? 4 + 1.1 * tiles : 4 + 2 * tiles) : (a.D <= 64 ? 6 + 1.7 * tiles : 10 + 3 * tiles);
-    return rows_us > tiles_us;
-}
-
 }  // namespace
-
-hipError_t launch_join(const PromptArgs &a, const Partials &from, hipStream_t stream)
-{
-    return join(a, from, (int64_t)a.Tq * a.Hq, stream);
-}
-hipError_t launch_join(const DecodeArgs &a, const Partials &from, hipStream_t stream)
-{
-    return join(a, from, (int64_t)a.B * a.Hq, stream);
-}
-
-size_t attention_prompt_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16)
-{
-    // Whatever the rows are, blocks of kRows of them and parts make no more than kPromptBlocks.
-    const size_t parts = prompt_parts(S, Tk, 1, D) > 1 ? partial_bytes(kPromptBlocks * kRows / 2, 2, padded(D)) : 0;
-    const size_t tiles = prompt_tile_workspace(S, Tk, Hkv, D, kv_f16);
-    return parts > tiles ? parts : tiles;
-}
 
 hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStream_t stream)
 {
-    const int g = a.Hq / a.Hkv;
-    const int64_t units = (int64_t)a.Tq * g / kRows + a.S, rows = (int64_t)a.Tq * a.Hq;
-    if (units > 0x7FFFFFFF / a.Hkv || rows > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    const bool w = wide(a.k.data, a.k.tok | a.k.head, a.D, a.kv_f16) && wide(a.v.data, a.v.tok | a.v.head, a.D, a.kv_f16);
-    const bool can = a.Tk > 0 && (!a.kv_f16 || (w && a.k.tok < ((int64_t)1 << 25) && a.v.tok < ((int64_t)1 << 25)));
-    if (can && prefer_tiles(a, units)) return launch_prompt_tile(a, workspace, stream);
-    Partials to = {nullptr, nullptr, nullptr, prompt_parts(a.S, a.Tk, units * a.Hkv, a.D), padded(a.D)};
-    const bool eight = eight_waves(ceil_div(a.Tk, (int64_t)a.S * to.slots), a.D);
-    place_partials(to, rows, workspace);
-    const dim3 grid((unsigned)(units * a.Hkv), (unsigned)to.slots);
-    CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, w, eight, grid, a, to);
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess || !to.o ? e : launch_join(a, to, stream);
-}
-
-namespace {
-
-// Which kernel takes the keys that all sequences share: estimates in
-// microseconds, of this one by its groups of 16 rows, of attention_tile.hip's
-// by its blocks of 128.  Measured, this against that, FP16 pages: 32 x 32/8 x
-// 128 behind 320 / 1280 / 5120 / 20480 keys 22 / 33 / 50 / 117 against 29 / 30 /
-// 33 / 45 us; 12 of these behind 1280 / 5120 18 / 35 against 24 / 26; 10 x 16/2
-// x 128 behind 5120 / 20480 18 / 34 against 20 / 25; 16 x 14/2 x 64 behind 1280 /
-// 5120 / 20480 12 / 16 / 29 against 15 / 16 / 18.
-bool prefer_tiles(int64_t rows, int64_t Hkv, int64_t D, int64_t keys)
-{
-    const double k = 1e-3 * (double)keys * Hkv, groups = (double)ceil_div(rows, kRows), blocks = (double)ceil_div(rows, 128);
-    return D <= 64 ? 0.06 * groups * k > 3 + 0.1 * blocks * k : 0.13 * groups * k > 8 + 0.13 * blocks * k;
-}
-
-// `tiles`: the pages allow the other kernel.
-DecodeParts decode_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int lg, int64_t shared_pages, bool tiles)
-{
-    DecodeParts c = {};
-    const int64_t g = Hq / Hkv, unit = 4 * wave_step(D);
-    const int64_t n_shared = B > 1 ? shared_pages << lg : 0, n_own = (W << lg) - n_shared;
-    c.shared_groups = (int)ceil_div(B * g, kRows);
-    c.own_groups = (int)ceil_div(g, kRows);
-    c.own_from = (int)n_shared;
-    if (n_shared) {
-        if (tiles && prefer_tiles(B * g, Hkv, D, n_shared)) c.tiles = decode_tile_parts(B, Hq, Hkv, n_shared, lg);
-        else c.shared = key_parts(n_shared, unit, c.shared_groups * Hkv, kDecodeBlocks);
+    const PromptPlan p = plan_prompt(a, workspace);
+    if (p.error != hipSuccess) return p.error;
+    hipError_t e;
+    if (p.tiles) {
+        e = launch_prompt_tile(a, p, stream);
+    } else {
+        const dim3 grid((unsigned)p.blocks, (unsigned)p.to.slots);
+        CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, p.wide, p.eight, grid, a, p.to);
+        e = hipGetLastError();
     }
-    if (n_own > 0) c.own = key_parts(n_own, unit, B * c.own_groups * Hkv, kDecodeBlocks);
-    // Tiles always leave their rows in slots: beside a single part, an empty one.
-    if (c.shared + c.own == 0 && c.tiles <= 1) c.own = 1;
-    c.eight = c.tiles == 0 && c.shared == 0 && c.own == 1 && eight_waves(n_own, D);
-    c.to.slots = c.tiles + c.shared + c.own;
-    c.to.dim = padded(D);
-    return c;
-}
-
-}  // namespace
-
-size_t attention_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int lg, int64_t shared_pages,
-                                  bool kv_f16)
-{
-    if (Hkv == 0) return 0;
-    const size_t a = partial_bytes(B * Hq, decode_parts(B, Hq, Hkv, D, W, lg, shared_pages, false).to.slots, padded(D));
-    if (!kv_f16) return a;
-    const size_t b = partial_bytes(B * Hq, decode_parts(B, Hq, Hkv, D, W, lg, shared_pages, true).to.slots, padded(D));
-    return a > b ? a : b;
+    return e != hipSuccess || !p.to.o ? e : join(a, p.to, (int64_t)a.Tq * a.Hq, stream);
 }
 
 hipError_t launch_attention_decode(const DecodeArgs &a, void *workspace, hipStream_t stream)
 {
-    if (a.Hkv > 65535) return hipErrorInvalidConfiguration;
+    const DecodePlan p = plan_decode(a, workspace);
+    if (p.error != hipSuccess) return p.error;
     if (a.P == 0) {
         const dim3 grid((unsigned)(a.B < 65536 ? a.B : 65536), (unsigned)(a.Hq < 65535 ? a.Hq : 65535));
         decode_no_pages_kernel<<<grid, 64, 0, stream>>>(a);
         return hipGetLastError();
     }
-    const bool w = wide(a.k.data, a.k.page | a.k.head | a.k.tok, a.D, a.kv_f16) &&
-                   wide(a.v.data, a.v.page | a.v.head | a.v.tok, a.D, a.kv_f16);
-    const bool tiles = a.kv_f16 && w && a.k.tok < ((int64_t)1 << 31) && a.v.tok < ((int64_t)1 << 31);
-    DecodeParts c = decode_parts(a.B, a.Hq, a.Hkv, a.D, a.W, a.page_log2, a.shared_pages, tiles);
-    const int64_t rows = (int64_t)a.B * a.Hq;
-    const int64_t blocks = (int64_t)c.shared * c.shared_groups + (int64_t)a.B * c.own_groups * c.own;
-    if (blocks > 0x7FFFFFFF || rows > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    place_partials(c.to, rows, workspace);
     hipError_t e;
-    if (c.tiles) {
-        e = launch_decode_tile(a, c, stream);
+    if (p.parts.tiles) {
+        e = launch_decode_tile(a, p, stream);
     } else {
-        const dim3 grid((unsigned)blocks, (unsigned)a.Hkv);
-        CFP32_BY_TYPE(decode_rows_kernel, a.kv_f16, a.D, w, c.eight, grid, a, c);
+        const dim3 grid((unsigned)p.blocks, (unsigned)a.Hkv);
+        CFP32_BY_TYPE(decode_rows_kernel, a.kv_f16, a.D, p.wide, p.parts.eight, grid, a, p.parts);
         e = hipGetLastError();
     }
-    return e != hipSuccess || !c.to.o ? e : launch_join(a, c.to, stream);
+    return e != hipSuccess || !p.parts.to.o ? e : join(a, p.parts.to, (int64_t)a.B * a.Hq, stream);
 }
 
 }  // namespace cfp32

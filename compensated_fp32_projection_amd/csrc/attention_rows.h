@@ -27,8 +27,6 @@ namespace cfp32 {
 
 namespace {
 
-constexpr int kRows = 16;
-
 // Where a block's keys are: packed rows, ...
 struct PackedKeys {
     const char *k, *v;       // key 0 of the head

@@ -44,31 +44,13 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef float float2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = 64;       // keys of a tile
-constexpr int kWaveRows = 32;
 constexpr int kTopWeight = 11;  // weights are multiplied at 2^kTopWeight: up to 2^(kTopWeight + kLazy) = 2^15
 constexpr int kNoValues = 1 << 20;  // shift of a tile or key whose values are all zero
 constexpr int kKeyShifts = 1 << 21; // shift of K: the tile's keys have shifts of their own
 
-// FP32 K and V, cut in two: of each K/V head and key, in the order of the packed
-// keys, [K hi, K lo, V hi, V lo][DP] FP16, zeros beyond D; each sequence's tiles
-// begin with its first key, and what its last one holds beyond its end are the
-// next sequence's keys, or zeros behind the last.  And the shifts of K and V of
-// each tile (sequence s's begin at cu_k[s] / 64 + s).  One shift for 64 keys
-// leaves each its bits as long as their largest magnitudes are within 1 /
-// kSpread of each other: an element is then off by no more than 2^-22 of itself
-// or 2^-27 of its key's largest.  Tiles whose keys differ by more, of which a
-// row may see the small ones alone, or weigh them alone, have a shift for each
-// key.  key_shifts has every key's, also those of a tile that are alike.
-struct Planes {
-    char *keys;                    // [Hkv][count]
-    int32_t *shifts, *key_shifts;  // [Hkv][slots][K, V], [Hkv][count][K, V]
-    int64_t count, slots;
-};
-
+// One shift for 64 keys where the largest magnitudes of those that are not zero
+// are within 1 / kSpread of each other (see Planes).
 constexpr float kSpread = 0x1p-12f;
-
-constexpr int plane_key_bytes(int dp) { return 4 * 2 * dp; }
 
 // ---- Where a tile's rows are ------------------------------------------------------
 
@@ -143,8 +125,6 @@ struct PackedSource {
     }
     __device__ __forceinline__ int shift(int, int) const { return 0; }
 };
-
-constexpr int kPageIds = 2048;  // pages of a block's keys
 
 // A row has the address of its page, looked up (page) before the loads of several rows.
 struct PagedSource {
@@ -920,113 +900,37 @@ __global__ __launch_bounds__(256) void prompt_planes_kernel(PromptArgs a, Planes
 
 }  // namespace
 
-namespace {
-
-// Of a packed batch's planes: how many keys (a tile may reach 63 beyond the last) and tiles there are, ...
-Planes planes_for(int64_t S, int64_t Tk) { return {nullptr, nullptr, nullptr, Tk + kTile, Tk / kTile + S}; }
-// ... and their bytes.
-int64_t plane_bytes(const Planes &p, int64_t Hkv, int64_t D)
+hipError_t launch_prompt_tile(const PromptArgs &a, const PromptPlan &p, hipStream_t stream)
 {
-    const int64_t n = Hkv * (p.count * (plane_key_bytes(D <= 64 ? 64 : 128) + 8) + p.slots * 8);
-    return (n + 255) & ~(int64_t)255;
-}
-
-// Where blocks of 128 rows are few, their keys make parts of at least
-// kPartTiles tiles for the average sequence, up to 512 blocks for long ones
-// (2048 x 12 x 64 FP32, 204 blocks: 68 -> 60 us), up to 320 for shorter (1500 x
-// 12 x 64, 144 blocks: 55 -> 46; with 200 to 256 blocks of 1000 keys two parts
-// cost more than they gave: x 32/8 x 128 FP16 43 -> 53 us; and so did parts of
-// four tiles: 4 x 300 x 12 x 64 FP16 after 100 each 16 -> 25 us).
-constexpr int64_t kTileBlocks = 512, kPartTiles = 8;
-int tile_parts(int64_t S, int64_t Tk, int64_t blocks)
-{
-    const int64_t most = (Tk / S + kPartTiles * kTile - 1) / (kPartTiles * kTile);
-    const int64_t want = (Tk / S >= 24 * kTile ? kTileBlocks : 320) / blocks;
-    return (int)(want <= 1 || most <= 1 ? 1 : most < want ? most : want);
-}
-
-}  // namespace
-
-size_t prompt_tile_workspace(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, bool kv_f16)
-{
-    // Whatever the rows are, blocks of 128 of them and parts make no more than kTileBlocks.
-    const size_t parts = tile_parts(S, Tk, 1) > 1 ? partial_bytes(kTileBlocks * 128 / 2, 2, D <= 64 ? 64 : 128) : 0;
-    return parts + (kv_f16 ? 0 : plane_bytes(planes_for(S, Tk), Hkv, D));
-}
-
-hipError_t launch_prompt_tile(const PromptArgs &a, void *workspace, hipStream_t stream)
-{
-    const int g = a.Hq / a.Hkv;
-    Planes planes = {};
-    char *ws = (char *)workspace;
     if (!a.kv_f16) {
-        planes = planes_for(a.S, a.Tk);
-        planes.keys = ws;
-        planes.key_shifts = (int32_t *)(ws + planes.count * a.Hkv * plane_key_bytes(a.D <= 64 ? 64 : 128));
-        planes.shifts = planes.key_shifts + 2 * planes.count * a.Hkv;
-        ws += plane_bytes(planes, a.Hkv, a.D);
-        if (planes.slots > 0x7FFFFFFF || a.Hkv > 65535) return hipErrorInvalidConfiguration;
-        const dim3 grid((unsigned)planes.slots, (unsigned)a.Hkv);
-        if (a.D <= 64) prompt_planes_kernel<64><<<grid, 256, 0, stream>>>(a, planes);
-        else prompt_planes_kernel<128><<<grid, 256, 0, stream>>>(a, planes);
+        const dim3 grid((unsigned)p.planes.slots, (unsigned)a.Hkv);
+        if (a.D <= 64) prompt_planes_kernel<64><<<grid, 256, 0, stream>>>(a, p.planes);
+        else prompt_planes_kernel<128><<<grid, 256, 0, stream>>>(a, p.planes);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    const int64_t blocks = ((int64_t)a.Tq * g / 128 + a.S) * a.Hkv;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    Partials to = {nullptr, nullptr, nullptr, tile_parts(a.S, a.Tk, blocks), a.D <= 64 ? 64 : 128};
-    place_partials(to, (int64_t)a.Tq * a.Hq, ws);
-    // Eight waves multiply and make weights at the same time; four give more
-    // and shorter blocks.  Two blocks of four to a CU and not more: four
-    // (1024 x 32/8 x 128 FP16 52 -> 43 us, FP32 77 -> 66; 8192: 903 -> 955 and
-    // 1321 -> 1572).  Where two of them fit a CU's LDS together, also for up
-    // to four and for short sequences, whose blocks are mostly beginning and
-    // end (eight against four: 2 x 4000 x 12 x 64 FP16 138 / 125, 16 x 1000 of
-    // these 105 / 91, 200 x 40 92 / 49, 8 x 750 x 32/8 x 128 136 / 128, 6 x
-    // 1400 218 / 229, 4 x 2000 275 / 287, FP32 4 x 4000 x 32/8 x 64 778 / 814;
-    // where they do not fit, 8 x 750 x 32/8 x 128 FP32 189 / 227).
-    const bool together = a.kv_f16 || a.D <= 64;
-    const bool eight = blocks > 512 && (!together || (blocks > 1024 && a.Tk / a.S > 1100));
-#define CFP32_PROMPT(T, DP, NW)                                                                                       \
-    prompt_tile_kernel<T, DP, NW><<<dim3((unsigned)(((int64_t)a.Tq * g / (NW * kWaveRows) + a.S) * a.Hkv),             \
-                                         (unsigned)to.slots), 64 * NW, 0, stream>>>(a, planes, to)
-    if (a.kv_f16 && a.D <= 64) {
-        if (eight) CFP32_PROMPT(_Float16, 64, 8);
-        else CFP32_PROMPT(_Float16, 64, 4);
-    } else if (a.kv_f16) {
-        if (eight) CFP32_PROMPT(_Float16, 128, 8);
-        else CFP32_PROMPT(_Float16, 128, 4);
-    } else if (a.D <= 64) {
-        if (eight) CFP32_PROMPT(float, 64, 8);
-        else CFP32_PROMPT(float, 64, 4);
+    const dim3 grid((unsigned)p.blocks, (unsigned)p.to.slots);
+#define CFP32_PROMPT(T, DP)                                                                            \
+    do {                                                                                               \
+        if (p.eight) prompt_tile_kernel<T, DP, 8><<<grid, 512, 0, stream>>>(a, p.planes, p.to);        \
+        else prompt_tile_kernel<T, DP, 4><<<grid, 256, 0, stream>>>(a, p.planes, p.to);                \
+    } while (0)
+    if (a.kv_f16) {
+        if (a.D <= 64) CFP32_PROMPT(_Float16, 64);
+        else CFP32_PROMPT(_Float16, 128);
     } else {
-        if (eight) CFP32_PROMPT(float, 128, 8);
-        else CFP32_PROMPT(float, 128, 4);
+        if (a.D <= 64) CFP32_PROMPT(float, 64);
+        else CFP32_PROMPT(float, 128);
     }
 #undef CFP32_PROMPT
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess || !to.o ? e : launch_join(a, to, stream);
+    return hipGetLastError();
 }
 
-int decode_tile_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t keys, int page_log2)
+hipError_t launch_decode_tile(const DecodeArgs &a, const DecodePlan &p, hipStream_t stream)
 {
-    const int64_t blocks = (B * (Hq / Hkv) + 127) / 128 * Hkv, tiles = (keys + kTile - 1) / kTile;
-    int64_t parts = 256 / blocks;  // one block to a CU, and room for the sequences' own keys beside it
-    if (parts > (tiles + 3) / 4) parts = (tiles + 3) / 4;
-    if (parts < 1) parts = 1;
-    // A part's page ids (and two tiles' more, by rounding) fit the block's list.
-    const int64_t room = ((int64_t)kPageIds - 2) << page_log2, per = room / kTile - 2;
-    const int64_t least = (tiles + per - 1) / per;
-    return (int)(parts > least ? parts : least);
-}
-
-hipError_t launch_decode_tile(const DecodeArgs &a, const DecodeParts &c, hipStream_t stream)
-{
-    const int64_t tiles = ((int64_t)a.B * (a.Hq / a.Hkv) + 127) / 128 * a.Hkv * c.tiles;
-    const int64_t blocks = tiles + (int64_t)a.B * c.own_groups * c.own * a.Hkv;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    if (a.D <= 64) decode_tile_kernel<64><<<(unsigned)blocks, 256, 0, stream>>>(a, c, (unsigned)tiles);
-    else decode_tile_kernel<128><<<(unsigned)blocks, 256, 0, stream>>>(a, c, (unsigned)tiles);
+    const unsigned blocks = (unsigned)p.blocks, tiles = (unsigned)p.tile_blocks;
+    if (a.D <= 64) decode_tile_kernel<64><<<blocks, 256, 0, stream>>>(a, p.parts, tiles);
+    else decode_tile_kernel<128><<<blocks, 256, 0, stream>>>(a, p.parts, tiles);
     return hipGetLastError();
 }
 

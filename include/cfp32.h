@@ -42,8 +42,10 @@
  * - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *   Calls are asynchronous and ordered on that stream.  Execution faults
  *   surface at the caller's next synchronisation.
- * - Arguments are validated before anything is enqueued.  A call that
- *   returns an error has enqueued nothing.
+ * - Arguments, and the grids they need, are validated before anything is
+ *   enqueued.  A call that returns an error has enqueued nothing (but where a
+ *   launch fails for a reason of the device's, CFP32_ERR_HIP, the launches
+ *   before it).
  * - Every dimension, and every rows x ld extent of an operand, must be
  *   below 2^48 elements; larger values give CFP32_ERR_INVALID_VALUE.
  * - M == 0 or N == 0 (rows == 0 or cols == 0 for split) is a no-op that
