@@ -1,6 +1,8 @@
 // C ABI of the attention and cache calls (declared in include/cfp32.h):
 // argument validation, the device check and workspace sizes.  Every call
 // validates all of its arguments before it enqueues anything.
+#include <cmath>
+
 #include "api_common.h"
 #include "attention.h"
 
@@ -18,6 +20,7 @@ bool heads_ok(int64_t Hq, int64_t Hkv, int64_t D)
 {
     return size_ok(Hq) && size_ok(Hkv) && size_ok(D) && D <= cfp32::kAttnMaxDim && (Hkv == 0 ? Hq == 0 : Hq % Hkv == 0);
 }
+bool scale_ok(double scale) { return std::isfinite((float)scale); }  // as the kernels take it
 bool type_ok(int t) { return t == CFP32_KV_F32 || t == CFP32_KV_F16; }
 
 // log2 of a page size, -1 if it is not a power of two up to 65536.
@@ -114,7 +117,7 @@ cfp32_status cfp32_attention_prompt(const float *q, int64_t q_tok, int64_t q_hea
         !view_ok(Tk, v_tok, Hkv, v_head, 1, 0, D) || !view_ok(Tq, out_tok, Hq, out_head, 1, 0, D) ||
         !distinct_ok(Tq, out_tok, Hq, out_head, 1, 0, D))
         return CFP32_ERR_INVALID_VALUE;
-    if (!(scale - scale == 0.0)) return CFP32_ERR_INVALID_VALUE;  // infinite or NaN
+    if (!scale_ok(scale)) return CFP32_ERR_INVALID_VALUE;
     if (Tk > 0 && Hkv > (kMaxDim >> 12) / (Tk / 64 + S)) return CFP32_ERR_INVALID_VALUE;
     const size_t need = cfp32_attention_prompt_workspace_bytes(S, Tk, Hkv, D, kv_type);
     if (need && (!workspace || workspace_bytes < need)) return CFP32_ERR_INVALID_VALUE;
@@ -158,7 +161,7 @@ cfp32_status cfp32_attention_decode(const float *q, int64_t q_seq, int64_t q_hea
     if (!aligned_to(q, 4) || !aligned_to(out, 4) || !view_ok(B, q_seq, Hq, q_head, 1, 0, D) ||
         !view_ok(B, out_seq, Hq, out_head, 1, 0, D) || !distinct_ok(B, out_seq, Hq, out_head, 1, 0, D))
         return CFP32_ERR_INVALID_VALUE;
-    if (!(scale - scale == 0.0)) return CFP32_ERR_INVALID_VALUE;
+    if (!scale_ok(scale)) return CFP32_ERR_INVALID_VALUE;
     const size_t need = cfp32_attention_decode_workspace_bytes(B, Hq, Hkv, D, W, page, shared_pages, kv_type);
     if (need && (!workspace || workspace_bytes < need)) return CFP32_ERR_INVALID_VALUE;
     cfp32_status st = api_check_device();

@@ -382,7 +382,7 @@ CFP32_API size_t cfp32_attention_prompt_workspace_bytes(int64_t S, int64_t Tk, i
  *   cu_q, cu_k : int32 [S + 1]: sequence s has query rows cu_q[s] ..
  *                cu_q[s+1] - 1 and keys cu_k[s] .. cu_k[s+1] - 1
  *                (non-decreasing, within [0, Tq] and [0, Tk]).
- *   scale      : factor on q . k.
+ *   scale      : factor on q . k, of a finite FP32 value.
  * Row i of a sequence with Lq rows and Lk keys sees all of its keys, or with
  * `causal` those at j <= i + Lk - Lq (the last row sees the last key: Lk > Lq
  * continues a cached prefix).  out = softmax(scale q K^T) V over the keys a
