@@ -129,6 +129,20 @@ struct Pool {
     int P, page_log2, Hkv, D, elem_bytes;
 };
 
+// How pages are moved: a tensor of a pool as rows of `vecs` vectors, n1 x n2 rows to a page.
+struct PageRows {
+    char *data;
+    int64_t page, s1, s2;  // bytes
+};
+struct PageShape {
+    PageRows k, v;
+    int64_t rows;          // of a page: n1 * n2
+    int n2;
+    int64_t vecs;          // vectors of a row
+    int vec_bytes;
+};
+PageShape page_shape(const Pool &p);
+
 hipError_t launch_cache_reserve(const int32_t *table, int64_t ld, const int32_t *lens, const int32_t *cu,
                                 const int32_t *refs, int32_t *table_out, int64_t ld_out, int32_t *refs_out,
                                 int32_t *missing, int S, int W, int P, int page_log2, hipStream_t stream);

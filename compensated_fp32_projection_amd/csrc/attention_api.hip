@@ -13,6 +13,7 @@ using cfp32::api_launched;
 
 constexpr int64_t kMaxDim = cfp32::kApiMaxDim;
 constexpr int64_t kMaxSize = 0x7FFFFFFF;  // dimensions: int32 offsets and lengths
+constexpr int64_t kMaxKeys = kMaxSize - 65535;  // of attention: int32 indices, and steps beyond the last
 constexpr size_t kAlign = 256;            // slack for rounding a workspace pointer up
 
 bool size_ok(int64_t v) { return v >= 0 && v <= kMaxSize; }
@@ -92,7 +93,7 @@ extern "C" {
 
 size_t cfp32_attention_prompt_workspace_bytes(int64_t S, int64_t Tk, int64_t Hkv, int64_t D, int kv_type)
 {
-    if (!size_ok(S) || !size_ok(Tk) || !heads_ok(Hkv, Hkv, D) || !type_ok(kv_type)) return 0;
+    if (!size_ok(S) || Tk < 0 || Tk > kMaxKeys || !heads_ok(Hkv, Hkv, D) || !type_ok(kv_type)) return 0;
     if (S == 0 || Tk == 0 || Hkv == 0 || D == 0) return 0;
     if (Hkv > (kMaxDim >> 12) / (Tk / 64 + S)) return 0;
     const size_t n = cfp32::attention_prompt_workspace(S, Tk, Hkv, D, kv_type == CFP32_KV_F16);
@@ -106,7 +107,7 @@ cfp32_status cfp32_attention_prompt(const float *q, int64_t q_tok, int64_t q_hea
                                     int64_t D, int causal, double scale, void *workspace, size_t workspace_bytes,
                                     void *stream)
 {
-    if (!size_ok(S) || !size_ok(Tq) || !size_ok(Tk) || !heads_ok(Hq, Hkv, D) || !type_ok(kv_type))
+    if (!size_ok(S) || !size_ok(Tq) || Tk < 0 || Tk > kMaxKeys || !heads_ok(Hq, Hkv, D) || !type_ok(kv_type))
         return CFP32_ERR_INVALID_VALUE;
     if (S == 0 || Tq == 0 || Hq == 0 || D == 0) return CFP32_OK;
     if (!q || !out || !cu_q || !cu_k || (Tk > 0 && (!k || !v))) return CFP32_ERR_INVALID_VALUE;
@@ -133,7 +134,7 @@ size_t cfp32_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv
                                               int64_t shared_pages, int kv_type)
 {
     const int lg = page_log2(page);
-    if (!size_ok(B) || !heads_ok(Hq, Hkv, D) || !size_ok(W) || lg < 0 || W > (kMaxSize >> lg) || !type_ok(kv_type) ||
+    if (!size_ok(B) || !heads_ok(Hq, Hkv, D) || !size_ok(W) || lg < 0 || W > (kMaxKeys >> lg) || !type_ok(kv_type) ||
         shared_pages < 0 || shared_pages > W)
         return 0;
     if (B == 0 || Hq == 0 || D == 0 || B > (kMaxDim >> 20) / Hq) return 0;
@@ -150,7 +151,7 @@ cfp32_status cfp32_attention_decode(const float *q, int64_t q_seq, int64_t q_hea
                                     size_t workspace_bytes, void *stream)
 {
     const int lg = page_log2(page);
-    if (!size_ok(B) || !heads_ok(Hq, Hkv, D) || !size_ok(W) || !size_ok(P) || lg < 0 || W > (kMaxSize >> lg) ||
+    if (!size_ok(B) || !heads_ok(Hq, Hkv, D) || !size_ok(W) || !size_ok(P) || lg < 0 || W > (kMaxKeys >> lg) ||
         !type_ok(kv_type) || shared_pages < 0 || shared_pages > W)
         return CFP32_ERR_INVALID_VALUE;
     if (B == 0 || Hq == 0 || D == 0) return CFP32_OK;

@@ -104,9 +104,9 @@ __global__ __launch_bounds__(kPlanThreads) void cache_reserve_kernel(const int32
                                                                      int64_t ld_out, int32_t *refs_out,
                                                                      int32_t *missing, int S, int W, int P, int lg)
 {
-    __shared__ int beyond;
+    __shared__ unsigned long long beyond;
     if (threadIdx.x == 0) beyond = 0;
-    for (int i = threadIdx.x; i < P; i += kPlanThreads) refs_out[i] = refs[i];
+    for (int64_t i = threadIdx.x; i < P; i += kPlanThreads) refs_out[i] = refs[i];
     const int64_t n = (int64_t)S * W;
     if (table != table_out)
         for (int64_t i = threadIdx.x; i < n; i += kPlanThreads) {
@@ -127,14 +127,14 @@ __global__ __launch_bounds__(kPlanThreads) void cache_reserve_kernel(const int32
             refs_out[p] = 1;
         });
     if (missing) {
-        int b = 0;
-        for (int s = threadIdx.x; s < S; s += kPlanThreads) {
+        unsigned long long b = 0;
+        for (int64_t s = threadIdx.x; s < S; s += kPlanThreads) {
             const int64_t m = need(s) - W;
-            b += m > 0 ? (int)m : 0;
+            b += m > 0 ? m : 0;
         }
         atomicAdd(&beyond, b);
         __syncthreads();
-        if (threadIdx.x == 0) *missing = left + beyond;
+        if (threadIdx.x == 0) *missing = (int)min(beyond + left, 0x7FFFFFFFull);
     }
 }
 
@@ -146,9 +146,9 @@ __global__ __launch_bounds__(kPlanThreads) void cache_fork_plan_kernel(const int
                                                                        int W, int C, int P, int lg, int32_t *src,
                                                                        int32_t *dst)
 {
-    for (int i = threadIdx.x; i < P; i += kPlanThreads) refs_out[i] = refs[i];
+    for (int64_t i = threadIdx.x; i < P; i += kPlanThreads) refs_out[i] = refs[i];
     const int mask = (1 << lg) - 1;
-    for (int c = threadIdx.x; c < C; c += kPlanThreads) {
+    for (int64_t c = threadIdx.x; c < C; c += kPlanThreads) {
         const int p = parents[c];
         int len = p >= 0 && p < S ? lens[p] : 0;
         len = len < 0 ? 0 : len;
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kPlanThreads) void cache_fork_plan_kernel(const int
             dst[c] = p;
             refs_out[p] = 1;
         });
-    for (int c = threadIdx.x; c < C; c += kPlanThreads)
+    for (int64_t c = threadIdx.x; c < C; c += kPlanThreads)
         if (src[c] >= 0 && dst[c] < 0) {
             lens_out[c] &= ~mask;
             src[c] = -1;
@@ -175,18 +175,6 @@ __global__ __launch_bounds__(kPlanThreads) void cache_fork_plan_kernel(const int
 }
 
 // ---- Moving pages --------------------------------------------------------------
-
-// One tensor of a pool as rows of `vecs` vectors: a page is n1 x n2 rows.
-struct PageRows {
-    char *data;
-    int64_t page, s1, s2;  // bytes
-};
-struct PageShape {
-    PageRows k, v;
-    int n2, rows;          // rows of a page: n1 * n2
-    int64_t vecs;          // vectors of a row
-    int vec_bytes;
-};
 
 typedef uint32_t vec4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t vec2_t __attribute__((ext_vector_type(2)));
@@ -245,30 +233,6 @@ __global__ __launch_bounds__(256) void cache_copy_kernel(PageShape g, const int3
         if (a < 0 || b < 0 || a >= P || b >= P) continue;
         copy_piece<V>(g, a, b, u - i * 2 * pieces, pieces);
     }
-}
-
-PageShape page_shape(const Pool &p)
-{
-    PageShape g;
-    const int64_t eb = p.elem_bytes, page = (int64_t)1 << p.page_log2;
-    auto rows = [&](const PagesView &v) { return PageRows{(char *)v.data, v.page * eb, v.head * eb, v.tok * eb}; };
-    g.k = rows(p.k), g.v = rows(p.v);
-    int64_t bytes = p.D * eb;
-    auto whole = [&](const PagesView &v) {  // every value of a page in one run
-        return (v.tok == p.D && (v.head == page * p.D || p.Hkv == 1)) || (v.head == p.D && (v.tok == p.Hkv * (int64_t)p.D || page == 1));
-    };
-    if (whole(p.k) && whole(p.v)) {
-        bytes *= p.Hkv * page;
-        g.n2 = g.rows = 1;
-    } else {
-        g.n2 = (int)page;
-        g.rows = p.Hkv * (int)page;
-    }
-    int64_t a = bytes | 16 | (int64_t)(uintptr_t)g.k.data | (int64_t)(uintptr_t)g.v.data | g.k.page | g.v.page;
-    if (g.rows > 1) a |= g.k.s1 | g.k.s2 | g.v.s1 | g.v.s2;
-    g.vec_bytes = (int)(a & -a);
-    g.vecs = bytes / g.vec_bytes;
-    return g;
 }
 
 template <class Tables>
@@ -396,7 +360,7 @@ __global__ __launch_bounds__(256) void cache_append_kernel(HeadsView k, HeadsVie
 
 __global__ __launch_bounds__(256) void cache_counts_kernel(const int32_t *refs, int32_t *refs_out, int P)
 {
-    const int i = blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < P) refs_out[i] = refs[i];
 }
 
@@ -435,17 +399,17 @@ __global__ __launch_bounds__(kPlanThreads) void cache_compact_plan_kernel(const 
 {
     __shared__ int sums[kPlanThreads / 64];
     int c = 0, n;
-    for (int i = threadIdx.x; i < P; i += kPlanThreads) c += refs[i] > 0;
+    for (int64_t i = threadIdx.x; i < P; i += kPlanThreads) c += refs[i] > 0;
     block_scan(c, sums, n);
     // The free pages below n and the live ones from n on, each in order:
     // equally many.
     int holes = 0, total;
-    for (int b = 0; b < n; b += kPlanThreads) {
-        const int i = b + threadIdx.x;
+    for (int64_t b = 0; b < n; b += kPlanThreads) {
+        const int64_t i = b + threadIdx.x;
         const bool free = i < n && refs[i] <= 0;
         const int r = holes + block_scan(free, sums, total);
-        if (i < n) map[i] = i;
-        if (free) dst[r] = i;
+        if (i < n) map[i] = (int)i;
+        if (free) dst[r] = (int)i;
         else if (i < n) refs_out[i] = refs[i];
         holes += total;
     }
@@ -539,7 +503,7 @@ hipError_t launch_cache_free(const int32_t *rows, int64_t ld, const int32_t *ref
         return hipGetLastError();
     }
     if (refs != refs_out) {
-        cache_counts_kernel<<<(P + 255) / 256, 256, 0, stream>>>(refs, refs_out, P);
+        cache_counts_kernel<<<(unsigned)(((int64_t)P + 255) / 256), 256, 0, stream>>>(refs, refs_out, P);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

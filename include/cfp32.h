@@ -354,7 +354,8 @@ CFP32_API cfp32_status cfp32_qkv_rotary(const float *qkv, int64_t ldq, const int
  * range and split into two FP16 parts; sums and softmax statistics are FP32.
  *
  * Shapes, in addition to the conventions above:
- * - Every dimension is below 2^31; Hq is a multiple of Hkv (query head h
+ * - Every dimension is below 2^31, and attention's keys (Tk, W * page) number
+ *   at most 2^31 - 2^16; Hq is a multiple of Hkv (query head h
  *   reads K/V head h / (Hq / Hkv)); 1 <= D <= 128.
  * - *_tok, *_head, *_seq and *_page are strides in elements between
  *   consecutive tokens, heads, sequences and pages; the D values of one

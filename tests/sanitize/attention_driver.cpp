@@ -1,9 +1,9 @@
 // Host-side checks of the attention and cache calls under AddressSanitizer and
 // UndefinedBehaviorSanitizer: the argument checks of attention_api.hip over
 // arguments from the ends of every range, and the plans of
-// attention_plans.hip: every part, slot and plane lies within the workspace
-// that the query asks for, without knowing the rows, and every grid is one
-// that can be launched.  Exit status 0 when every check holds.
+// attention_plans.hip and cache_plans.hip: every part, slot and plane lies
+// within the workspace that the query asks for, without knowing the rows, every
+// grid is one that can be launched, and pages are moved whole.  Exit status 0 when every check holds.
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -138,6 +138,30 @@ static void decodes()
                                 }
 }
 
+// Every value of a page is moved once, in vectors that its addresses allow.
+static void pages()
+{
+    for (int64_t d : {1l, 2l, 3l, 8l, 40l, 64l, 128l})
+        for (int64_t h : {1l, 2l, 5l, 8l, 65536l, 0x7FFFFFFFl})
+            for (int lg : {0, 1, 4, 6, 16})
+                for (int eb : {2, 4})
+                    for (int layout = 0; layout < 4; ++layout) {
+                        const int64_t page = 1l << lg, pad = layout == 3 ? d + 3 : d;
+                        if (h * page > ((1l << 47) / pad)) continue;
+                        Pool p = {};
+                        p.P = 3, p.page_log2 = lg, p.Hkv = (int)h, p.D = (int)d, p.elem_bytes = eb;
+                        const PagesView by_head = {kBase, h * page * pad, page * pad, pad}, by_tok = {kBase + eb, h * page * pad, pad, h * pad};
+                        p.k = layout == 1 ? by_tok : by_head, p.v = layout == 0 ? by_head : by_tok;
+                        const PageShape g = page_shape(p);
+                        CHECK(g.rows >= 1 && g.vecs >= 1 && g.n2 >= 1, "%ld x 2^%d x %ld", (long)h, lg, (long)d);
+                        CHECK((__int128)g.rows * g.vecs * g.vec_bytes == (__int128)h * page * d * eb, "%ld x 2^%d x %ld layout %d", (long)h, lg,
+                              (long)d, layout);
+                        CHECK(g.vec_bytes >= eb && g.vec_bytes <= 16 && (uintptr_t)p.k.data % g.vec_bytes == 0 &&
+                                  (uintptr_t)p.v.data % g.vec_bytes == 0, "vectors of %d", g.vec_bytes);
+                        if (g.rows > 1) CHECK(g.n2 == page && g.rows == h * page, "rows");
+                    }
+}
+
 // Every argument from the ends of its range; without a device no call gets further than the checks.
 static void arguments()
 {
@@ -197,6 +221,7 @@ int main(int argc, char **argv)
 {
     prompts();
     decodes();
+    pages();
     if (argc > 1 && !std::strcmp(argv[1], "no-device")) arguments();
     std::fprintf(stderr, "%ld checks, %ld failure(s)\n", checks, failures);
     return failures != 0;

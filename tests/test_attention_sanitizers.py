@@ -1,6 +1,6 @@
 """The host side of the attention and cache calls under AddressSanitizer and
 UndefinedBehaviorSanitizer, on the CPU: argument checks (attention_api.hip) and
-plans (attention_plans.hip), with launcher stubs that abort if reached
+plans (attention_plans.hip, cache_plans.hip), with launcher stubs that abort if reached
 (tests/sanitize/attention_driver.cpp)."""
 import os
 import shutil
@@ -17,7 +17,7 @@ def test_attention_host_code_under_sanitizers(tmp_path):
     san_host = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                 "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer"]
     objs = []
-    for src in ("api.hip", "plans.hip", "attention_api.hip", "attention_plans.hip"):
+    for src in ("api.hip", "plans.hip", "attention_api.hip", "attention_plans.hip", "cache_plans.hip"):
         objs.append(str(tmp_path / (src + ".o")))
         _run([hipcc, "--offload-arch=gfx950", "-std=c++17", "-O1", "-g", "-fPIC", "-ffp-contract=off", *san_host,
               "-c", os.path.join(CSRC, src), "-o", objs[-1]])
