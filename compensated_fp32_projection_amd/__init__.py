@@ -398,7 +398,7 @@ def merge(c_hi, c_lo, y=None, stream=None):
 
 
 class Workspace:
-    """Grow-only device scratch for ``linear`` and ``linear_geglu``.
+    """Grow-only device scratch for the tensor helpers that take one.
 
     The library's kernels read and write the workspace asynchronously, in the
     order of the stream they are launched on, so one Workspace serves one
@@ -409,7 +409,9 @@ class Workspace:
     by every stream it is handed to (``record_stream``), so when it grows, the
     caching allocator does not give the old buffer to anyone else before the
     work queued on those streams is done.  Threads that launch on one stream
-    may share one (their calls' kernels follow each other as a whole)."""
+    may share one (their calls' kernels follow each other as a whole).  A call
+    captured into a graph keeps the buffer's address: give it a Workspace of
+    its own that lives as long as the graph and makes no larger calls."""
 
     def __init__(self):
         self.buf = None

@@ -16,9 +16,12 @@
 //     split).
 // K of the next step is requested when its registers have been multiplied,
 // V when its have, so a step's loads are in flight during the step before.
-// These products are bounded by memory, not by the matrix units: 16 rows
-// against FP32 keys need 1024 cycles of a SIMD for 8 KiB at D = 64, which is
-// 19 TB/s over the chip.
+// 16 rows against FP32 keys need 1024 cycles of a SIMD for 8 KiB at D = 64,
+// which is 19 TB/s over the chip: a decode, whose keys come from memory, is
+// bounded by that and by its latency.  A prompt's keys come from the caches,
+// again for each 16 rows, and its FP32 products are much of its time: 512 x
+// 12 x 64 FP32 takes 15 us, of which 4 to 8 are a SIMD's matrix instructions
+// (64 keys of a wave: 128 of 32 cycles).
 #pragma once
 
 #include "attention_device.h"

@@ -421,9 +421,8 @@ CFP32_API size_t cfp32_attention_decode_workspace_bytes(int64_t B, int64_t Hq, i
  *                  (clamped to [0, W * page]); 0 gives a row of 0.
  *   shared_pages : the first shared_pages (<= W) table entries are the same
  *                  in every row (row 0's are read): the batch reads those
- *                  pages once, together.  A sequence whose length ends
- *                  inside them is right too, at the cost of reading its
- *                  pages on its own.
+ *                  pages together, once for each group of 16 or 128 rows
+ *                  (sequences x heads).  A sequence may end inside them.
  * A page id outside [0, P) where lens needs a page makes the row NaN. */
 CFP32_API cfp32_status cfp32_attention_decode(const float *q, int64_t q_seq, int64_t q_head,
                                     const void *k_pages, int64_t k_page, int64_t k_head, int64_t k_tok,
