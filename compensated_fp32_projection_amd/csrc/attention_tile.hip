@@ -8,7 +8,7 @@
 //   * Products: v_mfma_f32_32x32x16_f16 with FP32 sums.  An FP32 operand is
 //     scaled by a power of two to the top of FP16's range and split into two
 //     FP16 parts of 22 bits together (rows on the way in, weights as they are
-//     made, FP32 K and V in a pass over them beforehand, tile by tile);
+//     made, FP32 K and V in a pass over them beforehand, by tile or by key);
 //     high x high, high x low and low x high are summed, low x low (below
 //     2^-22) is not.  FP16 K and V are exact: two products.  The parts share
 //     one scale, so all products go to the same accumulators.
@@ -24,10 +24,11 @@
 //   * The running maximum is followed lazily (kLazy), so that most tiles do
 //     not touch the output sums.
 // Bound by the matrix units' power where there is enough to do: 8192 x 32/8 x
-// 128 FP32, causal, takes 1.29 ms, 1275 TFLOP/s of products (three for one)
-// with the units busy 78% of a clock that falls to 1.5 GHz.  8 x 750 of these
-// with FP16 keys take 121 us, 675 TFLOP/s (two for one): blocks of up to 18
-// tiles spend much of their time on their first one and their last stores.
+// 128 FP32, causal, takes 1.27 ms (1.40 on the warmest card), 1300 TFLOP/s of
+// products (three for one) with the units busy 77% of a clock that falls to 1.5
+// GHz.  8 x 750 of these with FP16 keys take 110 to 120 us, 680 to 740 TFLOP/s
+// (two for one): blocks of up to 18 tiles spend much of their time on their
+// first one and their last stores.
 #include <type_traits>
 
 #include "attention_rows.h"
