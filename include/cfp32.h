@@ -398,8 +398,9 @@ CFP32_API size_t cfp32_attention_prompt_workspace_bytes(int64_t S, int64_t Tk, i
  * prompts) than 2^-22 of itself or 2^-27 of the largest of its token and head,
  * and a weight (long prompts, shared prefixes) than 2^-22 of itself or 2^-36 of
  * the row's largest (with FP32 V: largest product of a weight and the largest
- * value of 64 tokens).  Tokens that a row does not see, or gives no weight,
- * cost it no bits, whatever their magnitude. */
+ * value of 64 tokens).  Weights below 2^-126 of the row's largest may count as
+ * 0.  Tokens that a row does not see, or gives no weight, cost it no bits,
+ * whatever their magnitude. */
 CFP32_API cfp32_status cfp32_attention_prompt(const float *q, int64_t q_tok, int64_t q_head,
                                     const void *k, int64_t k_tok, int64_t k_head,
                                     const void *v, int64_t v_tok, int64_t v_head, int kv_type,
