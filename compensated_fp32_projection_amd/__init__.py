@@ -62,10 +62,14 @@ EXPORTS = (
     "cfp32_cache_free",
     "cfp32_cache_compact_workspace_bytes",
     "cfp32_cache_compact",
+    "cfp32_rotary_frequencies",
+    "cfp32_rotary",
 )
 
 W_KN, W_NK = 0, 1
 KV_F32, KV_F16 = 0, 1
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_PARTS = 0, 1, 2, 3
 
 
 class Cfp32Error(RuntimeError):
@@ -156,6 +160,10 @@ def load_library():
     lib.cfp32_cache_compact_workspace_bytes.restype = SZ
     lib.cfp32_cache_compact.argtypes = pool * 2 + [I32] + [I64] * 4 + [P, I64, P, P, I64, P, P, I64, I64, P, SZ, P]
     lib.cfp32_cache_compact.restype = I32
+    lib.cfp32_rotary_frequencies.argtypes = [F64, I64, I32] + [F64] * 4 + [P, P]
+    lib.cfp32_rotary_frequencies.restype = I32
+    lib.cfp32_rotary.argtypes = view * 2 + [I32, P, P, F64, I32, I32] + view * 2 + [I64] * 5 + [P]
+    lib.cfp32_rotary.restype = I32
     _lib = lib
     return lib
 
@@ -296,6 +304,18 @@ def cfp32_cache_compact(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_
     return int(load_library().cfp32_cache_compact(k_pages, kp_page, kp_head, kp_tok, v_pages, vp_page, vp_head,
                                                   vp_tok, kv_type, P, page, Hkv, D, table, ld_table, refs, table_out,
                                                   ld_out, refs_out, live, S, W, workspace, workspace_bytes, stream))
+
+
+def cfp32_rotary_frequencies(theta, R, scaling, factor, trained, slow, fast, frequencies, amplitude) -> int:
+    return int(load_library().cfp32_rotary_frequencies(theta, R, scaling, factor, trained, slow, fast, frequencies,
+                                                       amplitude))
+
+
+def cfp32_rotary(q, q_tok, q_head, k, k_tok, k_head, type, positions, frequencies, amplitude, layout, transpose, q_out,
+                 qo_tok, qo_head, k_out, ko_tok, ko_head, T, Hq, Hkv, D, R, stream) -> int:
+    return int(load_library().cfp32_rotary(q, q_tok, q_head, k, k_tok, k_head, type, positions, frequencies, amplitude,
+                                           layout, transpose, q_out, qo_tok, qo_head, k_out, ko_tok, ko_head, T, Hq,
+                                           Hkv, D, R, stream))
 
 
 # -- tensor helpers -------------------------------------------------------------
@@ -886,3 +906,80 @@ def cache_compact(k_pages, v_pages, table, refs, table_out=None, refs_out=None, 
     _check(cfp32_cache_compact(*at, kv, P, page, Hkv, D, pt, _ld(table), pr, pto, _ld(table_out), pro,
                                live.data_ptr(), S, W, ws, need, st), "cfp32_cache_compact")
     return table_out, refs_out, live
+
+
+# -- rotary positions --------------------------------------------------------------
+
+_SCALINGS = {"plain": ROTARY_PLAIN, "linear": ROTARY_LINEAR, "ntk": ROTARY_NTK, "parts": ROTARY_PARTS}
+
+
+def _launch(call, where, device, *args, stream=None):
+    """The call on `stream`, or the current stream of `device`, with that device current."""
+    torch = _torch()
+    with torch.cuda.device(device):
+        _check(call(*args, _stream(stream)), where)
+
+
+def rotary_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                       trained: float = 0.0, slow: float = 1.0, fast: float = 32.0, device="cuda"):
+    """(frequencies, amplitude) for ``rotary``: the angle each of the
+    rotary_dim / 2 pairs turns by from one position to the next, FP64 on
+    `device`, and the factor on the turned values.  scaling: "plain",
+    "linear" (positions divided by `factor`), "ntk" (a larger base) or
+    "parts" (pairs of fewer than `slow` turns within the `trained` length
+    are interpolated, of more than `fast` left, between them in part)."""
+    torch = _torch()
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    f = (ctypes.c_double * max(rotary_dim // 2, 1))()
+    amplitude = ctypes.c_double()
+    _check(cfp32_rotary_frequencies(float(theta), rotary_dim, _SCALINGS[scaling], float(factor), float(trained), float(slow),
+                                    float(fast), f, ctypes.byref(amplitude)), "cfp32_rotary_frequencies")
+    return torch.tensor(list(f), dtype=torch.float64, device=device), amplitude.value
+
+
+def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: float = 1.0, transpose: bool = False,
+           q_out=None, k_out=None, stream=None):
+    """(q, k) turned by their tokens' positions: q [T, Hq, D] and k [T, Hkv, D]
+    (or None), FP32 or FP16, any strides with contiguous D; frequencies FP64
+    [R / 2] for the first R dims; positions int64 [T] (0 .. T-1 if None).
+    layout: "half" (pairs i, i + R/2) or "interleaved" (2i, 2i + 1).
+    ``transpose`` takes gradients of the outputs to those of the inputs.
+    q_out and k_out may be q and k."""
+    if layout not in ("half", "interleaved"):
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.device.type != "cuda":
+        raise TypeError("q: expected a GPU tensor")
+    dev, types = q.device, (torch.float32, torch.float16)
+    pq = _heads(q, types, "q", dev)
+    T, Hq, D = q.shape
+    pk, Hkv = (None, 0, 0), 0
+    if k is not None:
+        pk, Hkv = _heads(k, (q.dtype,), "k", dev), k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("q and k differ in tokens or head size")
+    if not isinstance(frequencies, torch.Tensor) or frequencies.dtype != torch.float64 or frequencies.device != dev or \
+            frequencies.dim() != 1 or not frequencies.is_contiguous() or 2 * frequencies.shape[0] > D:
+        raise ValueError("frequencies must be a contiguous FP64 tensor of at most D / 2 values on q's device")
+    pp = None
+    if positions is not None:
+        if positions.dtype != torch.int64 or positions.device != dev or positions.shape != (T,) or \
+                not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int64 [T] tensor on q's device")
+        pp = positions.data_ptr()
+    outs = []
+    for x, out, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            outs.append(None)
+            continue
+        out = _empty(x.shape, x.dtype, dev, stream) if out is None else out
+        if out.shape != x.shape:
+            raise ValueError(f"{name} has the wrong shape")
+        outs.append(out)
+    po = _heads(outs[0], (q.dtype,), "q_out", dev)
+    pko = (None, 0, 0) if k is None else _heads(outs[1], (q.dtype,), "k_out", dev)
+    _launch(cfp32_rotary, "cfp32_rotary", dev, *pq, *pk, KV_F16 if q.dtype == torch.float16 else KV_F32, pp,
+            frequencies.data_ptr(), float(amplitude), ROTARY_INTERLEAVED if layout == "interleaved" else ROTARY_HALF,
+            1 if transpose else 0, *po, *pko, T, Hq, Hkv, D, 2 * frequencies.shape[0], stream=stream)
+    return outs[0], outs[1]

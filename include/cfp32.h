@@ -511,6 +511,55 @@ CFP32_API cfp32_status cfp32_cache_compact(void *k_pages, int64_t kp_page, int64
                                  int32_t *table_out, int64_t ld_out, int32_t *refs_out, int32_t *live,
                                  int64_t S, int64_t W, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Rotary positions ---------------------------------------------------------
+ *
+ * For q and k of any head counts, beside cfp32_qkv_rotary's packing: grouped
+ * heads, FP16, pairs side by side, a part of each head, frequencies scaled for
+ * contexts longer than trained, far positions, and the gradient.
+ */
+typedef enum {
+    CFP32_ROTARY_HALF = 0,       /* pair i: dims i and i + R/2 */
+    CFP32_ROTARY_INTERLEAVED = 1 /* pair i: dims 2i and 2i + 1 */
+} cfp32_rotary_layout;
+
+typedef enum {
+    CFP32_ROTARY_PLAIN = 0,  /* f_i = theta^(-2i/R) */
+    CFP32_ROTARY_LINEAR = 1, /* f_i / factor: positions interpolated */
+    CFP32_ROTARY_NTK = 2,    /* of theta * factor^(R / (R - 2)): the slowest pair is interpolated, the fastest is not (R = 2: as plain) */
+    CFP32_ROTARY_PARTS = 3   /* g f_i + (1 - g) f_i / factor, g = (trained f_i / 2 pi - slow) / (fast - slow) cut to [0, 1];
+                                amplitude 1 + 0.1 ln factor */
+} cfp32_rotary_scaling;
+
+/* The angle that each pair turns by from one position to the next, in FP64, and
+ * the factor that goes onto the turned values.  Host only: no device is needed.
+ *   R           : dims that turn, even, >= 2.
+ *   factor      : >= 1, how many times longer the context is (ignored by PLAIN).
+ *   trained     : length of the trained context (> 0), and slow < fast: turns
+ *                 within it; used by PARTS only.
+ *   frequencies : host, R / 2 values.
+ *   amplitude   : host, one value. */
+CFP32_API cfp32_status cfp32_rotary_frequencies(double theta, int64_t R, int scaling, double factor, double trained,
+                                      double slow, double fast, double *frequencies, double *amplitude);
+
+/* Turns the pairs of q and k by their tokens' positions.
+ *   q, q_out    : [T, Hq, D] of `type` (cfp32_kv_type's values), the D values of
+ *                 a token and head contiguous, strides of tokens and heads in
+ *                 elements (those of inputs >= 0).  k, k_out: [T, Hkv, D].
+ *                 Hq or Hkv may be 0.  An output may be its input, with the same
+ *                 strides (in place).
+ *   positions   : int64 [T], device (any values), or NULL for 0 .. T-1.
+ *   frequencies : FP64 [R / 2], device, as cfp32_rotary_frequencies makes them.
+ *   R           : even, 0 <= R <= D <= 1024; dims from R on are copied.
+ *   transpose   : 0, or 1 for the transposed map, which takes gradients of
+ *                 outputs to those of inputs: the turn the other way.
+ * x1' = a (x1 cos - x2 sin), x2' = a (x2 cos + x1 sin): angles in FP64 (off by
+ * less than 1e-6 up to positions of 2^31), the rest in FP32, with one rounding
+ * to FP16.  One kernel launch. */
+CFP32_API cfp32_status cfp32_rotary(const void *q, int64_t q_tok, int64_t q_head, const void *k, int64_t k_tok, int64_t k_head,
+                          int type, const int64_t *positions, const double *frequencies, double amplitude, int layout,
+                          int transpose, void *q_out, int64_t qo_tok, int64_t qo_head, void *k_out, int64_t ko_tok,
+                          int64_t ko_head, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t R, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
