@@ -64,12 +64,28 @@ EXPORTS = (
     "cfp32_cache_compact",
     "cfp32_rotary_frequencies",
     "cfp32_rotary",
+    "cfp32_cache8_append",
+    "cfp32_cache8_read",
+    "cfp32_cache8_copy_pages",
+    "cfp32_cache8_fork",
+    "cfp32_cache8_compact",
 )
 
 W_KN, W_NK = 0, 1
 KV_F32, KV_F16 = 0, 1
+CODE_I8, CODE_E4M3 = 0, 1
 ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_PARTS = 0, 1, 2, 3
+
+
+class Cache8Desc(ctypes.Structure):
+    """cfp32_cache8: the pools of an 8-bit cache as the C calls take them."""
+
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v")] + \
+        [(n, ctypes.c_int64) for n in ("k_page", "k_head", "k_tok", "v_page", "v_head", "v_tok")] + \
+        [(n, ctypes.c_void_p) for n in ("k_scales", "v_scales")] + \
+        [(n, ctypes.c_int64) for n in ("ks_page", "ks_head", "vs_page", "vs_head", "P", "Hkv", "page", "block", "D",
+                                       "code_type")]
 
 
 class Cfp32Error(RuntimeError):
@@ -99,7 +115,8 @@ def load_library():
     # native form makes them, so that one's launches do not fall between another's.
     held = ctypes.PyDLL(LIB_PATH)
     for name in ("cfp32_linear", "cfp32_linear_ex", "cfp32_linear_geglu", "cfp32_attention_prompt",
-                 "cfp32_attention_decode", "cfp32_cache_fork", "cfp32_cache_compact"):
+                 "cfp32_attention_decode", "cfp32_cache_fork", "cfp32_cache_compact", "cfp32_cache8_fork",
+                 "cfp32_cache8_compact"):
         setattr(lib, name, getattr(held, name))
     P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     lib.cfp32_status_string.argtypes = [I32]
@@ -164,6 +181,16 @@ def load_library():
     lib.cfp32_rotary_frequencies.restype = I32
     lib.cfp32_rotary.argtypes = view * 2 + [I32, P, P, F64, I32, I32] + view * 2 + [I64] * 5 + [P]
     lib.cfp32_rotary.restype = I32
+    lib.cfp32_cache8_append.argtypes = view * 2 + [P] * 5 + [I64] * 4 + [P]
+    lib.cfp32_cache8_append.restype = I32
+    lib.cfp32_cache8_read.argtypes = [P, P, I64, P, P] + view * 2 + [I32] + [I64] * 3 + [P]
+    lib.cfp32_cache8_read.restype = I32
+    lib.cfp32_cache8_copy_pages.argtypes = [P, P, P, I64, P]
+    lib.cfp32_cache8_copy_pages.restype = I32
+    lib.cfp32_cache8_fork.argtypes = [P, P, I64, P, P, P, P, I64, P, P, P] + [I64] * 3 + [P, SZ, P]
+    lib.cfp32_cache8_fork.restype = I32
+    lib.cfp32_cache8_compact.argtypes = [P, P, I64, P, P, I64, P, P, I64, I64, P, SZ, P]
+    lib.cfp32_cache8_compact.restype = I32
     _lib = lib
     return lib
 
@@ -316,6 +343,34 @@ def cfp32_rotary(q, q_tok, q_head, k, k_tok, k_head, type, positions, frequencie
     return int(load_library().cfp32_rotary(q, q_tok, q_head, k, k_tok, k_head, type, positions, frequencies, amplitude,
                                            layout, transpose, q_out, qo_tok, qo_head, k_out, ko_tok, ko_head, T, Hq,
                                            Hkv, D, R, stream))
+
+
+def cfp32_cache8_append(k, k_tok, k_head, v, v_tok, v_head, cu, lens, lens_out, cache, table, ld_table, S, W, T,
+                        stream) -> int:
+    return int(load_library().cfp32_cache8_append(k, k_tok, k_head, v, v_tok, v_head, cu, lens, lens_out, cache, table,
+                                                  ld_table, S, W, T, stream))
+
+
+def cfp32_cache8_read(cache, table, ld_table, first, cu, k, k_tok, k_head, v, v_tok, v_head, out_type, S, W, T,
+                      stream) -> int:
+    return int(load_library().cfp32_cache8_read(cache, table, ld_table, first, cu, k, k_tok, k_head, v, v_tok, v_head,
+                                                out_type, S, W, T, stream))
+
+
+def cfp32_cache8_copy_pages(cache, src, dst, n, stream) -> int:
+    return int(load_library().cfp32_cache8_copy_pages(cache, src, dst, n, stream))
+
+
+def cfp32_cache8_fork(cache, table, ld_table, lens, refs, parents, table_out, ld_out, lens_out, refs_out, missing, S, W,
+                      C, workspace, workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_cache8_fork(cache, table, ld_table, lens, refs, parents, table_out, ld_out, lens_out,
+                                                refs_out, missing, S, W, C, workspace, workspace_bytes, stream))
+
+
+def cfp32_cache8_compact(cache, table, ld_table, refs, table_out, ld_out, refs_out, live, S, W, workspace,
+                         workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_cache8_compact(cache, table, ld_table, refs, table_out, ld_out, refs_out, live, S, W,
+                                                   workspace, workspace_bytes, stream))
 
 
 # -- tensor helpers -------------------------------------------------------------
@@ -983,3 +1038,168 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
             frequencies.data_ptr(), float(amplitude), ROTARY_INTERLEAVED if layout == "interleaved" else ROTARY_HALF,
             1 if transpose else 0, *po, *pko, T, Hq, Hkv, D, 2 * frequencies.shape[0], stream=stream)
     return outs[0], outs[1]
+
+
+# -- the 8-bit cache -----------------------------------------------------------------
+
+class Cache8:
+    """The pools of an 8-bit cache: codes k, v [P, Hkv, page, D] (int8 or
+    float8_e4m3fn, any strides with contiguous D) and FP32 scales [P, Hkv,
+    page / block], one for each block of tokens and head (``blocks`` of a
+    page: powers of two).  Holds the tensors; the calls read and write them."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "desc", "addr", "device", "shape", "block")
+
+    def __init__(self, k, v, k_scales, v_scales):
+        torch = _torch()
+        for t, name in ((k, "k"), (v, "v"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+            if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+                raise TypeError(f"{name}: expected a GPU tensor")
+            if t.device != k.device:
+                raise ValueError(f"{name}: on another device")
+        for t, name in ((k, "k"), (v, "v")):
+            if t.dtype not in (torch.int8, torch.float8_e4m3fn) or t.dtype != k.dtype:
+                raise TypeError(f"{name}: codes must be int8 or float8_e4m3fn, K and V alike")
+            if t.dim() != 4 or t.shape != k.shape or (t.shape[3] > 1 and t.stride(3) != 1 and t.numel()):
+                raise ValueError(f"{name}: expected [pages, heads, tokens, D] with contiguous D, K and V alike")
+        P, Hkv, page, D = k.shape
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            if t.dtype != torch.float32:
+                raise TypeError(f"{name}: scales must be float32")
+            if t.dim() != 3 or t.shape != k_scales.shape or t.shape[:2] != (P, Hkv) or \
+                    (t.shape[2] > 1 and t.stride(2) != 1 and t.numel()):
+                raise ValueError(f"{name}: expected [pages, heads, blocks of a page] with contiguous blocks")
+        blocks = k_scales.shape[2]
+        if blocks < 1 or page % blocks or page & (page - 1) or blocks & (blocks - 1) or not 1 <= page <= 65536:
+            raise ValueError("tokens and blocks of a page must be powers of two, of at most 65536 tokens")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.device, self.shape, self.block = k.device, k.shape, page // blocks
+        self.desc = Cache8Desc(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3], k_scales.data_ptr(),
+                               v_scales.data_ptr(), *k_scales.stride()[:2], *v_scales.stride()[:2], P, Hkv, page,
+                               self.block, D, CODE_I8 if k.dtype == torch.int8 else CODE_E4M3)
+        self.addr = ctypes.addressof(self.desc)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page: int, dim: int, block: int | None = None, dtype=None, device="cuda"):
+        """Pools of their own, with nothing in them; a block of tokens is a page unless given."""
+        torch = _torch()
+        block = page if block is None else block
+        if block < 1 or page % block:
+            raise ValueError("block must divide page")
+        codes = [torch.zeros((pages, heads, page, dim), dtype=torch.int8, device=device).view(dtype or torch.int8)
+                 for _ in range(2)]
+        return cls(*codes, *(torch.zeros((pages, heads, page // block), dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _cache8(cache):
+    if not isinstance(cache, Cache8):
+        raise TypeError("cache: expected a Cache8")
+    return cache
+
+
+def cache8_append(k, v, cu, cache: Cache8, table, lens, lens_out=None, stream=None):
+    """Writes new tokens, k and v FP32 [T, Hkv, D], into an 8-bit cache, as
+    ``cache_append``: rows cu[s] .. cu[s+1] - 1 become tokens lens[s], ... of
+    sequence s.  Returns the new lengths."""
+    P, Hkv, page, D = _cache8(cache).shape
+    dev = cache.device
+    torch = _torch()
+    pk, pv = _heads(k, (torch.float32,), "k", dev), _heads(v, (torch.float32,), "v", dev)
+    if k.shape != v.shape or k.shape[1] != Hkv or k.shape[2] != D:
+        raise ValueError("k, v and the pools differ in heads or head size")
+    pt, pl, pc = _ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1), _ints(cu, "cu", dev, 1)
+    S, W = table.shape
+    if lens.shape[0] != S or cu.shape[0] != S + 1:
+        raise ValueError("lens must have one entry per sequence, cu one more")
+    lens_out = _empty(lens.shape, torch.int32, dev, stream) if lens_out is None else lens_out
+    plo = _ints(lens_out, "lens_out", dev, 1)
+    if lens_out.shape != lens.shape:
+        raise ValueError("lens_out has the wrong shape")
+    _launch(cfp32_cache8_append, "cfp32_cache8_append", dev, *pk, *pv, pc, pl, plo, cache.addr, pt, _ld(table), S, W,
+            k.shape[0], stream=stream)
+    return lens_out
+
+
+def cache8_read(cache: Cache8, table, cu, tokens: int, first=None, dtype=None, k_out=None, v_out=None, stream=None):
+    """(k, v), [tokens, Hkv, D] of `dtype` (FP32 or FP16), read back from an
+    8-bit cache as ``attention_prompt`` takes them: rows cu[s] .. cu[s+1] - 1
+    are tokens first[s], first[s] + 1, ... of sequence s (from 0 on without
+    ``first``).  `tokens` is cu's last entry, or more: rows beyond it are not
+    written."""
+    torch = _torch()
+    P, Hkv, page, D = _cache8(cache).shape
+    dev = cache.device
+    dtype = torch.float32 if dtype is None else dtype
+    pt, pc = _ints(table, "table", dev, 2), _ints(cu, "cu", dev, 1)
+    S, W = table.shape
+    pf = None if first is None else _ints(first, "first", dev, 1)
+    if cu.shape[0] != S + 1 or (first is not None and first.shape[0] != S):
+        raise ValueError("first must have one entry per sequence, cu one more")
+    outs = []
+    for out, name in ((k_out, "k_out"), (v_out, "v_out")):
+        out = _empty((tokens, Hkv, D), dtype, dev, stream) if out is None else out
+        if out.shape != (tokens, Hkv, D):
+            raise ValueError(f"{name} has the wrong shape")
+        outs.append(out)
+    pk, pv = (_heads(o, (torch.float32,) if dtype == torch.float32 else (torch.float16,), n, dev)
+              for o, n in zip(outs, ("k_out", "v_out")))
+    _launch(cfp32_cache8_read, "cfp32_cache8_read", dev, cache.addr, pt, _ld(table), pf, pc, *pk, *pv,
+            KV_F16 if dtype == torch.float16 else KV_F32, S, W, tokens, stream=stream)
+    return outs[0], outs[1]
+
+
+def cache8_copy_pages(cache: Cache8, src, dst, stream=None):
+    """Copies page src[i] (codes and scales) to page dst[i] (int32 [n] each)."""
+    dev = _cache8(cache).device
+    ps, pd = _ints(src, "src", dev, 1), _ints(dst, "dst", dev, 1)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst differ in length")
+    _launch(cfp32_cache8_copy_pages, "cfp32_cache8_copy_pages", dev, cache.addr, ps, pd, src.shape[0], stream=stream)
+
+
+def cache8_fork(cache: Cache8, table, lens, refs, parents, missing=None, refs_out=None,
+                workspace: Workspace | None = None, stream=None):
+    """``cache_fork`` of an 8-bit cache: (table, refs, lens) of the children."""
+    torch = _torch()
+    P, dev = _cache8(cache).shape[0], cache.device
+    pt, pl, pr, pp = (_ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1), _ints(refs, "refs", dev, 1),
+                      _ints(parents, "parents", dev, 1))
+    (S, W), C = table.shape, parents.shape[0]
+    if lens.shape[0] != S or refs.shape[0] != P:
+        raise ValueError("lens must have one entry per sequence, refs one per page")
+    with torch.cuda.device(dev):
+        table_out = _empty((C, W), torch.int32, dev, stream)
+        lens_out = _empty(C, torch.int32, dev, stream)
+        refs_out = _empty(refs.shape, torch.int32, dev, stream) if refs_out is None else refs_out
+        pro = _ints(refs_out, "refs_out", dev, 1)
+        pm = None if missing is None else _ints(missing, "missing", dev, 1)
+        if refs_out.shape != refs.shape or (missing is not None and not missing.numel()):
+            raise ValueError("refs_out or missing has the wrong shape")
+        need = cfp32_cache_fork_workspace_bytes(C)
+        buf, ws, st = _scratch(need, dev, workspace, stream)
+        _check(cfp32_cache8_fork(cache.addr, pt, _ld(table), pl, pr, pp, table_out.data_ptr(), W, lens_out.data_ptr(), pro, pm,
+                                 S, W, C, ws, need, st), "cfp32_cache8_fork")
+    return table_out, refs_out, lens_out
+
+
+def cache8_compact(cache: Cache8, table, refs, table_out=None, refs_out=None, workspace: Workspace | None = None,
+                   stream=None):
+    """``cache_compact`` of an 8-bit cache: (table, refs, n)."""
+    torch = _torch()
+    P, dev = _cache8(cache).shape[0], cache.device
+    pt, pr = _ints(table, "table", dev, 2), _ints(refs, "refs", dev, 1)
+    S, W = table.shape
+    if refs.shape[0] != P:
+        raise ValueError("refs must have one entry per page")
+    with torch.cuda.device(dev):
+        table_out = _empty((S, W), torch.int32, dev, stream) if table_out is None else table_out
+        refs_out = _empty(refs.shape, torch.int32, dev, stream) if refs_out is None else refs_out
+        pto, pro = _ints(table_out, "table_out", dev, 2), _ints(refs_out, "refs_out", dev, 1)
+        if table_out.shape != table.shape or refs_out.shape != refs.shape:
+            raise ValueError("table_out or refs_out has the wrong shape")
+        live = _empty(1, torch.int32, dev, stream)
+        need = cfp32_cache_compact_workspace_bytes(P)
+        buf, ws, st = _scratch(need, dev, workspace, stream)
+        _check(cfp32_cache8_compact(cache.addr, pt, _ld(table), pr, pto, _ld(table_out), pro, live.data_ptr(), S, W, ws, need,
+                                    st), "cfp32_cache8_compact")
+    return table_out, refs_out, live

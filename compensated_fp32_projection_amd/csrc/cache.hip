@@ -9,6 +9,7 @@
 // Counts are integers, so atomics on them give the same results in any
 // order.
 #include "attention.h"
+#include "cache8.h"
 
 namespace cfp32 {
 
@@ -253,7 +254,8 @@ hipError_t launch_copy(const Pool &pool, const int32_t *src, const int32_t *dst,
     case 16: CFP32_COPY(vec4_t); break;
     case 8: CFP32_COPY(vec2_t); break;
     case 4: CFP32_COPY(uint32_t); break;
-    default: CFP32_COPY(uint16_t); break;
+    case 2: CFP32_COPY(uint16_t); break;
+    default: CFP32_COPY(uint8_t); break;
     }
 #undef CFP32_COPY
     return hipGetLastError();
@@ -495,6 +497,23 @@ hipError_t launch_cache_fork(const Pool &pool, const int32_t *table, int64_t ld,
     return launch_copy(pool, src, dst, C, nullptr, tables, (int64_t)C * W, stream);
 }
 
+hipError_t launch_cache8_copy_pages(const Pool &codes, const Pool &scales, const int32_t *src, const int32_t *dst, int n,
+                                    hipStream_t stream)
+{
+    const hipError_t e = launch_cache_copy_pages(codes, src, dst, n, stream);
+    return e != hipSuccess ? e : launch_cache_copy_pages(scales, src, dst, n, stream);
+}
+
+hipError_t launch_cache8_fork(const Pool &codes, const Pool &scales, const int32_t *table, int64_t ld, const int32_t *lens,
+                              const int32_t *refs, const int32_t *parents, int32_t *table_out, int64_t ld_out,
+                              int32_t *lens_out, int32_t *refs_out, int32_t *missing, int S, int W, int C,
+                              int32_t *workspace, hipStream_t stream)
+{
+    const hipError_t e = launch_cache_fork(codes, table, ld, lens, refs, parents, table_out, ld_out, lens_out, refs_out, missing,
+                                           S, W, C, workspace, stream);
+    return e != hipSuccess || C == 0 ? e : launch_copy(scales, workspace, workspace + C, C, nullptr, NoTables{}, 0, stream);
+}
+
 hipError_t launch_cache_free(const int32_t *rows, int64_t ld, const int32_t *refs, int32_t *refs_out, int R, int W,
                              int P, hipStream_t stream)
 {
@@ -522,6 +541,16 @@ hipError_t launch_cache_compact(const Pool &pool, const int32_t *table, int64_t 
     if (e != hipSuccess) return e;
     const MovedTables tables = {table, map, table_out, ld, ld_out, W, pool.P};
     return launch_copy(pool, src, dst, pool.P / 2, moves, tables, (int64_t)S * W, stream);
+}
+
+hipError_t launch_cache8_compact(const Pool &codes, const Pool &scales, const int32_t *table, int64_t ld, const int32_t *refs,
+                                 int32_t *table_out, int64_t ld_out, int32_t *refs_out, int32_t *live, int S, int W,
+                                 int32_t *workspace, hipStream_t stream)
+{
+    const hipError_t e = launch_cache_compact(codes, table, ld, refs, table_out, ld_out, refs_out, live, S, W, workspace, stream);
+    if (e != hipSuccess) return e;
+    const int32_t *src = workspace + codes.P, *dst = src + codes.P, *moves = dst + codes.P;
+    return launch_copy(scales, src, dst, codes.P / 2, moves, NoTables{}, 0, stream);
 }
 
 }  // namespace cfp32

@@ -2,6 +2,7 @@
 // include/cfp32.h): argument validation, the device check and workspace sizes.
 // Every call validates all of its arguments before it enqueues anything.
 #include "api_checks.h"
+#include "cache8.h"
 #include "rotary.h"
 
 namespace {
@@ -12,6 +13,45 @@ using namespace cfp32;
 bool same_view(const void *in, int64_t s0, int64_t s1, const void *out, int64_t o0, int64_t o1)
 {
     return in != out || (s0 == o0 && s1 == o1);
+}
+
+// An 8-bit cache: sizes, and (written: or) pools that are only read.
+bool sizes_ok(const cfp32_cache8 *c)
+{
+    if (!c || !size_ok(c->P) || page_log2(c->page) < 0 || page_log2(c->block) < 0 || c->block > c->page) return false;
+    if (!heads_ok(c->Hkv, c->Hkv, c->D) || c->Hkv > 65535) return false;  // a token's values are counted in 32 bits
+    return c->code_type == CFP32_CODE_I8 || c->code_type == CFP32_CODE_E4M3;
+}
+
+bool pools_ok(const cfp32_cache8 *c, bool written)
+{
+    if (c->P == 0 || c->Hkv == 0 || c->D == 0) return true;
+    const int64_t P = c->P, H = c->Hkv, blocks = c->page / c->block;
+    if (!c->k || !c->v || !c->k_scales || !c->v_scales || !aligned_to(c->k_scales, 4) || !aligned_to(c->v_scales, 4)) return false;
+    auto ok = [&](int64_t s1, int64_t s2, int64_t n3, int64_t s3, int64_t n) {
+        return view_ok(P, s1, H, s2, n3, s3, n) && (!written || distinct_ok(P, s1, H, s2, n3, s3, n));
+    };
+    return ok(c->k_page, c->k_head, c->page, c->k_tok, c->D) && ok(c->v_page, c->v_head, c->page, c->v_tok, c->D) &&
+           ok(c->ks_page, c->ks_head, 1, 0, blocks) && ok(c->vs_page, c->vs_head, 1, 0, blocks);
+}
+
+Cache8 view_of(const cfp32_cache8 *c)
+{
+    return {{c->k, c->k_page, c->k_head, c->k_tok}, {c->v, c->v_page, c->v_head, c->v_tok}, {c->k_scales, c->ks_page, c->ks_head},
+            {c->v_scales, c->vs_page, c->vs_head}, (int)c->P, (int)c->Hkv, (int)c->D, page_log2(c->page), page_log2(c->block),
+            c->code_type == CFP32_CODE_E4M3};
+}
+
+// Its codes and its scales (a page's are one value wide) as pools of pages to be moved.
+Pool codes_of(const cfp32_cache8 *c)
+{
+    return {{c->k, c->k_page, c->k_head, c->k_tok}, {c->v, c->v_page, c->v_head, c->v_tok}, (int)c->P, page_log2(c->page),
+            (int)c->Hkv, (int)c->D, 1};
+}
+Pool scales_of(const cfp32_cache8 *c)
+{
+    return {{c->k_scales, c->ks_page, c->ks_head, 1}, {c->v_scales, c->vs_page, c->vs_head, 1}, (int)c->P,
+            page_log2(c->page) - page_log2(c->block), (int)c->Hkv, c->D > 0 ? 1 : 0, 4};
 }
 
 }  // namespace
@@ -71,6 +111,95 @@ cfp32_status cfp32_rotary(const void *q, int64_t q_tok, int64_t q_head, const vo
                           positions, frequencies, (float)amplitude, type == CFP32_KV_F16, layout == CFP32_ROTARY_INTERLEAVED,
                           transpose != 0, (int)T, (int)D, (int)R};
     return api_launched(launch_rotary(a, (hipStream_t)stream));
+}
+
+cfp32_status cfp32_cache8_append(const float *k, int64_t k_tok, int64_t k_head, const float *v, int64_t v_tok, int64_t v_head,
+                                 const int32_t *cu, const int32_t *lens, int32_t *lens_out, const cfp32_cache8 *cache,
+                                 const int32_t *table, int64_t ld_table, int64_t S, int64_t W, int64_t T, void *stream)
+{
+    if (!sizes_ok(cache) || !size_ok(S) || !size_ok(W) || !size_ok(T) || W > (kMaxSize >> page_log2(cache->page)))
+        return CFP32_ERR_INVALID_VALUE;
+    if (S == 0) return CFP32_OK;
+    if (!cu || !lens || !lens_out || lens == lens_out || !table_ok(table, ld_table, S, W)) return CFP32_ERR_INVALID_VALUE;
+    const int64_t H = cache->Hkv, D = cache->D;
+    if (T > 0 && H > 0 && D > 0) {
+        if (!k || !v || !aligned_to(k, 4) || !aligned_to(v, 4) || !view_ok(T, k_tok, H, k_head, 1, 0, D) ||
+            !view_ok(T, v_tok, H, v_head, 1, 0, D) || !pools_ok(cache, true))
+            return CFP32_ERR_INVALID_VALUE;
+    }
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    return api_launched(launch_cache8_append({k, k_tok, k_head}, {v, v_tok, v_head}, cu, lens, lens_out, view_of(cache), table,
+                                             ld_table, (int)S, (int)W, (int)T, (hipStream_t)stream));
+}
+
+cfp32_status cfp32_cache8_read(const cfp32_cache8 *cache, const int32_t *table, int64_t ld_table, const int32_t *first,
+                               const int32_t *cu, void *k, int64_t k_tok, int64_t k_head, void *v, int64_t v_tok, int64_t v_head,
+                               int out_type, int64_t S, int64_t W, int64_t T, void *stream)
+{
+    if (!sizes_ok(cache) || !type_ok(out_type) || !size_ok(S) || !size_ok(W) || !size_ok(T) ||
+        W > (kMaxSize >> page_log2(cache->page)))
+        return CFP32_ERR_INVALID_VALUE;
+    const int64_t H = cache->Hkv, D = cache->D;
+    if (S == 0 || T == 0 || H == 0 || D == 0) return CFP32_OK;
+    const size_t al = out_type == CFP32_KV_F16 ? 2 : 4;
+    if (!cu || !k || !v || !aligned_to(k, al) || !aligned_to(v, al) || !table_ok(table, ld_table, S, W) || !pools_ok(cache, false))
+        return CFP32_ERR_INVALID_VALUE;
+    if (!view_ok(T, k_tok, H, k_head, 1, 0, D) || !view_ok(T, v_tok, H, v_head, 1, 0, D) ||
+        !distinct_ok(T, k_tok, H, k_head, 1, 0, D) || !distinct_ok(T, v_tok, H, v_head, 1, 0, D))
+        return CFP32_ERR_INVALID_VALUE;
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    return api_launched(launch_cache8_read(view_of(cache), table, ld_table, first, cu, {k, k_tok, k_head}, {v, v_tok, v_head},
+                                           out_type == CFP32_KV_F16, (int)S, (int)W, (int)T, (hipStream_t)stream));
+}
+
+cfp32_status cfp32_cache8_copy_pages(const cfp32_cache8 *cache, const int32_t *src, const int32_t *dst, int64_t n, void *stream)
+{
+    if (!sizes_ok(cache) || !size_ok(n)) return CFP32_ERR_INVALID_VALUE;
+    if (n == 0 || cache->P == 0 || cache->Hkv == 0 || cache->D == 0) return CFP32_OK;
+    if (!src || !dst || !pools_ok(cache, true)) return CFP32_ERR_INVALID_VALUE;
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    return api_launched(launch_cache8_copy_pages(codes_of(cache), scales_of(cache), src, dst, (int)n, (hipStream_t)stream));
+}
+
+cfp32_status cfp32_cache8_fork(const cfp32_cache8 *cache, const int32_t *table, int64_t ld_table, const int32_t *lens,
+                               const int32_t *refs, const int32_t *parents, int32_t *table_out, int64_t ld_out, int32_t *lens_out,
+                               int32_t *refs_out, int32_t *missing, int64_t S, int64_t W, int64_t C, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
+    if (!sizes_ok(cache) || !size_ok(S) || !size_ok(W) || !size_ok(C) || W > (kMaxSize >> page_log2(cache->page)))
+        return CFP32_ERR_INVALID_VALUE;
+    if ((cache->P > 0 && (!refs || !refs_out)) || !table_ok(table, ld_table, S, W) || !table_ok(table_out, ld_out, C, W))
+        return CFP32_ERR_INVALID_VALUE;
+    if (cache->P == 0 && C == 0 && !missing) return CFP32_OK;
+    if (C > 0) {
+        if (!parents || !lens_out || (S > 0 && !lens) || table_out == table || lens_out == lens || !pools_ok(cache, true))
+            return CFP32_ERR_INVALID_VALUE;
+        if (!workspace || workspace_bytes < cfp32_cache_fork_workspace_bytes(C)) return CFP32_ERR_INVALID_VALUE;
+    }
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    return api_launched(launch_cache8_fork(codes_of(cache), scales_of(cache), table, ld_table, lens, refs, parents, table_out,
+                                           ld_out, lens_out, refs_out, missing, (int)S, (int)W, (int)C,
+                                           (int32_t *)align_up(workspace), (hipStream_t)stream));
+}
+
+cfp32_status cfp32_cache8_compact(const cfp32_cache8 *cache, const int32_t *table, int64_t ld_table, const int32_t *refs,
+                                  int32_t *table_out, int64_t ld_out, int32_t *refs_out, int32_t *live, int64_t S, int64_t W,
+                                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!sizes_ok(cache) || !size_ok(S) || !size_ok(W)) return CFP32_ERR_INVALID_VALUE;
+    if (!table_ok(table, ld_table, S, W) || !table_ok(table_out, ld_out, S, W) || !live) return CFP32_ERR_INVALID_VALUE;
+    if (table == table_out && ld_table != ld_out) return CFP32_ERR_INVALID_VALUE;
+    if (cache->P > 0 && (!refs || !refs_out || !workspace ||
+                         workspace_bytes < cfp32_cache_compact_workspace_bytes(cache->P) || !pools_ok(cache, true)))
+        return CFP32_ERR_INVALID_VALUE;
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    return api_launched(launch_cache8_compact(codes_of(cache), scales_of(cache), table, ld_table, refs, table_out, ld_out, refs_out,
+                                              live, (int)S, (int)W, (int32_t *)align_up(workspace), (hipStream_t)stream));
 }
 
 }  // extern "C"

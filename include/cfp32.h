@@ -560,6 +560,77 @@ CFP32_API cfp32_status cfp32_rotary(const void *q, int64_t q_tok, int64_t q_head
                           int transpose, void *q_out, int64_t qo_tok, int64_t qo_head, void *k_out, int64_t ko_tok,
                           int64_t ko_head, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t R, void *stream);
 
+/* ---- The 8-bit cache ------------------------------------------------------------
+ *
+ * A paged cache whose K and V are held in 8 bits: codes, with one FP32 scale for
+ * each block of `block` tokens and head, for K and for V.  A code c of a block
+ * with scale s stands for c s.  Tables, lengths and counts are those of the
+ * paged cache above (cfp32_cache_reserve and cfp32_cache_free serve both).
+ *
+ * A block's scale is made when its first token is written: the largest magnitude
+ * m of what is written / 127 for integers (rounded to FP32), the least power of
+ * two that brings m to 448 or below for floats, and 2^-126 at least.  A later
+ * token that does not fit (m > the largest code x the scale, in FP32) multiplies
+ * the scale by the least power of two that holds it, and the block's codes are
+ * divided by it: so a value of its first tokens is off by less than one step of
+ * the block's last scale however often that grew, and by half a step where it
+ * did not.  Codes are x / s rounded to nearest even, of the exact quotient (with
+ * scales of floats that are not powers of two, which no call makes: of the
+ * product with 1 / s).  A block that is given an infinity or NaN, or holds
+ * tokens under a scale that is not a finite normal positive number, gets the
+ * scale NaN: all of it reads as NaN until its page is begun anew.  The float
+ * codes 0x7F and 0xFF, which no call writes, count as +-480.
+ */
+typedef enum {
+    CFP32_CODE_I8 = 0,  /* -127 .. 127 */
+    CFP32_CODE_E4M3 = 1 /* sign, 4 bits of exponent (bias 7), 3 of mantissa; +-448 at most */
+} cfp32_code_type;
+
+/* The pools of an 8-bit cache: a description in host memory, read by the call
+ * that it is given to and not kept. */
+typedef struct {
+    void *k, *v;                                           /* codes [P, Hkv, page, D], contiguous D */
+    int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;  /* element strides */
+    float *k_scales, *v_scales;                            /* [P, Hkv, page / block], contiguous blocks */
+    int64_t ks_page, ks_head, vs_page, vs_head;
+    int64_t P, Hkv, page, block, D;                        /* page and block: powers of two, block <= page */
+    int64_t code_type;
+} cfp32_cache8;
+
+/* Writes new tokens, as cfp32_cache_append: k, v FP32 [T, Hkv, D], rows cu[s] ..
+ * cu[s+1] - 1 become tokens lens[s], lens[s] + 1, ... of sequence s.
+ *   lens_out : int32 [S]: lens[s] + cu[s+1] - cu[s]; not lens itself.
+ * Tokens whose table entry is not a page of the pool, or beyond the table, and
+ * those of sequences of negative length, are not written.  A page that is
+ * written has to be the sequence's own.  One kernel launch. */
+CFP32_API cfp32_status cfp32_cache8_append(const float *k, int64_t k_tok, int64_t k_head, const float *v, int64_t v_tok,
+                                 int64_t v_head, const int32_t *cu, const int32_t *lens, int32_t *lens_out,
+                                 const cfp32_cache8 *cache, const int32_t *table, int64_t ld_table, int64_t S, int64_t W,
+                                 int64_t T, void *stream);
+
+/* Reads tokens back, packed as cfp32_attention_prompt takes them: rows cu[s] ..
+ * cu[s+1] - 1 of k, v [T, Hkv, D] of out_type (a cfp32_kv_type) get tokens
+ * first[s], first[s] + 1, ... of sequence s (first NULL: from 0 on).  c s is
+ * rounded to FP32, then, where asked for, to FP16.  A token that has no page in
+ * the table, or a position that is negative or beyond it, reads as NaN; rows
+ * outside all sequences are not written.  One kernel launch. */
+CFP32_API cfp32_status cfp32_cache8_read(const cfp32_cache8 *cache, const int32_t *table, int64_t ld_table, const int32_t *first,
+                               const int32_t *cu, void *k, int64_t k_tok, int64_t k_head, void *v, int64_t v_tok,
+                               int64_t v_head, int out_type, int64_t S, int64_t W, int64_t T, void *stream);
+
+/* cfp32_cache_copy_pages, _fork and _compact of codes and scales (workspaces:
+ * cfp32_cache_fork_workspace_bytes and cfp32_cache_compact_workspace_bytes). */
+CFP32_API cfp32_status cfp32_cache8_copy_pages(const cfp32_cache8 *cache, const int32_t *src, const int32_t *dst, int64_t n,
+                                     void *stream);
+CFP32_API cfp32_status cfp32_cache8_fork(const cfp32_cache8 *cache, const int32_t *table, int64_t ld_table, const int32_t *lens,
+                               const int32_t *refs, const int32_t *parents, int32_t *table_out, int64_t ld_out,
+                               int32_t *lens_out, int32_t *refs_out, int32_t *missing, int64_t S, int64_t W, int64_t C,
+                               void *workspace, size_t workspace_bytes, void *stream);
+CFP32_API cfp32_status cfp32_cache8_compact(const cfp32_cache8 *cache, const int32_t *table, int64_t ld_table,
+                                  const int32_t *refs, int32_t *table_out, int64_t ld_out, int32_t *refs_out,
+                                  int32_t *live, int64_t S, int64_t W, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
 #ifdef __cplusplus
 }
 #endif
