@@ -69,6 +69,8 @@ EXPORTS = (
     "cfp32_cache8_copy_pages",
     "cfp32_cache8_fork",
     "cfp32_cache8_compact",
+    "cfp32_attention8_decode_workspace_bytes",
+    "cfp32_attention8_decode",
 )
 
 W_KN, W_NK = 0, 1
@@ -116,7 +118,7 @@ def load_library():
     held = ctypes.PyDLL(LIB_PATH)
     for name in ("cfp32_linear", "cfp32_linear_ex", "cfp32_linear_geglu", "cfp32_attention_prompt",
                  "cfp32_attention_decode", "cfp32_cache_fork", "cfp32_cache_compact", "cfp32_cache8_fork",
-                 "cfp32_cache8_compact"):
+                 "cfp32_cache8_compact", "cfp32_attention8_decode"):
         setattr(lib, name, getattr(held, name))
     P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     lib.cfp32_status_string.argtypes = [I32]
@@ -191,6 +193,10 @@ def load_library():
     lib.cfp32_cache8_fork.restype = I32
     lib.cfp32_cache8_compact.argtypes = [P, P, I64, P, P, I64, P, P, I64, I64, P, SZ, P]
     lib.cfp32_cache8_compact.restype = I32
+    lib.cfp32_attention8_decode_workspace_bytes.argtypes = [I64] * 6
+    lib.cfp32_attention8_decode_workspace_bytes.restype = SZ
+    lib.cfp32_attention8_decode.argtypes = view + [P, P, I64, I64, P] + view + [I64, I64, F64, P, SZ, P]
+    lib.cfp32_attention8_decode.restype = I32
     _lib = lib
     return lib
 
@@ -371,6 +377,16 @@ def cfp32_cache8_compact(cache, table, ld_table, refs, table_out, ld_out, refs_o
                          workspace_bytes, stream) -> int:
     return int(load_library().cfp32_cache8_compact(cache, table, ld_table, refs, table_out, ld_out, refs_out, live, S, W,
                                                    workspace, workspace_bytes, stream))
+
+
+def cfp32_attention8_decode_workspace_bytes(B, Hq, Hkv, D, W, page) -> int:
+    return int(load_library().cfp32_attention8_decode_workspace_bytes(B, Hq, Hkv, D, W, page))
+
+
+def cfp32_attention8_decode(q, q_seq, q_head, cache, table, ld_table, W, lens, out, out_seq, out_head, B, Hq, scale,
+                            workspace, workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_attention8_decode(q, q_seq, q_head, cache, table, ld_table, W, lens, out, out_seq,
+                                                      out_head, B, Hq, scale, workspace, workspace_bytes, stream))
 
 
 # -- tensor helpers -------------------------------------------------------------
@@ -1203,3 +1219,31 @@ def cache8_compact(cache: Cache8, table, refs, table_out=None, refs_out=None, wo
         _check(cfp32_cache8_compact(cache.addr, pt, _ld(table), pr, pto, _ld(table_out), pro, live.data_ptr(), S, W, ws, need,
                                     st), "cfp32_cache8_compact")
     return table_out, refs_out, live
+
+
+def attention8_decode(q, cache: Cache8, table, lens, scale: float | None = None, out=None,
+                      workspace: Workspace | None = None, stream=None):
+    """Attention of one new token per sequence against an 8-bit cache: q FP32
+    [B, Hq, D]; table int32 [B, W]; lens int32 [B].  Returns FP32 [B, Hq, D]."""
+    torch = _torch()
+    P, Hkv, page, D2 = _cache8(cache).shape
+    dev = cache.device
+    pq = _heads(q, (torch.float32,), "q", dev)
+    B, Hq, D = q.shape
+    if D2 != D or Hkv == 0 or Hq % Hkv:
+        raise ValueError("q and the pools differ in head size or heads")
+    pt, pl = _ints(table, "table", dev, 2), _ints(lens, "lens", dev, 1)
+    W = table.shape[1]
+    if table.shape[0] != B or lens.shape[0] != B:
+        raise ValueError("table and lens must have one row per sequence")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = _empty((B, Hq, D), torch.float32, dev, stream)
+        elif out.shape != q.shape:
+            raise ValueError("out has the wrong shape")
+        po = _heads(out, (torch.float32,), "out", dev)
+        need = cfp32_attention8_decode_workspace_bytes(B, Hq, Hkv, D, W, page)
+        buf, ws, st = _scratch(need, dev, workspace, stream)
+        _check(cfp32_attention8_decode(*pq, cache.addr, pt, _ld(table), W, pl, *po, B, Hq,
+                                       D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention8_decode")
+    return out

@@ -1,5 +1,6 @@
 // Launches of the attention calls (as attention_plans.hip has them): the
 // kernels of few rows (attention_rows.h), and the joining of parts.
+#include "attention_join.h"
 #include "attention_rows.h"
 
 namespace cfp32 {
@@ -66,110 +67,37 @@ __global__ __launch_bounds__(64 * NW, 2) void decode_rows_kernel(DecodeArgs a, D
     decode_rows<T, DP, WIDE, NW, false>(a, c, blockIdx.x, blockIdx.y, sh);
 }
 
-// Row (i, h) of a call: where its result goes (null: it is no row of a sequence), and its slow form.
-__device__ __forceinline__ float *row_out(const DecodeArgs &a, int64_t i, int h) { return a.out + i * a.out_seq + h * a.out_head; }
+// A call's rows for the join: where their results go, and their slow form.
 template <class T>
-__device__ __forceinline__ void redo_row(const DecodeArgs &a, int64_t i, int h) { attend_decode_row<T>(a, i, h); }
-__device__ __forceinline__ bool prompt_row(const PromptArgs &a, int64_t i, Sequence &sq)
-{
-    const int lo = find_last(a.S, i, [&](int s) { return (int64_t)a.cu_q[s]; });
-    sq = sequence(a, lo);
-    return i >= sq.q0 && i < sq.q0 + sq.nq;
-}
-__device__ __forceinline__ float *row_out(const PromptArgs &a, int64_t i, int h)
-{
-    Sequence sq;
-    return prompt_row(a, i, sq) ? a.out + i * a.out_tok + h * a.out_head : nullptr;
-}
+struct DecodeRows {
+    DecodeArgs a;
+    __device__ __forceinline__ int Hq() const { return a.Hq; }
+    __device__ __forceinline__ int D() const { return a.D; }
+    __device__ __forceinline__ float *out(int64_t i, int h) const { return a.out + i * a.out_seq + h * a.out_head; }
+    __device__ __forceinline__ void finish(int64_t i, int h) const { attend_decode_row<T>(a, i, h); }
+};
 template <class T>
-__device__ __forceinline__ void redo_row(const PromptArgs &a, int64_t i, int h)
-{
-    Sequence sq;
-    if (prompt_row(a, i, sq)) attend_prompt_row<T>(a, sq, (int)i - sq.q0, h);
-}
-
-// Rows from their parts.  WAVES: of a row, each taking every WAVES-th part,
-// their sums joined in LDS.  Few parts: a wave to a row (a block to a row made
-// 9600 rows of 2 parts cost 15 us).  Many: four (a wave to a row took 10 us
-// for 1024 rows of 68 parts x 128, for want of loads in flight; now 6).
-template <class T, int DP, int WAVES, class Args>
-__global__ __launch_bounds__(256) void join_kernel(Args a, Partials from, int64_t rows)
-{
-    constexpr int E = DP / 64;
-    __shared__ float sums[4][DP], weight[4];
-    const int lane = threadIdx.x & 63, w4 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = w4 % WAVES;
-    const int64_t row = min((int64_t)blockIdx.x * (4 / WAVES) + w4 / WAVES, rows - 1), b = row / a.Hq;
-    const int h = (int)(row - b * a.Hq);
-    float *out = row_out(a, b, h);
-    const int64_t s0 = row * from.slots;
-    const int slots = out ? from.slots : 0;
-    float m = -INFINITY;
-    for (int i = lane; i < slots; i += 64) m = fmaxf(m, from.m[s0 + i]);
-#pragma unroll
-    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-    float l = 0.0f, o[E] = {};
-    for (int i0 = 0; i0 < slots; i0 += 64 * WAVES) {
-        const int i = i0 + WAVES * lane + wave;
-        float f = 0.0f, li = 0.0f;
-        if (i < slots) {
-            const float mi = from.m[s0 + i];
-            f = mi == -INFINITY ? 0.0f : exp2_raw(mi - m);
-            li = from.l[s0 + i];
-        }
-        l = fmaf(f, li, l);
-        // Nothing was written where li is 0; what is has to be read also where
-        // f is 0, for the NaN of an infinite value.
-        uint64_t used = __ballot(li != 0.0f);
-        while (used) {
-            constexpr int U = 8;  // loads in flight
-            float w[U], x[U][E];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = used ? __builtin_ctzll(used) : -1;
-                w[u] = 0.0f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[u][e] = 0.0f;
-                if (k >= 0) {
-                    used &= used - 1;
-                    w[u] = __shfl(f, k);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[u][e] = from.o[(s0 + i0 + WAVES * k + wave) * DP + lane * E + e];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(w[u], x[u][e], o[e]);
-        }
+struct PromptRows {
+    PromptArgs a;
+    __device__ __forceinline__ int Hq() const { return a.Hq; }
+    __device__ __forceinline__ int D() const { return a.D; }
+    __device__ __forceinline__ bool row(int64_t i, Sequence &sq) const
+    {
+        const int lo = find_last(a.S, i, [&](int s) { return (int64_t)a.cu_q[s]; });
+        sq = sequence(a, lo);
+        return i >= sq.q0 && i < sq.q0 + sq.nq;
     }
-#pragma unroll
-    for (int x = 32; x; x >>= 1) l += __shfl_xor(l, x);
-    if (WAVES == 4) {
-        if (lane == 0) weight[wave] = l;
-#pragma unroll
-        for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = o[e];
-        __syncthreads();
-        if (wave) return;
-        l = (weight[0] + weight[1]) + (weight[2] + weight[3]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int d = lane * E + e;
-            o[e] = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
-        }
+    __device__ __forceinline__ float *out(int64_t i, int h) const
+    {
+        Sequence sq;
+        return row(i, sq) ? a.out + i * a.out_tok + h * a.out_head : nullptr;
     }
-    if (!out) return;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    bool odd = !(fabsf(l) < INFINITY) || l == 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float y = o[e] * inv;
-        if (lane * E + e < a.D) {
-            out[lane * E + e] = y;
-            odd |= !(fabsf(y) < INFINITY);
-        }
+    __device__ __forceinline__ void finish(int64_t i, int h) const
+    {
+        Sequence sq;
+        if (row(i, sq)) attend_prompt_row<T>(a, sq, (int)i - sq.q0, h);
     }
-    if (__any(odd)) redo_row<T>(a, b, h);
-}
+};
 
 // Rows against a pool without pages: 0, or NaN where a sequence has tokens.
 __global__ __launch_bounds__(64) void decode_no_pages_kernel(DecodeArgs a)
@@ -209,25 +137,10 @@ __global__ __launch_bounds__(64) void decode_no_pages_kernel(DecodeArgs a)
 
 namespace {
 
-template <class Args>
+template <template <class> class Rows, class Args>
 hipError_t join(const Args &a, const Partials &from, int64_t rows, hipStream_t stream)
 {
-    const bool four = from.slots > kJoinByWave;
-    const unsigned blocks = (unsigned)join_blocks(from, rows);
-#define CFP32_JOIN(T, DP)                                                            \
-    do {                                                                           \
-        if (four) join_kernel<T, DP, 4><<<blocks, 256, 0, stream>>>(a, from, rows); \
-        else join_kernel<T, DP, 1><<<blocks, 256, 0, stream>>>(a, from, rows);      \
-    } while (0)
-    if (a.kv_f16) {
-        if (a.D <= 64) CFP32_JOIN(_Float16, 64);
-        else CFP32_JOIN(_Float16, 128);
-    } else {
-        if (a.D <= 64) CFP32_JOIN(float, 64);
-        else CFP32_JOIN(float, 128);
-    }
-#undef CFP32_JOIN
-    return hipGetLastError();
+    return a.kv_f16 ? launch_join(Rows<_Float16>{a}, from, rows, stream) : launch_join(Rows<float>{a}, from, rows, stream);
 }
 
 }  // namespace
@@ -244,7 +157,7 @@ hipError_t launch_attention_prompt(const PromptArgs &a, void *workspace, hipStre
         CFP32_BY_TYPE(prompt_rows_kernel, a.kv_f16, a.D, p.wide, p.eight, grid, a, p.to);
         e = hipGetLastError();
     }
-    return e != hipSuccess || !p.to.o ? e : join(a, p.to, (int64_t)a.Tq * a.Hq, stream);
+    return e != hipSuccess || !p.to.o ? e : join<PromptRows>(a, p.to, (int64_t)a.Tq * a.Hq, stream);
 }
 
 hipError_t launch_attention_decode(const DecodeArgs &a, void *workspace, hipStream_t stream)
@@ -264,7 +177,7 @@ hipError_t launch_attention_decode(const DecodeArgs &a, void *workspace, hipStre
         CFP32_BY_TYPE(decode_rows_kernel, a.kv_f16, a.D, p.wide, p.parts.eight, grid, a, p.parts);
         e = hipGetLastError();
     }
-    return e != hipSuccess || !p.parts.to.o ? e : join(a, p.parts.to, (int64_t)a.B * a.Hq, stream);
+    return e != hipSuccess || !p.parts.to.o ? e : join<DecodeRows>(a, p.parts.to, (int64_t)a.B * a.Hq, stream);
 }
 
 }  // namespace cfp32

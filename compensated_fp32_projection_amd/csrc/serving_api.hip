@@ -2,7 +2,7 @@
 // include/cfp32.h): argument validation, the device check and workspace sizes.
 // Every call validates all of its arguments before it enqueues anything.
 #include "api_checks.h"
-#include "cache8.h"
+#include "attention8.h"
 #include "rotary.h"
 
 namespace {
@@ -200,6 +200,40 @@ cfp32_status cfp32_cache8_compact(const cfp32_cache8 *cache, const int32_t *tabl
     if (st != CFP32_OK) return st;
     return api_launched(launch_cache8_compact(codes_of(cache), scales_of(cache), table, ld_table, refs, table_out, ld_out, refs_out,
                                               live, (int)S, (int)W, (int32_t *)align_up(workspace), (hipStream_t)stream));
+}
+
+size_t cfp32_attention8_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int64_t page)
+{
+    const int lg = page_log2(page);
+    if (!size_ok(B) || !heads_ok(Hq, Hkv, D) || Hkv > 65535 || !size_ok(W) || lg < 0 || W > (kMaxKeys >> lg)) return 0;
+    if (B == 0 || Hq == 0 || D == 0 || B > (kMaxDim >> 20) / Hq) return 0;
+    const size_t n = attention8_decode_workspace(B, Hq, Hkv, D, W, lg);
+    return n ? n + kAlign : 0;
+}
+
+cfp32_status cfp32_attention8_decode(const float *q, int64_t q_seq, int64_t q_head, const cfp32_cache8 *cache,
+                                     const int32_t *table, int64_t ld_table, int64_t W, const int32_t *lens, float *out,
+                                     int64_t out_seq, int64_t out_head, int64_t B, int64_t Hq, double scale, void *workspace,
+                                     size_t workspace_bytes, void *stream)
+{
+    if (!sizes_ok(cache) || !size_ok(B) || !heads_ok(Hq, cache->Hkv, cache->D) || !size_ok(W) ||
+        W > (kMaxKeys >> page_log2(cache->page)))
+        return CFP32_ERR_INVALID_VALUE;
+    const int64_t D = cache->D;
+    if (B == 0 || Hq == 0 || D == 0) return CFP32_OK;
+    if (B > (kMaxDim >> 20) / Hq) return CFP32_ERR_INVALID_VALUE;
+    if (!q || !out || !lens || !table_ok(table, ld_table, B, W) || !pools_ok(cache, false)) return CFP32_ERR_INVALID_VALUE;
+    if (!aligned_to(q, 4) || !aligned_to(out, 4) || !view_ok(B, q_seq, Hq, q_head, 1, 0, D) ||
+        !view_ok(B, out_seq, Hq, out_head, 1, 0, D) || !distinct_ok(B, out_seq, Hq, out_head, 1, 0, D))
+        return CFP32_ERR_INVALID_VALUE;
+    if (!scale_ok(scale)) return CFP32_ERR_INVALID_VALUE;
+    const size_t need = cfp32_attention8_decode_workspace_bytes(B, Hq, cache->Hkv, D, W, cache->page);
+    if (need && (!workspace || workspace_bytes < need)) return CFP32_ERR_INVALID_VALUE;
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    const Decode8Args a = {q, q_seq, q_head, view_of(cache), table, ld_table, lens, out, out_seq, out_head, (int)B, (int)Hq,
+                           (int)W, (float)scale};
+    return api_launched(launch_attention8_decode(a, align_up(workspace), (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -631,6 +631,27 @@ CFP32_API cfp32_status cfp32_cache8_compact(const cfp32_cache8 *cache, const int
                                   int32_t *live, int64_t S, int64_t W, void *workspace, size_t workspace_bytes,
                                   void *stream);
 
+/* Workspace bytes of cfp32_attention8_decode; 0 for sizes it refuses, and where
+ * none is needed. */
+CFP32_API size_t cfp32_attention8_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int64_t page);
+
+/* Attention of one new token per sequence against an 8-bit cache: as
+ * cfp32_attention_decode, with K and V the codes times their scales.
+ *   q, out : FP32 [B, Hq, D], Hq a multiple of the cache's Hkv.
+ *   table  : int32 [B, W], leading dimension ld_table >= W.
+ *   lens   : int32 [B]: sequence b sees its first lens[b] tokens (clamped to
+ *            [0, W * page]); 0 gives a row of 0.
+ * Codes are exact operands; q, and each row's products of weights and V's
+ * scales, are cut into two FP16 parts (22 bits: a product is off by 2^-22 of
+ * itself or 2^-36 of the largest of the row's 32 or 64 keys beside it); sums
+ * and softmax statistics are FP32.  A page id outside [0, P) where lens needs a
+ * page, and a scale that is NaN, make the rows that see it NaN, as an infinity
+ * or NaN of q does its own row; scales of tokens that no row sees reach none. */
+CFP32_API cfp32_status cfp32_attention8_decode(const float *q, int64_t q_seq, int64_t q_head, const cfp32_cache8 *cache,
+                                     const int32_t *table, int64_t ld_table, int64_t W, const int32_t *lens, float *out,
+                                     int64_t out_seq, int64_t out_head, int64_t B, int64_t Hq, double scale,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

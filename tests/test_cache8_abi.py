@@ -31,7 +31,10 @@ FORK = dict(cache=None, table=FAKE, ld_table=4, lens=FAKE, refs=FAKE, parents=FA
             stream=None)
 COMPACT = dict(cache=None, table=FAKE, ld_table=4, refs=FAKE, table_out=FAKE2, ld_out=4, refs_out=FAKE2, live=FAKE, S=2,
                W=4, workspace=FAKE, workspace_bytes=1 << 20, stream=None)
-CALLS = {"append": APPEND, "read": READ, "copy_pages": COPY, "fork": FORK, "compact": COMPACT}
+DECODE = dict(q=FAKE, q_seq=256, q_head=64, cache=None, table=FAKE, ld_table=400, W=400, lens=FAKE, out=FAKE2, out_seq=256,
+              out_head=64, B=2, Hq=4, scale=0.125, workspace=FAKE, workspace_bytes=1 << 40, stream=None)
+CALLS = {"append": APPEND, "read": READ, "copy_pages": COPY, "fork": FORK, "compact": COMPACT,
+         "decode": DECODE}
 
 
 def call(name, cache=None, no_cache=False, **changed):
@@ -41,7 +44,7 @@ def call(name, cache=None, no_cache=False, **changed):
     args.update(changed)
     desc = cf.Cache8Desc(**{**CACHE, **(cache or {})})
     args["cache"] = None if no_cache else ctypes.addressof(desc)
-    return getattr(cf, "cfp32_cache8_" + name)(**args)
+    return getattr(cf, "cfp32_attention8_decode" if name == "decode" else "cfp32_cache8_" + name)(**args)
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -64,7 +67,7 @@ WRITTEN = [dict(k_tok=63), dict(v_page=2047), dict(k_head=0), dict(ks_head=1), d
 @pytest.mark.parametrize("name", CALLS)
 def test_refused_pools(name):
     assert call(name, no_cache=True) == E
-    for bad in BOTH + (WRITTEN if name != "read" else []):
+    for bad in BOTH + (WRITTEN if name not in ("read", "decode") else []):
         assert call(name, cache=bad) == E, bad
 
 
@@ -82,6 +85,10 @@ REFUSED = {
     "compact": [dict(table=None), dict(refs=None), dict(table_out=None), dict(refs_out=None), dict(live=None),
                 dict(workspace=None), dict(workspace_bytes=100), dict(ld_out=3), dict(table_out=FAKE, ld_out=5),
                 dict(S=-1)],
+    "decode": [dict(q=None), dict(table=None), dict(lens=None), dict(out=None), dict(B=-1), dict(Hq=3), dict(Hq=-4),
+               dict(W=-1), dict(ld_table=399), dict(W=1 << 28, ld_table=1 << 28), dict(q=FAKE + 2), dict(out=FAKE + 1),
+               dict(q_seq=-1), dict(out_seq=255), dict(out_head=63), dict(scale=float("nan")), dict(scale=1e39),
+               dict(workspace=None), dict(workspace_bytes=100), dict(B=1 << 30, Hq=1 << 30)],
 }
 
 
@@ -98,6 +105,18 @@ def test_empty_problems_are_no_ops():
     assert call("copy_pages", n=0, src=None, dst=None) == OK
     assert call("copy_pages", cache=dict(P=0)) == OK
     assert call("fork", cache=dict(P=0), C=0, refs=None, refs_out=None) == OK
+    assert call("decode", B=0, q=None, table=None, lens=None) == OK
+    assert call("decode", cache=dict(D=0), workspace=None) == OK
+    assert call("decode", cache=dict(Hkv=0), Hq=0) == OK
+
+
+def test_workspace_queries():
+    need = cf.cfp32_attention8_decode_workspace_bytes
+    assert need(2, 4, 2, 64, 4, 16) == 0  # one step of keys: no parts
+    assert need(1, 32, 8, 128, 1024, 64) > 0
+    for bad in ((-1, 4, 2, 64, 4, 16), (2, 3, 2, 64, 4, 16), (2, 4, 2, 129, 4, 16), (2, 4, 2, 64, -1, 16), (2, 4, 2, 64, 4, 17),
+                (2, 4, 2, 64, 1 << 28, 16), (2 ** 31 - 1, 2 ** 30, 1, 64, 4, 16), (2, 65536, 65536, 64, 4, 16)):
+        assert need(*bad) == 0, bad
 
 
 def test_the_description_is_the_headers():
@@ -121,6 +140,6 @@ def test_the_helpers_check_their_tensors():
     i = torch.zeros(3, dtype=torch.int32)
     for f in (lambda: cf.cache8_append(codes, codes, i, codes, i, i), lambda: cf.cache8_read(codes, i, i, 3),
               lambda: cf.cache8_fork(codes, i, i, i, i), lambda: cf.cache8_compact(codes, i, i),
-              lambda: cf.cache8_copy_pages(codes, i, i)):
+              lambda: cf.cache8_copy_pages(codes, i, i), lambda: cf.attention8_decode(scales, codes, i, i)):
         with pytest.raises(TypeError):
             f()
