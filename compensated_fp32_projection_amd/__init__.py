@@ -71,6 +71,9 @@ EXPORTS = (
     "cfp32_cache8_compact",
     "cfp32_attention8_decode_workspace_bytes",
     "cfp32_attention8_decode",
+    "cfp32_beam_select_workspace_bytes",
+    "cfp32_beam_select",
+    "cfp32_beam_reorder",
 )
 
 W_KN, W_NK = 0, 1
@@ -118,7 +121,7 @@ def load_library():
     held = ctypes.PyDLL(LIB_PATH)
     for name in ("cfp32_linear", "cfp32_linear_ex", "cfp32_linear_geglu", "cfp32_attention_prompt",
                  "cfp32_attention_decode", "cfp32_cache_fork", "cfp32_cache_compact", "cfp32_cache8_fork",
-                 "cfp32_cache8_compact", "cfp32_attention8_decode"):
+                 "cfp32_cache8_compact", "cfp32_attention8_decode", "cfp32_beam_select"):
         setattr(lib, name, getattr(held, name))
     P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     lib.cfp32_status_string.argtypes = [I32]
@@ -197,6 +200,12 @@ def load_library():
     lib.cfp32_attention8_decode_workspace_bytes.restype = SZ
     lib.cfp32_attention8_decode.argtypes = view + [P, P, I64, I64, P] + view + [I64, I64, F64, P, SZ, P]
     lib.cfp32_attention8_decode.restype = I32
+    lib.cfp32_beam_select_workspace_bytes.argtypes = [I64] * 4
+    lib.cfp32_beam_select_workspace_bytes.restype = SZ
+    lib.cfp32_beam_select.argtypes = [P, I64, P, P] + [I64] * 5 + [P] * 5 + [SZ, P]
+    lib.cfp32_beam_select.restype = I32
+    lib.cfp32_beam_reorder.argtypes = [P, I64, P, I64, P, I64, I64, I64, P]
+    lib.cfp32_beam_reorder.restype = I32
     _lib = lib
     return lib
 
@@ -387,6 +396,20 @@ def cfp32_attention8_decode(q, q_seq, q_head, cache, table, ld_table, W, lens, o
                             workspace, workspace_bytes, stream) -> int:
     return int(load_library().cfp32_attention8_decode(q, q_seq, q_head, cache, table, ld_table, W, lens, out, out_seq,
                                                       out_head, B, Hq, scale, workspace, workspace_bytes, stream))
+
+
+def cfp32_beam_select_workspace_bytes(S, beams, V, n) -> int:
+    return int(load_library().cfp32_beam_select_workspace_bytes(S, beams, V, n))
+
+
+def cfp32_beam_select(logits, ld, scores, done, S, beams, V, n, eos, parents, tokens, scores_out, done_out, workspace,
+                      workspace_bytes, stream) -> int:
+    return int(load_library().cfp32_beam_select(logits, ld, scores, done, S, beams, V, n, eos, parents, tokens, scores_out,
+                                                done_out, workspace, workspace_bytes, stream))
+
+
+def cfp32_beam_reorder(states, stride, out, out_stride, parents, rows, n, row_bytes, stream) -> int:
+    return int(load_library().cfp32_beam_reorder(states, stride, out, out_stride, parents, rows, n, row_bytes, stream))
 
 
 # -- tensor helpers -------------------------------------------------------------
@@ -1246,4 +1269,72 @@ def attention8_decode(q, cache: Cache8, table, lens, scale: float | None = None,
         buf, ws, st = _scratch(need, dev, workspace, stream)
         _check(cfp32_attention8_decode(*pq, cache.addr, pt, _ld(table), W, pl, *po, B, Hq,
                                        D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention8_decode")
+    return out
+
+
+# -- beam search -----------------------------------------------------------------------
+
+def beam_select(logits, scores, n: int | None = None, done=None, eos: int = -1, workspace: Workspace | None = None,
+                stream=None):
+    """(parents, tokens, scores, done), [S, n] each (n: as many beams as there
+    are unless given; at most 64): the best continuations of S sequences.
+    logits FP32 [S * beams, V]; scores FP32 [S, beams], the beams' sums of
+    log-probabilities; done bool [S, beams] or None; eos: the token that
+    finishes a beam.  parents are rows of the batch of S * beams beams, as
+    ``beam_reorder`` and ``cache_fork`` take them (-1 where there is no
+    offer)."""
+    torch = _torch()
+    px, rows, V, ld = _mat(logits, (torch.float32,), "logits")
+    dev = logits.device
+    if not isinstance(scores, torch.Tensor) or scores.dtype != torch.float32 or scores.device != dev:
+        raise TypeError("scores: expected a float32 tensor on logits' device")
+    if scores.dim() != 2 or not scores.is_contiguous() or scores.numel() != rows:
+        raise ValueError("scores must be contiguous [sequences, beams], a beam to each row of logits")
+    S, beams = scores.shape
+    if done is not None:
+        if not isinstance(done, torch.Tensor) or done.dtype not in (torch.bool, torch.uint8) or done.device != dev:
+            raise TypeError("done: expected a bool tensor on logits' device")
+        if done.shape != scores.shape or not done.is_contiguous():
+            raise ValueError("done must be contiguous, of the shape of scores")
+    n = beams if n is None else n
+    with torch.cuda.device(dev):
+        parents, tokens = (_empty((S, n), torch.int32, dev, stream) for _ in range(2))
+        out, ended = _empty((S, n), torch.float32, dev, stream), _empty((S, n), torch.bool, dev, stream)
+        need = cfp32_beam_select_workspace_bytes(S, beams, V, n)
+        buf, ws, st = _scratch(need, dev, workspace, stream)
+        _check(cfp32_beam_select(px, ld, scores.data_ptr(), None if done is None else done.data_ptr(), S, beams, V, n, eos,
+                                 parents.data_ptr(), tokens.data_ptr(), out.data_ptr(), ended.data_ptr(), ws, need, st),
+               "cfp32_beam_select")
+    return parents, tokens, out, ended
+
+
+def beam_reorder(states, parents, out=None, stream=None):
+    """Rows of ``states`` [rows, ...] (any type, contiguous rows) in the order of
+    ``parents`` (int32, any shape): [parents.numel(), ...]; zeros where a parent
+    is no row."""
+    torch = _torch()
+    if not isinstance(states, torch.Tensor) or states.device.type != "cuda":
+        raise TypeError("states: expected a GPU tensor")
+    dev = states.device
+    if not isinstance(parents, torch.Tensor) or parents.dtype != torch.int32 or parents.device != dev:
+        raise TypeError("parents: expected an int32 tensor on states' device")
+    if not parents.is_contiguous():
+        raise ValueError("parents must be contiguous")
+    rest = states.shape[1:]
+    if states.dim() < 1 or (states.shape[0] and not states[0].is_contiguous()):
+        raise ValueError("states must have contiguous rows")
+    shape, size = (parents.numel(), *rest), states.element_size()
+    row = size
+    for d in rest:
+        row *= d
+    if out is None:
+        out = _empty(shape, states.dtype, dev, stream)
+    elif out.shape != shape or out.dtype != states.dtype or out.device != dev or (shape[0] and not out[0].is_contiguous()):
+        raise ValueError("out must have a row for each parent, of the type of states")
+
+    def stride(t):
+        return t.stride(0) * size if t.shape[0] > 1 else row
+
+    _launch(cfp32_beam_reorder, "cfp32_beam_reorder", dev, states.data_ptr(), stride(states), out.data_ptr(), stride(out),
+            parents.data_ptr(), states.shape[0], shape[0], row, stream=stream)
     return out

@@ -1,0 +1,303 @@
+// Beam search (include/cfp32.h: cfp32_beam_select, cfp32_beam_reorder).
+//
+// A beam's offers are ordered as its logits are, so the n best of a sequence are
+// among the n largest logits of each beam.  One launch passes over the logits:
+// a wave takes 512 or 2048 of a row, holds them in registers, and leaves
+//   * the largest of its logits and the sum of exp(x - largest);
+//   * its n largest logits with their tokens, in order.  The n-th largest of
+//     the lanes' own largest is a lower bound of the n-th largest of all, so
+//     few logits but the wanted ones reach the sort.
+// The second launch, a block to a sequence, joins a row's sums and lists, a wave
+// to a beam, and merges the beams' lists.  The logits are read once; that
+// bounds the first launch, latency the second.
+#include "beam.h"
+#include "device_common.h"
+
+namespace cfp32 {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// A logit and its token as one number: larger logits first, of equal ones the
+// lower token.  0: none.
+__device__ __forceinline__ uint64_t offer_key(float x, int token)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);  // one zero
+    const uint32_t o = b >> 31 ? ~b : b | 0x80000000u;
+    return (uint64_t)o << 32 | (uint32_t)~token;
+}
+__device__ __forceinline__ float key_logit(uint64_t k)
+{
+    const uint32_t o = (uint32_t)(k >> 32);
+    return __builtin_bit_cast(float, o >> 31 ? o & 0x7FFFFFFFu : ~o);
+}
+__device__ __forceinline__ int key_token(uint64_t k) { return (int)~(uint32_t)k; }
+
+template <class V>
+__device__ __forceinline__ V exchange(V v, int j, bool keep_larger)
+{
+    const V o = __shfl_xor(v, j);
+    return (v > o) == keep_larger ? v : o;
+}
+
+// Bitonic: the wave's values in order, the largest in lane 0.
+template <class V>
+__device__ __forceinline__ V sort_wave(V v)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 2; k <= 64; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j; j >>= 1) v = exchange(v, j, ((lane & j) == 0) == ((lane & k) == 0));
+    return v;
+}
+
+// The 64 largest of two wave's lists that are in order, in order.
+__device__ __forceinline__ uint64_t merge_wave(uint64_t a, uint64_t b)
+{
+    const int lane = threadIdx.x & 63;
+    const uint64_t r = __shfl_xor(b, 63);
+    uint64_t v = a > r ? a : r;
+#pragma unroll
+    for (int j = 32; j; j >>= 1) v = exchange(v, j, (lane & j) == 0);
+    return v;
+}
+
+// The largest keys seen by a wave, in order, and those that wait to be sorted
+// into them (in LDS, of this wave alone).
+struct Best {
+    uint64_t top;       // lane i: the i-th largest
+    uint64_t *waiting;  // [128]
+    int count;
+    bool any;
+    __device__ __forceinline__ void sync() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+    // `mine`: this lane's key is to be taken.  All lanes call.
+    __device__ __forceinline__ void add(bool mine, uint64_t key)
+    {
+        const uint64_t mask = __ballot(mine);
+        if (!mask) return;
+        const int lane = threadIdx.x & 63;
+        if (mine) waiting[count + __popcll(mask & (((uint64_t)1 << lane) - 1))] = key;
+        count += __popcll(mask);
+        if (count >= 64) flush();
+    }
+    __device__ __forceinline__ void flush()
+    {
+        const int lane = threadIdx.x & 63;
+        sync();
+        const uint64_t k = sort_wave(lane < count ? waiting[lane] : (uint64_t)0);
+        top = any ? merge_wave(top, k) : k;
+        any = true;
+        const uint64_t rest = waiting[64 + lane];
+        sync();
+        count = count > 64 ? count - 64 : 0;
+        if (lane < count) waiting[lane] = rest;
+    }
+};
+
+// E logits of a lane, VEC at a time (4: rows allow loads of 16 bytes).
+template <int E, int VEC>
+__global__ __launch_bounds__(256) void beam_rows_kernel(BeamArgs a, int chunks, float2 *stats, uint64_t *lists)
+{
+    __shared__ uint64_t waiting[4][128];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = (int64_t)blockIdx.x * 4 + wave, row = unit / chunks;
+    const int chunk = (int)(unit - row * chunks);
+    if (row >= (int64_t)a.S * a.beams) return;
+    if (a.done && a.done[row]) return;
+    const float score = a.scores[row];
+    if (!(fabsf(score) < INFINITY)) return;
+
+    // Which logits a lane takes does not depend on where the row lies, so equal
+    // rows have equal sums, and equal offers stay equal.
+    const float *x0 = a.logits + row * a.ld;
+    auto token = [&](int e) { return (int64_t)chunk * (64 * E) + (64 * (e / VEC) + lane) * VEC + e % VEC; };
+    float x[E];
+#pragma unroll
+    for (int e = 0; e < E; e += VEC) {
+        const int64_t t = token(e);
+        if (VEC == 4 && t + 4 <= a.V) {
+            const floatx4_t w = *reinterpret_cast<const floatx4_t *>(x0 + t);
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) x[e + u] = w[u];
+        } else {
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) x[e + u] = t + u < a.V ? x0[t + u] : -INFINITY;
+        }
+    }
+    float mine = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) mine = fmaxf(mine, x[e]);
+    const float sorted = sort_wave(mine);
+    const float most = __shfl(sorted, 0), least = __shfl(sorted, a.n - 1);
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((x[e] - most) * kLog2e);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+    // A NaN, or infinity less itself, leaves a sum of NaN; of nothing but -infinity (and no NaN) it is 0.
+    if (most == -INFINITY) {
+        float odd = 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) odd = x[e] != x[e] ? NAN : odd;
+        sum = __any(odd != odd) ? NAN : 0.0f;
+    }
+
+    Best best = {0, waiting[wave], 0, false};
+#pragma unroll
+    for (int e = 0; e < E; ++e) best.add(x[e] >= least && x[e] > -INFINITY, offer_key(x[e], (int)token(e)));
+    if (best.count) best.flush();
+    if (lane < a.n) lists[unit * a.n + lane] = best.top;
+    if (lane == 0) stats[unit] = make_float2(most, sum);
+}
+
+// A wave's sum of doubles.
+__device__ __forceinline__ double wave_sum(double v)
+{
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+__global__ __launch_bounds__(1024) void beam_join_kernel(BeamArgs a, int chunks, const float2 *stats, const uint64_t *lists)
+{
+    extern __shared__ double totals[];                // [beams][n]
+    int *tokens = (int *)(totals + a.beams * a.n);    // [beams][n]
+    __shared__ uint64_t waiting[16][128];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int64_t s = blockIdx.x;
+    for (int b = wave; b < a.beams; b += waves) {
+        const int64_t row = s * a.beams + b;
+        const float score = a.scores[row];
+        double total = -INFINITY;
+        int token = -1;
+        if (!(fabsf(score) < INFINITY)) {
+        } else if (a.done && a.done[row]) {
+            if (lane == 0) {
+                total = score;
+                token = a.eos;
+            }
+        } else {
+            const float2 *st = stats + row * chunks;
+            float most = -INFINITY;
+            for (int i = lane; i < chunks; i += 64) most = fmaxf(most, st[i].x);
+#pragma unroll
+            for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
+            double sum = 0.0;
+            for (int i = lane; i < chunks; i += 64) {
+                const float2 c = st[i];
+                if (c.y != 0.0f) sum += (double)c.y * exp((double)c.x - (double)most);
+            }
+            sum = wave_sum(sum);
+            Best best = {0, waiting[wave], 0, false};
+            const uint64_t *keys = lists + row * chunks * a.n;
+            const int64_t count = (int64_t)chunks * a.n;
+            for (int64_t i0 = 0; i0 < count; i0 += 64) {
+                const int64_t i = i0 + lane;
+                const uint64_t k = i < count ? keys[i] : 0;
+                const uint64_t least = best.any ? __shfl(best.top, a.n - 1) : 0;
+                best.add(k > least, k);
+            }
+            if (best.count) best.flush();
+            if (sum > 0.0 && sum < INFINITY && lane < a.n && best.any && best.top) {
+                const double lse = (double)most + log(sum);
+                total = (double)score + ((double)key_logit(best.top) - lse);
+                token = key_token(best.top);
+            }
+        }
+        if (lane < a.n) {
+            totals[b * a.n + lane] = total;
+            tokens[b * a.n + lane] = token;
+        }
+    }
+    __syncthreads();
+    if (wave) return;
+    // Lane b holds the best offer of beam b that is left.
+    int at = 0;
+    for (int i = 0; i < a.n; ++i) {
+        double v = lane < a.beams && at < a.n ? totals[lane * a.n + at] : -INFINITY;
+        int who = lane;
+#pragma unroll
+        for (int o = 32; o; o >>= 1) {
+            const double w = __shfl_xor(v, o);
+            const int x = __shfl_xor(who, o);
+            if (w > v || (w == v && x < who)) v = w, who = x;
+        }
+        const bool some = v > -INFINITY;
+        const int64_t out = s * a.n + i;
+        if (lane == who) {
+            const int token = some ? tokens[lane * a.n + at] : a.eos;
+            const bool was = some && a.done && a.done[s * a.beams + lane];
+            a.parents[out] = some ? (int)(s * a.beams) + lane : -1;
+            a.tokens[out] = token;
+            a.scores_out[out] = (float)v;
+            if (a.done_out) a.done_out[out] = !some || was || (a.eos >= 0 && token == a.eos);
+            ++at;
+        }
+    }
+}
+
+template <class V>
+__global__ __launch_bounds__(256) void beam_reorder_kernel(const char *states, int64_t stride, char *out, int64_t out_stride,
+                                                           const int32_t *parents, int rows, int n, int64_t vecs)
+{
+    const int64_t total = n * vecs;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / vecs, c = i - r * vecs;
+        const int p = parents[r];
+        V v = {};
+        if (p >= 0 && p < rows) v = *reinterpret_cast<const V *>(states + p * stride + c * (int64_t)sizeof(V));
+        *reinterpret_cast<V *>(out + r * out_stride + c * (int64_t)sizeof(V)) = v;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_beam_select(const BeamArgs &a, void *workspace, hipStream_t stream)
+{
+    const BeamPlan p = plan_beam(a.S, a.beams, a.V, a.n);
+    const int64_t units = (int64_t)a.S * a.beams * p.chunks, blocks = (units + 3) / 4;
+    if (blocks > 0x7FFFFFFF || blocks * 256 > 0xFFFFFFFF) return hipErrorInvalidConfiguration;
+    float2 *stats = (float2 *)workspace;
+    uint64_t *lists = (uint64_t *)(stats + units);
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.logits) | (uintptr_t)(a.ld * 4)) & 15) == 0;
+#define CFP32_BEAM_ROWS(E, VEC) beam_rows_kernel<E, VEC><<<(unsigned)blocks, 256, 0, stream>>>(a, p.chunks, stats, lists)
+    if (p.each == 32) {
+        if (wide) CFP32_BEAM_ROWS(32, 4);
+        else CFP32_BEAM_ROWS(32, 1);
+    } else {
+        if (wide) CFP32_BEAM_ROWS(8, 4);
+        else CFP32_BEAM_ROWS(8, 1);
+    }
+#undef CFP32_BEAM_ROWS
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int waves = a.beams < 16 ? a.beams : 16;
+    const size_t lds = (size_t)a.beams * a.n * (sizeof(double) + sizeof(int));
+    beam_join_kernel<<<(unsigned)a.S, 64 * waves, lds, stream>>>(a, p.chunks, stats, lists);
+    return hipGetLastError();
+}
+
+hipError_t launch_beam_reorder(const void *states, int64_t stride, void *out, int64_t out_stride, const int32_t *parents,
+                               int rows, int n, int64_t row_bytes, hipStream_t stream)
+{
+    typedef uint32_t vec4_t __attribute__((ext_vector_type(4)));
+    const int64_t m = 16 | row_bytes | stride | out_stride | (int64_t)((uintptr_t)states | (uintptr_t)out);
+    const int vec = (int)(m & -m);
+    const int64_t vecs = row_bytes / vec, blocks = (n * vecs + 255) / 256;
+    const unsigned grid = (unsigned)(blocks < 16384 ? blocks : 16384);
+#define CFP32_REORDER(V) \
+    beam_reorder_kernel<V><<<grid, 256, 0, stream>>>((const char *)states, stride, (char *)out, out_stride, parents, rows, n, vecs)
+    switch (vec) {
+    case 16: CFP32_REORDER(vec4_t); break;
+    case 8: CFP32_REORDER(uint64_t); break;
+    case 4: CFP32_REORDER(uint32_t); break;
+    case 2: CFP32_REORDER(uint16_t); break;
+    default: CFP32_REORDER(uint8_t); break;
+    }
+#undef CFP32_REORDER
+    return hipGetLastError();
+}
+
+}  // namespace cfp32

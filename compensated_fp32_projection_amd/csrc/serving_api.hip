@@ -3,6 +3,7 @@
 // Every call validates all of its arguments before it enqueues anything.
 #include "api_checks.h"
 #include "attention8.h"
+#include "beam.h"
 #include "rotary.h"
 
 namespace {
@@ -234,6 +235,44 @@ cfp32_status cfp32_attention8_decode(const float *q, int64_t q_seq, int64_t q_he
     const Decode8Args a = {q, q_seq, q_head, view_of(cache), table, ld_table, lens, out, out_seq, out_head, (int)B, (int)Hq,
                            (int)W, (float)scale};
     return api_launched(launch_attention8_decode(a, align_up(workspace), (hipStream_t)stream));
+}
+
+size_t cfp32_beam_select_workspace_bytes(int64_t S, int64_t beams, int64_t V, int64_t n)
+{
+    if (!size_ok(S) || beams < 1 || beams > kMaxBeams || n < 1 || n > kMaxBeams || V < 1 || V > kMaxSize - 4096) return 0;
+    if (S == 0 || S > kMaxSize / kMaxBeams) return 0;
+    return plan_beam(S, beams, V, n).bytes + kAlign;
+}
+
+cfp32_status cfp32_beam_select(const float *logits, int64_t ld, const float *scores, const uint8_t *done, int64_t S,
+                               int64_t beams, int64_t V, int64_t n, int64_t eos, int32_t *parents, int32_t *tokens,
+                               float *scores_out, uint8_t *done_out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!size_ok(S) || S > kMaxSize / kMaxBeams || beams < 1 || beams > kMaxBeams || n < 1 || n > kMaxBeams || V < 1 ||
+        V > kMaxSize - 4096 || ld < V || eos < -kMaxSize || eos > kMaxSize)
+        return CFP32_ERR_INVALID_VALUE;
+    if (S == 0) return CFP32_OK;
+    if (!logits || !scores || !parents || !tokens || !scores_out || !aligned_to(logits, 4) || !view_ok(S * beams, ld, 1, 0, 1, 0, V))
+        return CFP32_ERR_INVALID_VALUE;
+    if (!workspace || workspace_bytes < cfp32_beam_select_workspace_bytes(S, beams, V, n)) return CFP32_ERR_INVALID_VALUE;
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    const BeamArgs a = {logits, ld, scores, done, (int)S, (int)beams, (int)V, (int)n, (int)eos, parents, tokens, scores_out, done_out};
+    return api_launched(launch_beam_select(a, align_up(workspace), (hipStream_t)stream));
+}
+
+cfp32_status cfp32_beam_reorder(const void *states, int64_t stride, void *out, int64_t out_stride, const int32_t *parents,
+                                int64_t rows, int64_t n, int64_t row_bytes, void *stream)
+{
+    if (!size_ok(rows) || !size_ok(n) || row_bytes < 0 || row_bytes > kMaxDim || !term_ok(rows, stride) || out_stride < row_bytes ||
+        !term_ok(n, out_stride) || (n > 0 && row_bytes > kMaxDim / n))
+        return CFP32_ERR_INVALID_VALUE;
+    if (n == 0 || row_bytes == 0) return CFP32_OK;
+    if ((rows > 0 && !states) || !out || !parents || out == states) return CFP32_ERR_INVALID_VALUE;
+    cfp32_status st = api_check_device();
+    if (st != CFP32_OK) return st;
+    return api_launched(launch_beam_reorder(states, stride, out, out_stride, parents, (int)rows, (int)n, row_bytes,
+                                            (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -652,6 +652,44 @@ CFP32_API cfp32_status cfp32_attention8_decode(const float *q, int64_t q_seq, in
                                      int64_t out_seq, int64_t out_head, int64_t B, int64_t Hq, double scale,
                                      void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Beam search ------------------------------------------------------------------
+ *
+ * One step of a search that keeps the best `n` continuations of S sequences: the
+ * selection over beams and vocabulary, and the beams' states put in their new
+ * order.  The parents it returns are rows of the batch of S * beams beams, which
+ * cfp32_beam_reorder takes, and cfp32_cache_fork and cfp32_cache8_fork for the
+ * beams' pages (cfp32_cache_free then gives up the old tables').
+ */
+
+/* Workspace bytes of cfp32_beam_select; 0 for sizes it refuses. */
+CFP32_API size_t cfp32_beam_select_workspace_bytes(int64_t S, int64_t beams, int64_t V, int64_t n);
+
+/* The n best continuations of each sequence.
+ *   logits : FP32 [S * beams, V], leading dimension ld >= V.
+ *   scores : FP32 [S, beams], the beams' sums of log-probabilities.
+ *   done   : uint8 [S, beams], nonzero for finished beams, or NULL for none.
+ *   beams, n : 1 .. 64;  V >= 1, below 2^31.
+ *   eos    : the token that finishes a beam (negative: none does).
+ *   parents, tokens : int32 [S, n];  scores_out : FP32 [S, n];
+ *   done_out : uint8 [S, n] (0 or 1) or NULL.
+ * Beam b offers token t with scores[b] + x_t - log sum exp(x) (the sum's
+ * terms FP32, off by some 2^-22, FP64 from there on; rounded once, at the end).  A finished beam offers itself alone, with its score and the token eos.
+ * Offers are taken in order of their scores, of equal ones the lowest beam's
+ * and of a beam's equal logits the lowest token first; a beam's are in the order
+ * of its logits.  A token whose logit is -infinity is not offered, nor is
+ * anything of a beam whose score is not finite, or of one whose logits hold a
+ * NaN or +infinity.  Where there are fewer than n offers, the rest has parent
+ * -1, token eos, score -infinity and is done.  Two kernel launches. */
+CFP32_API cfp32_status cfp32_beam_select(const float *logits, int64_t ld, const float *scores, const uint8_t *done, int64_t S,
+                               int64_t beams, int64_t V, int64_t n, int64_t eos, int32_t *parents, int32_t *tokens,
+                               float *scores_out, uint8_t *done_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Rows of states in the order of their parents: row i of out [n] is row
+ * parents[i] of states [rows], or zeros where that is no row.  Rows are row_bytes
+ * long, at strides of bytes (>= row_bytes; those of states >= 0).  One kernel launch. */
+CFP32_API cfp32_status cfp32_beam_reorder(const void *states, int64_t stride, void *out, int64_t out_stride,
+                                const int32_t *parents, int64_t rows, int64_t n, int64_t row_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
