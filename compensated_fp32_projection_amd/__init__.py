@@ -697,7 +697,9 @@ def _native():
         names = ("cfp32_attention_prompt_workspace_bytes", "cfp32_attention_prompt",
                  "cfp32_attention_decode_workspace_bytes", "cfp32_attention_decode", "cfp32_cache_reserve",
                  "cfp32_cache_append", "cfp32_cache_fork_workspace_bytes", "cfp32_cache_fork", "cfp32_cache_free",
-                 "cfp32_cache_compact_workspace_bytes", "cfp32_cache_compact")
+                 "cfp32_cache_compact_workspace_bytes", "cfp32_cache_compact", "cfp32_rotary", "cfp32_cache8_append",
+                 "cfp32_cache8_read", "cfp32_attention8_decode_workspace_bytes", "cfp32_attention8_decode",
+                 "cfp32_beam_select_workspace_bytes", "cfp32_beam_select", "cfp32_beam_reorder")
         mod.bind(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
                  torch._C._cuda_getCurrentRawStream, _scratch_buffer)
         _helpers = mod
@@ -1042,6 +1044,10 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
     q_out and k_out may be q and k."""
     if layout not in ("half", "interleaved"):
         raise ValueError("layout must be 'half' or 'interleaved'")
+    if stream is None:
+        done = _native().rotary(q, k, frequencies, positions, layout == "interleaved", amplitude, transpose, q_out, k_out)
+        if done is not None:
+            return done
     torch = _torch()
     if not isinstance(q, torch.Tensor) or q.device.type != "cuda":
         raise TypeError("q: expected a GPU tensor")
@@ -1087,7 +1093,7 @@ class Cache8:
     page / block], one for each block of tokens and head (``blocks`` of a
     page: powers of two).  Holds the tensors; the calls read and write them."""
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "desc", "addr", "device", "shape", "block")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "desc", "addr", "device", "index", "shape", "block")
 
     def __init__(self, k, v, k_scales, v_scales):
         torch = _torch()
@@ -1116,7 +1122,7 @@ class Cache8:
         self.desc = Cache8Desc(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3], k_scales.data_ptr(),
                                v_scales.data_ptr(), *k_scales.stride()[:2], *v_scales.stride()[:2], P, Hkv, page,
                                self.block, D, CODE_I8 if k.dtype == torch.int8 else CODE_E4M3)
-        self.addr = ctypes.addressof(self.desc)
+        self.addr, self.index = ctypes.addressof(self.desc), k.device.index
 
     @classmethod
     def empty(cls, pages: int, heads: int, page: int, dim: int, block: int | None = None, dtype=None, device="cuda"):
@@ -1141,6 +1147,10 @@ def cache8_append(k, v, cu, cache: Cache8, table, lens, lens_out=None, stream=No
     ``cache_append``: rows cu[s] .. cu[s+1] - 1 become tokens lens[s], ... of
     sequence s.  Returns the new lengths."""
     P, Hkv, page, D = _cache8(cache).shape
+    if stream is None and lens_out is None:
+        done = _native().cache8_append(k, v, cu, cache.addr, cache.index, table, lens)
+        if done is not None:
+            return done
     dev = cache.device
     torch = _torch()
     pk, pv = _heads(k, (torch.float32,), "k", dev), _heads(v, (torch.float32,), "v", dev)
@@ -1169,6 +1179,12 @@ def cache8_read(cache: Cache8, table, cu, tokens: int, first=None, dtype=None, k
     P, Hkv, page, D = _cache8(cache).shape
     dev = cache.device
     dtype = torch.float32 if dtype is None else dtype
+    if dtype not in (torch.float32, torch.float16):
+        raise TypeError("dtype must be float32 or float16")
+    if stream is None and k_out is None and v_out is None:
+        done = _native().cache8_read(cache.addr, cache.index, table, cu, tokens, first, dtype == torch.float16)
+        if done is not None:
+            return done
     pt, pc = _ints(table, "table", dev, 2), _ints(cu, "cu", dev, 1)
     S, W = table.shape
     pf = None if first is None else _ints(first, "first", dev, 1)
@@ -1180,8 +1196,7 @@ def cache8_read(cache: Cache8, table, cu, tokens: int, first=None, dtype=None, k
         if out.shape != (tokens, Hkv, D):
             raise ValueError(f"{name} has the wrong shape")
         outs.append(out)
-    pk, pv = (_heads(o, (torch.float32,) if dtype == torch.float32 else (torch.float16,), n, dev)
-              for o, n in zip(outs, ("k_out", "v_out")))
+    pk, pv = (_heads(o, (dtype,), n, dev) for o, n in zip(outs, ("k_out", "v_out")))
     _launch(cfp32_cache8_read, "cfp32_cache8_read", dev, cache.addr, pt, _ld(table), pf, pc, *pk, *pv,
             KV_F16 if dtype == torch.float16 else KV_F32, S, W, tokens, stream=stream)
     return outs[0], outs[1]
@@ -1250,6 +1265,10 @@ def attention8_decode(q, cache: Cache8, table, lens, scale: float | None = None,
     [B, Hq, D]; table int32 [B, W]; lens int32 [B].  Returns FP32 [B, Hq, D]."""
     torch = _torch()
     P, Hkv, page, D2 = _cache8(cache).shape
+    if stream is None and workspace is None:
+        done = _native().attention8_decode(q, cache.addr, cache.index, table, lens, scale, out)
+        if done is not None:
+            return done
     dev = cache.device
     pq = _heads(q, (torch.float32,), "q", dev)
     B, Hq, D = q.shape
@@ -1283,6 +1302,10 @@ def beam_select(logits, scores, n: int | None = None, done=None, eos: int = -1, 
     finishes a beam.  parents are rows of the batch of S * beams beams, as
     ``beam_reorder`` and ``cache_fork`` take them (-1 where there is no
     offer)."""
+    if stream is None and workspace is None:
+        done_ = _native().beam_select(logits, scores, n, done, eos)
+        if done_ is not None:
+            return done_
     torch = _torch()
     px, rows, V, ld = _mat(logits, (torch.float32,), "logits")
     dev = logits.device
@@ -1312,6 +1335,10 @@ def beam_reorder(states, parents, out=None, stream=None):
     """Rows of ``states`` [rows, ...] (any type, contiguous rows) in the order of
     ``parents`` (int32, any shape): [parents.numel(), ...]; zeros where a parent
     is no row."""
+    if stream is None and out is None:
+        done = _native().beam_reorder(states, parents)
+        if done is not None:
+            return done
     torch = _torch()
     if not isinstance(states, torch.Tensor) or states.device.type != "cuda":
         raise TypeError("states: expected a GPU tensor")

@@ -1,4 +1,4 @@
-// The attention and cache helpers of __init__.py for their plain calls: GPU
+// The attention, cache, rotary and beam helpers of __init__.py for their plain calls: GPU
 // tensors of the right types and shapes, the current stream, the helpers' own
 // workspace.  Each checks its arguments, allocates its results and calls the
 // C ABI, as the Python form does, in 3 to 6 us of host time instead of 15 to
@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -34,6 +35,14 @@ struct Api {
     decltype(&cfp32_cache_free) free;
     decltype(&cfp32_cache_compact_workspace_bytes) compact_ws;
     decltype(&cfp32_cache_compact) compact;
+    decltype(&cfp32_rotary) rotary;
+    decltype(&cfp32_cache8_append) append8;
+    decltype(&cfp32_cache8_read) read8;
+    decltype(&cfp32_attention8_decode_workspace_bytes) decode8_ws;
+    decltype(&cfp32_attention8_decode) decode8;
+    decltype(&cfp32_beam_select_workspace_bytes) select_ws;
+    decltype(&cfp32_beam_select) select;
+    decltype(&cfp32_beam_reorder) reorder;
 } api;
 PyObject *raw_stream, *scratch;
 
@@ -336,6 +345,192 @@ PyObject *compact(PyObject *const *a)
     return tuple_of({to, ro, live});
 }
 
+// The device is the current one: launches go there.
+bool current(c10::Device dev) { return c10::impl::VirtualGuardImpl(c10::DeviceType::CUDA).getDevice() == dev; }
+
+// An integer argument (-1 with false: none).
+bool whole(PyObject *o, int64_t &v)
+{
+    if (!PyLong_CheckExact(o)) return false;
+    v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+    }
+    return true;
+}
+
+// The description that a Cache8 holds, and its device: (address, device index).
+bool cache8(PyObject *addr, PyObject *index, c10::Device &dev, const cfp32_cache8 *&c)
+{
+    int64_t i;
+    if (!PyLong_CheckExact(addr) || !whole(index, i) || i < 0) return false;
+    c = (const cfp32_cache8 *)PyLong_AsVoidPtr(addr);
+    dev = c10::Device(c10::DeviceType::CUDA, (c10::DeviceIndex)i);
+    return c != nullptr;
+}
+
+// (q, k or None, frequencies, positions or None, interleaved, amplitude, transpose, q_out or None, k_out or None)
+PyObject *rotary(PyObject *const *a)
+{
+    const at::Tensor *q = tensor(a[0]), *k = a[1] == Py_None ? nullptr : tensor(a[1]), *f = tensor(a[2]);
+    const at::Tensor *pos = a[3] == Py_None ? nullptr : tensor(a[3]), *qo = a[7] == Py_None ? nullptr : tensor(a[7]),
+                     *ko = a[8] == Py_None ? nullptr : tensor(a[8]);
+    if (!q || !f || !q->is_cuda() || (a[1] != Py_None && !k) || (a[3] != Py_None && !pos) || (a[7] != Py_None && !qo) ||
+        (a[8] != Py_None && !ko) || !PyFloat_CheckExact(a[5]) || !PyBool_Check(a[4]) || !PyBool_Check(a[6]))
+        return none();
+    const c10::Device dev = q->device();
+    const at::ScalarType type = q->scalar_type();
+    int kv;
+    View vq, vk = {}, vqo, vko = {};
+    if (!current(dev) || !kv_type(*q, kv) || !heads(q, type, dev, vq) || (k && !heads(k, type, dev, vk))) return none();
+    const int64_t T = q->size(0), Hq = q->size(1), D = q->size(2), Hkv = k ? k->size(1) : 0;
+    if ((k && (k->size(0) != T || k->size(2) != D)) || f->scalar_type() != at::kDouble || f->device() != dev || f->dim() != 1 ||
+        !f->is_contiguous() || 2 * f->size(0) > D)
+        return none();
+    if (pos && (pos->scalar_type() != at::kLong || pos->device() != dev || pos->dim() != 1 || pos->size(0) != T || !pos->is_contiguous()))
+        return none();
+    const at::Tensor oq = qo ? *qo : empty(q->sizes(), type, dev), ok = !k ? at::Tensor() : ko ? *ko : empty(k->sizes(), type, dev);
+    if (oq.sizes() != q->sizes() || !heads(&oq, type, dev, vqo) || (k && (ok.sizes() != k->sizes() || !heads(&ok, type, dev, vko))))
+        return none();
+    Call c;
+    if (!c.ready(dev, 0)) return nullptr;
+    if (api.rotary(vq.p, vq.s0, vq.s1, vk.p, vk.s0, vk.s1, kv, pos ? (const int64_t *)pos->data_ptr() : nullptr,
+                   (const double *)f->data_ptr(), PyFloat_AS_DOUBLE(a[5]), a[4] == Py_True, a[6] == Py_True, vqo.p, vqo.s0, vqo.s1,
+                   vko.p, vko.s0, vko.s1, T, Hq, Hkv, D, 2 * f->size(0), c.stream) != CFP32_OK)
+        return none();
+    PyObject *r = PyTuple_New(2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(oq));
+    PyTuple_SET_ITEM(r, 1, k ? THPVariable_Wrap(ok) : (Py_INCREF(Py_None), Py_None));
+    return r;
+}
+
+// (k, v, cu, cache, device index, table, lens)
+PyObject *append8(PyObject *const *a)
+{
+    const at::Tensor *k = tensor(a[0]), *v = tensor(a[1]), *cu = tensor(a[2]), *table = tensor(a[5]), *lens = tensor(a[6]);
+    c10::Device dev(c10::DeviceType::CPU);
+    const cfp32_cache8 *cache;
+    if (!k || !v || !cu || !table || !lens || !cache8(a[3], a[4], dev, cache)) return none();
+    View vk, vv;
+    int32_t *pt, *pl, *pc;
+    if (!current(dev) || !heads(k, at::kFloat, dev, vk) || !heads(v, at::kFloat, dev, vv) || !ints(table, dev, 2, pt) ||
+        !ints(lens, dev, 1, pl) || !ints(cu, dev, 1, pc))
+        return none();
+    const int64_t S = table->size(0), W = table->size(1);
+    if (k->sizes() != v->sizes() || k->size(1) != cache->Hkv || k->size(2) != cache->D || lens->size(0) != S || cu->size(0) != S + 1)
+        return none();
+    const at::Tensor lo = empty({S}, at::kInt, dev);
+    Call c;
+    if (!c.ready(dev, 0)) return nullptr;
+    if (api.append8((const float *)vk.p, vk.s0, vk.s1, (const float *)vv.p, vv.s0, vv.s1, pc, pl, (int32_t *)lo.data_ptr(), cache, pt,
+                    ld(*table), S, W, k->size(0), c.stream) != CFP32_OK)
+        return none();
+    return THPVariable_Wrap(lo);
+}
+
+// (cache, device index, table, cu, tokens, first or None, half)
+PyObject *read8(PyObject *const *a)
+{
+    const at::Tensor *table = tensor(a[2]), *cu = tensor(a[3]), *first = a[5] == Py_None ? nullptr : tensor(a[5]);
+    c10::Device dev(c10::DeviceType::CPU);
+    const cfp32_cache8 *cache;
+    int64_t T;
+    if (!table || !cu || (a[5] != Py_None && !first) || !cache8(a[0], a[1], dev, cache) || !whole(a[4], T) || T < 0 || !PyBool_Check(a[6]))
+        return none();
+    int32_t *pt, *pc, *pf = nullptr;
+    if (!current(dev) || !ints(table, dev, 2, pt) || !ints(cu, dev, 1, pc) || (first && !ints(first, dev, 1, pf))) return none();
+    const int64_t S = table->size(0), W = table->size(1);
+    if (cu->size(0) != S + 1 || (first && first->size(0) != S)) return none();
+    const bool half = a[6] == Py_True;
+    const at::Tensor k = empty({T, cache->Hkv, cache->D}, half ? at::kHalf : at::kFloat, dev), v = at::empty_like(k);
+    Call c;
+    if (!c.ready(dev, 0)) return nullptr;
+    if (api.read8(cache, pt, ld(*table), pf, pc, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+                  half ? CFP32_KV_F16 : CFP32_KV_F32, S, W, T, c.stream) != CFP32_OK)
+        return none();
+    return tuple_of({k, v});
+}
+
+// (q, cache, device index, table, lens, scale or None, out or None)
+PyObject *decode8(PyObject *const *a)
+{
+    const at::Tensor *q = tensor(a[0]), *table = tensor(a[3]), *lens = tensor(a[4]), *out = a[6] == Py_None ? nullptr : tensor(a[6]);
+    c10::Device dev(c10::DeviceType::CPU);
+    const cfp32_cache8 *cache;
+    if (!q || !table || !lens || (a[6] != Py_None && !out) || !cache8(a[1], a[2], dev, cache)) return none();
+    View vq, vo;
+    int32_t *pt, *pl;
+    double scale;
+    if (!current(dev) || !heads(q, at::kFloat, dev, vq) || !ints(table, dev, 2, pt) || !ints(lens, dev, 1, pl)) return none();
+    const int64_t B = q->size(0), Hq = q->size(1), D = q->size(2), W = table->size(1);
+    if (D == 0 || D != cache->D || cache->Hkv == 0 || Hq % cache->Hkv || table->size(0) != B || lens->size(0) != B ||
+        !scale_of(a[5], D, scale))
+        return none();
+    const at::Tensor o = out ? *out : empty(q->sizes(), at::kFloat, dev);
+    if (o.sizes() != q->sizes() || !heads(&o, at::kFloat, dev, vo)) return none();
+    Call c;
+    const size_t need = api.decode8_ws(B, Hq, cache->Hkv, D, W, cache->page);
+    if (!c.ready(dev, need)) return nullptr;
+    if (api.decode8((const float *)vq.p, vq.s0, vq.s1, cache, pt, ld(*table), W, pl, (float *)vo.p, vo.s0, vo.s1, B, Hq, scale, c.ws,
+                    need, c.stream) != CFP32_OK)
+        return none();
+    return THPVariable_Wrap(o);
+}
+
+// (logits, scores, n or None, done or None, eos)
+PyObject *select(PyObject *const *a)
+{
+    const at::Tensor *x = tensor(a[0]), *scores = tensor(a[1]), *done = a[3] == Py_None ? nullptr : tensor(a[3]);
+    int64_t n = 0, eos;
+    if (!x || !scores || !x->is_cuda() || (a[3] != Py_None && !done) || (a[2] != Py_None && !whole(a[2], n)) || !whole(a[4], eos))
+        return none();
+    const c10::Device dev = x->device();
+    if (!current(dev) || x->scalar_type() != at::kFloat || x->dim() != 2 || (x->size(1) > 1 && x->stride(1) != 1) ||
+        scores->scalar_type() != at::kFloat || scores->device() != dev || scores->dim() != 2 || !scores->is_contiguous() ||
+        scores->numel() != x->size(0))
+        return none();
+    if (done && ((done->scalar_type() != at::kBool && done->scalar_type() != at::kByte) || done->device() != dev ||
+                 done->sizes() != scores->sizes() || !done->is_contiguous()))
+        return none();
+    const int64_t S = scores->size(0), beams = scores->size(1), V = x->size(1);
+    if (a[2] == Py_None) n = beams;
+    if (n < 1 || n > 64) return none();
+    const at::Tensor parents = empty({S, n}, at::kInt, dev), tokens = empty({S, n}, at::kInt, dev),
+                     out = empty({S, n}, at::kFloat, dev), ended = empty({S, n}, at::kBool, dev);
+    Call c;
+    const size_t need = api.select_ws(S, beams, V, n);
+    if (!c.ready(dev, need)) return nullptr;
+    if (api.select((const float *)x->data_ptr(), ld(*x), (const float *)scores->data_ptr(), done ? (const uint8_t *)done->data_ptr() : nullptr,
+                   S, beams, V, n, eos, (int32_t *)parents.data_ptr(), (int32_t *)tokens.data_ptr(), (float *)out.data_ptr(),
+                   (uint8_t *)ended.data_ptr(), c.ws, need, c.stream) != CFP32_OK)
+        return none();
+    return tuple_of({parents, tokens, out, ended});
+}
+
+// (states, parents): contiguous states
+PyObject *reorder(PyObject *const *a)
+{
+    const at::Tensor *x = tensor(a[0]), *parents = tensor(a[1]);
+    if (!x || !parents || !x->is_cuda()) return none();
+    const c10::Device dev = x->device();
+    if (!current(dev) || x->dim() < 1 || !x->is_contiguous() || parents->scalar_type() != at::kInt || parents->device() != dev ||
+        !parents->is_contiguous())
+        return none();
+    const int64_t rows = x->size(0), n = parents->numel();
+    at::DimVector size(x->sizes().begin(), x->sizes().end());
+    size[0] = n;
+    const at::Tensor out = empty(size, x->scalar_type(), dev);
+    int64_t row = (int64_t)x->element_size();
+    for (size_t i = 1; i < size.size(); ++i) row *= size[i];
+    Call c;
+    if (!c.ready(dev, 0)) return nullptr;
+    if (api.reorder(x->data_ptr(), row, out.data_ptr(), row, (const int32_t *)parents->data_ptr(), rows, n, row, c.stream) != CFP32_OK)
+        return none();
+    return THPVariable_Wrap(out);
+}
+
 // (entry points' addresses in Api's order, raw_stream, scratch)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
@@ -369,6 +564,12 @@ CFP32_HELPER(append, append, 7)
 CFP32_HELPER(fork, fork, 6)
 CFP32_HELPER(free, free_pages, 2)
 CFP32_HELPER(compact, compact, 4)
+CFP32_HELPER(rotary, rotary, 9)
+CFP32_HELPER(append8, append8, 7)
+CFP32_HELPER(read8, read8, 7)
+CFP32_HELPER(decode8, decode8, 7)
+CFP32_HELPER(select, select, 5)
+CFP32_HELPER(reorder, reorder, 2)
 #undef CFP32_HELPER
 
 #define CFP32_METHOD(NAME, FUNC) {NAME, (PyCFunction)(void (*)(void))FUNC, METH_FASTCALL, nullptr}
@@ -380,6 +581,12 @@ PyMethodDef methods[] = {CFP32_METHOD("bind", bind),
                          CFP32_METHOD("cache_fork", fork_call),
                          CFP32_METHOD("cache_free", free_call),
                          CFP32_METHOD("cache_compact", compact_call),
+                         CFP32_METHOD("rotary", rotary_call),
+                         CFP32_METHOD("cache8_append", append8_call),
+                         CFP32_METHOD("cache8_read", read8_call),
+                         CFP32_METHOD("attention8_decode", decode8_call),
+                         CFP32_METHOD("beam_select", select_call),
+                         CFP32_METHOD("beam_reorder", reorder_call),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_helpers", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -672,9 +672,9 @@ CFP32_API size_t cfp32_beam_select_workspace_bytes(int64_t S, int64_t beams, int
  *   eos    : the token that finishes a beam (negative: none does).
  *   parents, tokens : int32 [S, n];  scores_out : FP32 [S, n];
  *   done_out : uint8 [S, n] (0 or 1) or NULL.
- * Beam b offers token t with scores[b] + x_t - log sum exp(x) (the sum's
- * terms FP32, off by some 2^-22, FP64 from there on; rounded once, at the end).  A finished beam offers itself alone, with its score and the token eos.
- * Offers are taken in order of their scores, of equal ones the lowest beam's
+ * Beam b offers token t with scores[b] + x_t - log sum exp(x) (the sum's terms
+ * FP32, off by some 2^-22, FP64 from there on; rounded once, at the end).  A
+ * finished beam offers itself alone, with its score and the token eos.  Offers are taken in order of their scores, of equal ones the lowest beam's
  * and of a beam's equal logits the lowest token first; a beam's are in the order
  * of its logits.  A token whose logit is -infinity is not offered, nor is
  * anything of a beam whose score is not finite, or of one whose logits hold a
