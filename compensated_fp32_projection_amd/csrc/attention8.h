@@ -24,6 +24,7 @@ struct Decode8Args {
 struct Decode8Plan {
     hipError_t error;
     int align;       // bytes that divide every address and the head size: 16, 8 or 1
+    bool fast;       // see Tile8
     int groups;      // of 16 query heads to a K/V head
     int parts;       // of a sequence's keys
     int64_t blocks;  // of each K/V head

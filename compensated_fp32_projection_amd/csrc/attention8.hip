@@ -19,6 +19,7 @@
 #include "attention8.h"
 #include "attention_join.h"
 #include "attention_rows.h"
+#include "lanes.h"
 
 namespace cfp32 {
 
@@ -29,8 +30,8 @@ typedef short short2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
 
-// Bytes I of `a` and J of `b` as FP16: integers, or floats times 2^-8.  The
-// bytes of integers have their signs turned (see turned).
+// Bytes I of `a` and J of `b` as FP16: integers, or floats times 2^-8.  An
+// integer c goes, as c + 128, into the last bits of 1024, which leaves 1152 + c.
 template <bool E4M3, int I, int J>
 __device__ __forceinline__ half2_t two_codes(uint32_t a, uint32_t b)
 {
@@ -39,21 +40,32 @@ __device__ __forceinline__ half2_t two_codes(uint32_t a, uint32_t b)
         const uint32_t y = __builtin_bit_cast(uint32_t, (short2_t)(__builtin_bit_cast(short2_t, x) >> 1)) & 0xBF80BF80u;
         return __builtin_bit_cast(half2_t, y);
     } else {
-        const uint32_t x = __builtin_amdgcn_perm(b, a, 0x0C000C00 | (uint32_t)I | (uint32_t)(4 + J) << 16) | 0x64006400u;
+        const uint32_t x = __builtin_amdgcn_perm(b, a, 0x0C000C00 | (uint32_t)I | (uint32_t)(4 + J) << 16) ^ 0x64806480u;
         return __builtin_bit_cast(half2_t, x) - (half2_t)(_Float16)1152;
     }
 }
 
+// Four codes of a key, one after the other.
 template <bool E4M3>
-__device__ __forceinline__ uint32_t turned(uint32_t w) { return E4M3 ? w : w ^ 0x80808080u; }
-
-// Eight codes of a key, one after the other.
-template <bool E4M3>
-__device__ __forceinline__ half8_t eight_codes(uint2_t w)
+__device__ __forceinline__ void four_codes(uint32_t w, half2_t &x, half2_t &y)
 {
-    const uint32_t a = turned<E4M3>(w[0]), b = turned<E4M3>(w[1]);
-    const half2_t p[4] = {two_codes<E4M3, 0, 1>(a, a), two_codes<E4M3, 2, 3>(a, a), two_codes<E4M3, 0, 1>(b, b),
-                          two_codes<E4M3, 2, 3>(b, b)};
+    if constexpr (E4M3) {
+        x = two_codes<true, 0, 1>(w, w);
+        y = two_codes<true, 2, 3>(w, w);
+    } else {  // the exponent's byte from the permutation, too
+        const uint32_t u = w ^ 0x80808080u;
+        x = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - (half2_t)(_Float16)1152;
+        y = __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - (half2_t)(_Float16)1152;
+    }
+}
+
+// Eight codes of a key.
+template <bool E4M3>
+__device__ __forceinline__ half8_t eight_codes(uint32_t a, uint32_t b)
+{
+    half2_t p[4];
+    four_codes<E4M3>(a, p[0], p[1]);
+    four_codes<E4M3>(b, p[2], p[3]);
     half8_t h;
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = p[e / 2][e % 2];
@@ -74,7 +86,8 @@ __device__ __forceinline__ half8_t column(const uint32_t (&w)[8])
 }
 
 // Where a sequence's keys are.  A page id outside the pool is replaced by page 0
-// (the pool has pages) and remembered: rows that see it become NaN.
+// (the pool has pages) and remembered: rows that see it become NaN.  What is
+// the same for a block's lanes (the sequence, its pages) is in scalar registers.
 struct Keys8 {
     const char *k, *v;       // the head in page 0
     const float *ks, *vs;
@@ -88,8 +101,6 @@ struct Keys8 {
         bad = min(bad, j >> lg << lg);
         return 0;
     }
-    // The page of 16 keys from a multiple of 16 on, where pages hold as many.
-    __device__ __forceinline__ int page_step(int j) { return lg >= 4 ? page_of(j) : 0; }
     __device__ __forceinline__ int page(int j, int p) { return lg >= 4 ? p : page_of(j); }
     __device__ __forceinline__ int inside(int j) const { return j & ((1 << lg) - 1); }
     __device__ __forceinline__ const char *key(int j, int p) { return k + page(j, p) * k_page + inside(j) * k_tok; }
@@ -125,13 +136,25 @@ __device__ __forceinline__ void load_codes(const char *p, int at, int n, uint32_
     }
 }
 
+// The codes and scales of a step's keys that a lane takes.  FAST: pages of 16
+// tokens or more and blocks of 4 or more, so that 16 keys have one page and the
+// four keys of a lane's scores one scale; and offsets within 16 tokens fit 31
+// bits, so that addresses are a scalar and a lane's offset that never changes.
+template <int DP, bool FAST>
+struct Tile8 {
+    static constexpr int NB = row_step<DP>() / 16, KL = DP / 64, NV = DP / 16;
+    uint32_t k[NB][KL][4], v[NB][4][NV / 4];
+    float ks[NB][FAST ? 1 : 4], vs[NB][FAST ? 1 : 4];
+};
+
 // One wave's share: keys [kb, hi), NW steps further each time, all of which
 // this lane's row q sees.
-template <bool E4M3, int DP, int A, int NW>
+template <bool E4M3, int DP, int A, bool FAST, int NW>
 __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D, float scale, int kb, int hi, Keys8 keys,
                                               const Joined<DP, NW> &to)
 {
-    constexpr int kStep = row_step<DP>(), NB = kStep / 16, KL = DP / 64, NV = DP / 16;
+    using Tile = Tile8<DP, FAST>;
+    constexpr int kStep = row_step<DP>(), NB = Tile::NB, KL = Tile::KL, NV = Tile::NV;
     constexpr float kCode = E4M3 ? 256.0f : 1.0f;  // of a value's FP16 form
     const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -149,48 +172,102 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
             if (q_wide) load_floats<16, true>(q, 64 * i + 16 * quad, D, x[i]);
             else load_floats<16, false>(q, 64 * i + 16 * quad, D, x[i]);
         }
-        uint32_t kr[NB][KL][4], vr[NB][4][NV / 4];
-        float ks[NB][4], vs[NB][4];
-        int page[NB], next[NB];
         const int last = hi - 1;
-        auto pages = [&](int b0, int (&p)[NB]) {
+        int page[NB], next[NB];
+        auto ask = [&](int b0) {  // for the pages of a step
 #pragma unroll
-            for (int b = 0; b < NB; ++b) p[b] = keys.page_step(min(b0 + 16 * b, last));
+            for (int b = 0; b < NB; ++b) next[b] = FAST || keys.lg >= 4 ? keys.row[min(b0 + 16 * b, last) >> keys.lg] : 0;
         };
-        auto load_k = [&](int b0) {
+        auto take = [&](int b0) {  // ... which have come
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const char *p = keys.key(min(b0 + 16 * b + col, last), page[b]);
-#pragma unroll
-                for (int i = 0; i < KL; ++i) load_codes<16, A>(p, 64 * i + 16 * quad, D, kr[b][i]);
-                const int j = b0 + 16 * b + 4 * quad;
-                if (keys.blg >= 2) {
-                    ks[b][0] = ks[b][1] = ks[b][2] = ks[b][3] = keys.k_scale(min(j, last), page[b]);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) ks[b][r] = keys.k_scale(min(j + r, last), page[b]);
+                page[b] = __builtin_amdgcn_readfirstlane(next[b]);
+                if (page[b] < 0 || page[b] >= keys.P) {
+                    const int j = min(b0 + 16 * b, last);
+                    keys.bad = min(keys.bad, j >> keys.lg << keys.lg);
+                    page[b] = 0;
                 }
             }
         };
-        auto load_v = [&](int b0) {
+        uint32_t k_off = 0, v_off[4] = {};
+        if constexpr (FAST) {
+            k_off = (uint32_t)col * (uint32_t)keys.k_tok + 16 * quad;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int j = b0 + 16 * b + 4 * quad;
+            for (int r = 0; r < 4; ++r) v_off[r] = (uint32_t)(4 * quad + r) * (uint32_t)keys.v_tok + (col * NV < D ? col * NV : 0);
+        }
+        auto load = [&](int b0, Tile &t) {
+            if constexpr (FAST) {
+                const bool all = b0 + kStep <= hi;
+                const char *kp[NB], *vp[NB];
+                int room[NB], in[NB], pg[NB];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    load_codes<NV, A>(keys.value(min(j + r, last), page[b]), col * NV, D, vr[b][r]);
-                if (keys.blg >= 2) {
-                    vs[b][0] = vs[b][1] = vs[b][2] = vs[b][3] = keys.v_scale(min(j, last), page[b]);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) vs[b][r] = keys.v_scale(min(j + r, last), page[b]);
+                for (int b = 0; b < NB; ++b) {
+                    // Keys beyond the last: the last's place, or the first sixteen's.
+                    const bool some = b0 + 16 * b <= last;
+                    const int j = some ? b0 + 16 * b : b0;
+                    pg[b] = some ? page[b] : page[0];
+                    in[b] = keys.inside(j);
+                    room[b] = last - j;
+                    kp[b] = keys.k + pg[b] * keys.k_page + in[b] * keys.k_tok;
+                    vp[b] = keys.v + pg[b] * keys.v_page + in[b] * keys.v_tok;
                 }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t off = all ? k_off : (uint32_t)min(col, room[b]) * (uint32_t)keys.k_tok + 16 * quad;
+#pragma unroll
+                    for (int i = 0; i < KL; ++i) {
+                        // Dims beyond D: the row's first (q is 0 there).
+                        const uint32_t back = 64 * i + 16 * quad < D ? 0u : (uint32_t)(64 * i + 16 * quad);
+                        if constexpr (A == 16) {
+                            const uint4_t w = *reinterpret_cast<const uint4_t *>(kp[b] + (off + 64 * i - back));
+                            t.k[b][i][0] = w[0], t.k[b][i][1] = w[1], t.k[b][i][2] = w[2], t.k[b][i][3] = w[3];
+                        } else {
+                            const uint32_t more = 64 * i + 16 * quad + 8 < D ? 8u : 0u;
+                            const uint2_t w = *reinterpret_cast<const uint2_t *>(kp[b] + (off + 64 * i - back));
+                            const uint2_t u = *reinterpret_cast<const uint2_t *>(kp[b] + (off + 64 * i - back + more));
+                            t.k[b][i][0] = w[0], t.k[b][i][1] = w[1], t.k[b][i][2] = u[0], t.k[b][i][3] = u[1];
+                        }
+                    }
+                    t.ks[b][0] = (keys.ks + pg[b] * keys.ks_page)[(uint32_t)(in[b] + 4 * quad) >> keys.blg];
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t off = all ? v_off[r]
+                                                 : (uint32_t)min(4 * quad + r, room[b]) * (uint32_t)keys.v_tok + (col * NV < D ? col * NV : 0);
+                        typedef uint32_t vec __attribute__((ext_vector_type(NV / 4)));
+                        const vec w = *reinterpret_cast<const vec *>(vp[b] + off);
+#pragma unroll
+                        for (int i = 0; i < NV / 4; ++i) t.v[b][r][i] = w[i];
+                    }
+                    t.vs[b][0] = (keys.vs + pg[b] * keys.vs_page)[(uint32_t)(in[b] + 4 * quad) >> keys.blg];
+                }
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const char *p = keys.key(min(b0 + 16 * b + col, last), page[b]);
+#pragma unroll
+                    for (int i = 0; i < KL; ++i) load_codes<16, A>(p, 64 * i + 16 * quad, D, t.k[b][i]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) t.ks[b][r] = keys.k_scale(min(b0 + 16 * b + 4 * quad + r, last), page[b]);
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = min(b0 + 16 * b + 4 * quad + r, last);
+                        load_codes<NV, A>(keys.value(j, page[b]), col * NV, D, t.v[b][r]);
+                        t.vs[b][r] = keys.v_scale(j, page[b]);
+                    }
             }
         };
-        pages(kb, page);
-        load_k(kb);
-        load_v(kb);
-        pages(kb + NW * kStep, next);
+
+        Tile tiles[2];
+        ask(kb);
+        take(kb);
+        if (kb + NW * kStep < hi) ask(kb + NW * kStep);
+        load(kb, tiles[0]);
 
         half8_t qh[2 * KL], ql[2 * KL];
         float mx = 0.0f;
@@ -201,8 +278,7 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                 const float ax = fabsf(x[i][e]);
                 mx = fmaxf(mx, ax < INFINITY ? ax : 0.0f);
             }
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx = max_of_quads(mx);
         const int e2 = top_shift(mx);
 #pragma unroll
         for (int i = 0; i < KL; ++i)
@@ -214,39 +290,33 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
             }
         const float f = __builtin_amdgcn_ldexpf(scale * kLog2e * kCode, -e2);
 
-        for (; kb < hi;) {
+        // A step's work on one tile, while the next one's is on its way into the other.
+        auto step = [&](Tile &t, Tile &ahead) {
+            const int nb = kb + NW * kStep;
+            if (nb < hi) {
+                take(nb);
+                if (nb + NW * kStep < hi) ask(nb + NW * kStep);
+                load(nb, ahead);
+            }
+            const int room = hi - kb - 4 * quad;  // of this lane's keys 16 b + r
             floatx4_t s[NB];
+            float top = -INFINITY;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 s[b] = floatx4_t{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < 2 * KL; ++i) {
-                    const half8_t a = eight_codes<E4M3>(uint2_t{kr[b][i / 2][2 * (i % 2)], kr[b][i / 2][2 * (i % 2) + 1]});
+                    const half8_t a = eight_codes<E4M3>(t.k[b][i / 2][2 * (i % 2)], t.k[b][i / 2][2 * (i % 2) + 1]);
                     s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[i], s[b], 0, 0, 0);
                     s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[i], s[b], 0, 0, 0);
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const bool seen = kb + 16 * b + 4 * quad + r < hi;
-                    s[b][r] = seen ? s[b][r] * f * ks[b][r] : -INFINITY;
+                    s[b][r] = 16 * b + r < room ? s[b][r] * f * t.ks[b][FAST ? 0 : r] : -INFINITY;
+                    top = fmaxf(top, s[b][r]);
                 }
             }
-            const int nb = kb + NW * kStep;
-            const bool more = nb < hi;
-            if (more) {
-                // The next step's pages are known; ask for those after it first.
-#pragma unroll
-                for (int b = 0; b < NB; ++b) page[b] = next[b];
-                if (nb + NW * kStep < hi) pages(nb + NW * kStep, next);
-                load_k(nb);
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
+            top = max_of_quads(top);
             if (__any(top > m + kLazy)) {
                 const float mn = fmaxf(m, top);
                 const float c = mn == -INFINITY ? 1.0f : exp2_raw(m - mn);
@@ -264,52 +334,52 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                     const float p = exp2_raw(s[b][r] - base);
                     l += p;
                     // What lies beyond the last key is not multiplied: its scale may be anything.
-                    w[b][r] = kb + 16 * b + 4 * quad + r < hi ? p * vs[b][r] : 0.0f;
+                    w[b][r] = 16 * b + r < room ? p * t.vs[b][FAST ? 0 : r] : 0.0f;
                     most = fmaxf(most, fabsf(w[b][r]));
                 }
-            most = fmaxf(most, __shfl_xor(most, 16));
-            most = fmaxf(most, __shfl_xor(most, 32));
-            const int e = top_shift(most);
+            const int e = top_shift(max_of_quads(most));
             half8_t wh[NB / 2], wl[NB / 2];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    _Float16 h, t;
-                    split_scaled(w[b][r], e, h, t);
-                    wh[b / 2][b % 2 * 4 + r] = h, wl[b / 2][b % 2 * 4 + r] = t;
+                    _Float16 h, u;
+                    split_scaled(w[b][r], e, h, u);
+                    wh[b / 2][b % 2 * 4 + r] = h, wl[b / 2][b % 2 * 4 + r] = u;
                 }
-            floatx4_t add[NV];
+            const bool far = __any(e > 120 || e < -120);  // the power of two is beyond FP32's, the products may not be
+            const float g = __builtin_amdgcn_ldexpf(kCode, -e);
 #pragma unroll
-            for (int c = 0; c < NV; ++c) add[c] = floatx4_t{0, 0, 0, 0};
+            for (int i = 0; i < NV / 4; ++i) {
+                floatx4_t add[4];
 #pragma unroll
-            for (int u = 0; u < NB / 2; ++u)
+                for (int c = 0; c < 4; ++c) add[c] = floatx4_t{0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < NV / 4; ++i) {
+                for (int u = 0; u < NB / 2; ++u) {
                     uint32_t word[8];
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) word[t] = turned<E4M3>(vr[2 * u + t / 4][t % 4][i]);
+                    for (int n = 0; n < 8; ++n) word[n] = t.v[2 * u + n / 4][n % 4][i];
                     const half8_t a[4] = {column<E4M3, 0>(word), column<E4M3, 1>(word), column<E4M3, 2>(word), column<E4M3, 3>(word)};
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        add[4 * i + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t], wl[u], add[4 * i + t], 0, 0, 0);
-                        add[4 * i + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[t], wh[u], add[4 * i + t], 0, 0, 0);
-                    }
+                    for (int c = 0; c < 4; ++c) add[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[c], wl[u], add[c], 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) add[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[c], wh[u], add[c], 0, 0, 0);
                 }
-            if (__any(e > 120 || e < -120)) {  // the power of two is beyond FP32's, the products may not be
 #pragma unroll
-                for (int c = 0; c < NV; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) o[c][r] += __builtin_amdgcn_ldexpf(add[c][r] * kCode, -e);
-            } else {
-                const float g = __builtin_amdgcn_ldexpf(kCode, -e);
-#pragma unroll
-                for (int c = 0; c < NV; ++c)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[c][r] = fmaf(add[c][r], g, o[c][r]);
+                    for (int r = 0; r < 4; ++r) {
+                        if (far) o[4 * i + c][r] += __builtin_amdgcn_ldexpf(add[c][r] * kCode, -e);
+                        else o[4 * i + c][r] = fmaf(add[c][r], g, o[4 * i + c][r]);
+                    }
             }
-            if (more) load_v(nb);
             kb = nb;
+        };
+        for (;;) {
+            step(tiles[0], tiles[1]);
+            if (kb >= hi) break;
+            step(tiles[1], tiles[0]);
+            if (kb >= hi) break;
         }
         int bad = keys.bad;
         if (__any(bad != 0x7FFFFFFF)) {
@@ -317,8 +387,8 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
             for (int t = 32; t; t >>= 1) bad = min(bad, __shfl_xor(bad, t));
             if (hi > bad) l = NAN;
         }
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
+        l += from_lane<16>(l);
+        l += from_lane<32>(l);
     }
     // O^T: this lane's column, dims NV (4 quad + r) + c.
     CFP32_LDS float *sums = to.o[0];
@@ -339,7 +409,7 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
     }
 }
 
-template <bool E4M3, int DP, int A, int NW>
+template <bool E4M3, int DP, int A, bool FAST, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void decode8_kernel(Decode8Args a, Decode8Plan p)
 {
     __shared__ float sums[NW][kRows * (DP + 4)], maxima[NW * kRows], weights[NW * kRows];
@@ -354,7 +424,7 @@ __global__ __launch_bounds__(64 * NW, 2) void decode8_kernel(Decode8Args a, Deco
     const int kh = blockIdx.y, g = a.Hq / c.Hkv;
     const int part = blockIdx.x % p.parts, group = blockIdx.x / p.parts;
     const int b = group / p.groups, h0 = group % p.groups * kRows, live = min(kRows, g - h0);
-    const int n = min(max(a.lens[b], 0), a.W << c.page_log2);
+    const int n = __builtin_amdgcn_readfirstlane(min(max(a.lens[b], 0), a.W << c.page_log2));
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int lo, hi;
     part_range(0, n, part, p.parts, NW * row_step<DP>(), lo, hi);
@@ -362,7 +432,7 @@ __global__ __launch_bounds__(64 * NW, 2) void decode8_kernel(Decode8Args a, Deco
     const Keys8 keys = {(const char *)c.k.data + kh * c.k.head, (const char *)c.v.data + kh * c.v.head,
                         c.ks.data + kh * c.ks.head, c.vs.data + kh * c.vs.head, c.k.page, c.v.page, c.k.tok, c.v.tok,
                         c.ks.page, c.vs.page, a.table + b * a.ld_table, c.page_log2, c.block_log2, c.P, 0x7FFFFFFF};
-    attend_share8<E4M3, DP, A, NW>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, c.D), c.D, a.scale,
+    attend_share8<E4M3, DP, A, FAST, NW>(a.q + b * a.q_seq + h * a.q_head, rows_wide(a.q, a.q_seq | a.q_head, c.D), c.D, a.scale,
                                    lo + wave * row_step<DP>(), hi, keys, sh);
     __syncthreads();
     const int row = threadIdx.x >> 4, rh = kh * g + h0 + row;
@@ -404,9 +474,10 @@ hipError_t launch_attention8_decode(const Decode8Args &a, void *workspace, hipSt
     const dim3 grid((unsigned)p.blocks, (unsigned)a.c.Hkv);
 #define CFP32_DECODE8_ALIGN(E4M3, DP)                                                          \
     do {                                                                                       \
-        if (p.align == 16) decode8_kernel<E4M3, DP, 16, 4><<<grid, 256, 0, stream>>>(a, p);    \
-        else if (p.align == 8) decode8_kernel<E4M3, DP, 8, 4><<<grid, 256, 0, stream>>>(a, p); \
-        else decode8_kernel<E4M3, DP, 1, 4><<<grid, 256, 0, stream>>>(a, p);                   \
+        if (p.fast && p.align == 16) decode8_kernel<E4M3, DP, 16, true, 4><<<grid, 256, 0, stream>>>(a, p);    \
+        else if (p.fast) decode8_kernel<E4M3, DP, 8, true, 4><<<grid, 256, 0, stream>>>(a, p);                 \
+        else if (p.align >= 8) decode8_kernel<E4M3, DP, 8, false, 4><<<grid, 256, 0, stream>>>(a, p);          \
+        else decode8_kernel<E4M3, DP, 1, false, 4><<<grid, 256, 0, stream>>>(a, p);                            \
     } while (0)
     if (a.c.e4m3) {
         if (a.c.D <= 64) CFP32_DECODE8_ALIGN(true, 64);

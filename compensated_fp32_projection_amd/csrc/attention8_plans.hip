@@ -39,6 +39,7 @@ Decode8Plan plan_decode8(const Decode8Args &a, void *workspace)
     const int64_t m = 16 | c.D | (int64_t)((uintptr_t)c.k.data | (uintptr_t)c.v.data) | c.k.page | c.k.head | c.k.tok | c.v.page |
                       c.v.head | c.v.tok;
     p.align = m % 16 == 0 ? 16 : m % 8 == 0 ? 8 : 1;
+    p.fast = p.align >= 8 && c.page_log2 >= 4 && c.block_log2 >= 2 && c.k.tok < (int64_t)1 << 26 && c.v.tok < (int64_t)1 << 26;
     p.groups = (int)ceil_div(a.Hq / c.Hkv, kRows);
     p.parts = key_parts(a.B, a.Hq, c.Hkv, c.D, (int64_t)a.W << c.page_log2);
     p.blocks = (int64_t)a.B * p.groups * p.parts;
