@@ -189,60 +189,65 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                 }
             }
         };
-        uint32_t k_off = 0, v_off[4] = {};
-        if constexpr (FAST) {
-            k_off = (uint32_t)col * (uint32_t)keys.k_tok + 16 * quad;
+        // A lane's bytes of 16 keys: its key's of K, and of each of its four keys of V.  Dims beyond D: the row's first
+        // (where q is 0, or nothing is written).
+        uint32_t k_dim[KL], v_dim = col * NV < D ? col * NV : 0, k_off, v_off[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v_off[r] = (uint32_t)(4 * quad + r) * (uint32_t)keys.v_tok + (col * NV < D ? col * NV : 0);
-        }
+        for (int i = 0; i < KL; ++i) k_dim[i] = 64 * i + 16 * quad < D ? 64 * i + 16 * quad : 0;
+        k_off = (uint32_t)col * (uint32_t)keys.k_tok + k_dim[0];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v_off[r] = (uint32_t)(4 * quad + r) * (uint32_t)keys.v_tok + v_dim;
+        // ALL: every key of the step is there.  Of others, keys beyond the last are the last's place, or the first sixteen's.
+        auto load_fast = [&](int b0, Tile &t, auto all) {
+            constexpr bool ALL = decltype(all)::value;
+            int64_t pg[NB];
+            int in[NB], room[NB];
+            const char *kp[NB], *vp[NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const bool some = ALL || b0 + 16 * b <= last;
+                const int j = some ? b0 + 16 * b : b0;
+                pg[b] = some ? page[b] : page[0];
+                in[b] = keys.inside(j);
+                room[b] = last - j;
+                kp[b] = keys.k + pg[b] * keys.k_page + in[b] * keys.k_tok;
+                vp[b] = keys.v + pg[b] * keys.v_page + in[b] * keys.v_tok;
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t off = ALL ? k_off : (uint32_t)min(col, room[b]) * (uint32_t)keys.k_tok + k_dim[0];
+#pragma unroll
+                for (int i = 0; i < KL; ++i) {
+                    const uint32_t at = off + (k_dim[i] - k_dim[0]);
+                    if constexpr (A == 16) {
+                        const uint4_t w = __builtin_nontemporal_load(reinterpret_cast<const uint4_t *>(kp[b] + at));
+                        t.k[b][i][0] = w[0], t.k[b][i][1] = w[1], t.k[b][i][2] = w[2], t.k[b][i][3] = w[3];
+                    } else {
+                        const uint32_t more = 64 * i + 16 * quad + 8 < D ? 8u : 0u;
+                        const uint2_t w = *reinterpret_cast<const uint2_t *>(kp[b] + at);
+                        const uint2_t u = *reinterpret_cast<const uint2_t *>(kp[b] + (at + more));
+                        t.k[b][i][0] = w[0], t.k[b][i][1] = w[1], t.k[b][i][2] = u[0], t.k[b][i][3] = u[1];
+                    }
+                }
+                t.ks[b][0] = (keys.ks + pg[b] * keys.ks_page)[(uint32_t)(in[b] + 4 * quad) >> keys.blg];
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t off = ALL ? v_off[r] : (uint32_t)min(4 * quad + r, room[b]) * (uint32_t)keys.v_tok + v_dim;
+                    typedef uint32_t vec __attribute__((ext_vector_type(NV / 4)));
+                    const vec w = __builtin_nontemporal_load(reinterpret_cast<const vec *>(vp[b] + off));
+#pragma unroll
+                    for (int i = 0; i < NV / 4; ++i) t.v[b][r][i] = w[i];
+                }
+                t.vs[b][0] = (keys.vs + pg[b] * keys.vs_page)[(uint32_t)(in[b] + 4 * quad) >> keys.blg];
+            }
+        };
         auto load = [&](int b0, Tile &t) {
             if constexpr (FAST) {
-                const bool all = b0 + kStep <= hi;
-                const char *kp[NB], *vp[NB];
-                int room[NB], in[NB], pg[NB];
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    // Keys beyond the last: the last's place, or the first sixteen's.
-                    const bool some = b0 + 16 * b <= last;
-                    const int j = some ? b0 + 16 * b : b0;
-                    pg[b] = some ? page[b] : page[0];
-                    in[b] = keys.inside(j);
-                    room[b] = last - j;
-                    kp[b] = keys.k + pg[b] * keys.k_page + in[b] * keys.k_tok;
-                    vp[b] = keys.v + pg[b] * keys.v_page + in[b] * keys.v_tok;
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const uint32_t off = all ? k_off : (uint32_t)min(col, room[b]) * (uint32_t)keys.k_tok + 16 * quad;
-#pragma unroll
-                    for (int i = 0; i < KL; ++i) {
-                        // Dims beyond D: the row's first (q is 0 there).
-                        const uint32_t back = 64 * i + 16 * quad < D ? 0u : (uint32_t)(64 * i + 16 * quad);
-                        if constexpr (A == 16) {
-                            const uint4_t w = *reinterpret_cast<const uint4_t *>(kp[b] + (off + 64 * i - back));
-                            t.k[b][i][0] = w[0], t.k[b][i][1] = w[1], t.k[b][i][2] = w[2], t.k[b][i][3] = w[3];
-                        } else {
-                            const uint32_t more = 64 * i + 16 * quad + 8 < D ? 8u : 0u;
-                            const uint2_t w = *reinterpret_cast<const uint2_t *>(kp[b] + (off + 64 * i - back));
-                            const uint2_t u = *reinterpret_cast<const uint2_t *>(kp[b] + (off + 64 * i - back + more));
-                            t.k[b][i][0] = w[0], t.k[b][i][1] = w[1], t.k[b][i][2] = u[0], t.k[b][i][3] = u[1];
-                        }
-                    }
-                    t.ks[b][0] = (keys.ks + pg[b] * keys.ks_page)[(uint32_t)(in[b] + 4 * quad) >> keys.blg];
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint32_t off = all ? v_off[r]
-                                                 : (uint32_t)min(4 * quad + r, room[b]) * (uint32_t)keys.v_tok + (col * NV < D ? col * NV : 0);
-                        typedef uint32_t vec __attribute__((ext_vector_type(NV / 4)));
-                        const vec w = *reinterpret_cast<const vec *>(vp[b] + off);
-#pragma unroll
-                        for (int i = 0; i < NV / 4; ++i) t.v[b][r][i] = w[i];
-                    }
-                    t.vs[b][0] = (keys.vs + pg[b] * keys.vs_page)[(uint32_t)(in[b] + 4 * quad) >> keys.blg];
-                }
+                if (b0 + kStep <= hi) load_fast(b0, t, std::integral_constant<bool, true>{});
+                else load_fast(b0, t, std::integral_constant<bool, false>{});
             } else {
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -274,10 +279,7 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
 #pragma unroll
         for (int i = 0; i < KL; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float ax = fabsf(x[i][e]);
-                mx = fmaxf(mx, ax < INFINITY ? ax : 0.0f);
-            }
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(x[i][e]));  // of a row with an infinity none is needed
         mx = max_of_quads(mx);
         const int e2 = top_shift(mx);
 #pragma unroll
@@ -298,24 +300,36 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                 if (nb + NW * kStep < hi) ask(nb + NW * kStep);
                 load(nb, ahead);
             }
+            const bool ends = kb + kStep > hi;
             const int room = hi - kb - 4 * quad;  // of this lane's keys 16 b + r
             floatx4_t s[NB];
             float top = -INFINITY;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                s[b] = floatx4_t{0, 0, 0, 0};
+            for (int b = 0; b < NB; ++b) s[b] = floatx4_t{0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 2 * KL; ++i) {
-                    const half8_t a = eight_codes<E4M3>(t.k[b][i / 2][2 * (i % 2)], t.k[b][i / 2][2 * (i % 2) + 1]);
-                    s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, ql[i], s[b], 0, 0, 0);
-                    s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, qh[i], s[b], 0, 0, 0);
-                }
+            for (int i = 0; i < 2 * KL; ++i) {
+                half8_t a[NB];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    s[b][r] = 16 * b + r < room ? s[b][r] * f * t.ks[b][FAST ? 0 : r] : -INFINITY;
-                    top = fmaxf(top, s[b][r]);
-                }
+                for (int b = 0; b < NB; ++b) a[b] = eight_codes<E4M3>(t.k[b][i / 2][2 * (i % 2)], t.k[b][i / 2][2 * (i % 2) + 1]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b], ql[i], s[b], 0, 0, 0);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b], qh[i], s[b], 0, 0, 0);
             }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[b][r] = s[b][r] * f * t.ks[b][FAST ? 0 : r];
+            if (ends) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[b][r] = 16 * b + r < room ? s[b][r] : -INFINITY;
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, s[b][r]);
             top = max_of_quads(top);
             if (__any(top > m + kLazy)) {
                 const float mn = fmaxf(m, top);
@@ -333,11 +347,20 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                 for (int r = 0; r < 4; ++r) {
                     const float p = exp2_raw(s[b][r] - base);
                     l += p;
-                    // What lies beyond the last key is not multiplied: its scale may be anything.
-                    w[b][r] = 16 * b + r < room ? p * t.vs[b][FAST ? 0 : r] : 0.0f;
-                    most = fmaxf(most, fabsf(w[b][r]));
+                    w[b][r] = p * t.vs[b][FAST ? 0 : r];
                 }
-            const int e = top_shift(max_of_quads(most));
+            if (ends) {  // what lies beyond the last key has a scale that may be anything
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) w[b][r] = 16 * b + r < room ? w[b][r] : 0.0f;
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(w[b][r]));
+            // Up to 2^-149 and back, both in FP32's range: no weight is too small to keep its bits.
+            const int e = min(top_shift(max_of_quads(most)), 149);
             half8_t wh[NB / 2], wl[NB / 2];
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -347,7 +370,6 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                     split_scaled(w[b][r], e, h, u);
                     wh[b / 2][b % 2 * 4 + r] = h, wl[b / 2][b % 2 * 4 + r] = u;
                 }
-            const bool far = __any(e > 120 || e < -120);  // the power of two is beyond FP32's, the products may not be
             const float g = __builtin_amdgcn_ldexpf(kCode, -e);
 #pragma unroll
             for (int i = 0; i < NV / 4; ++i) {
@@ -368,10 +390,7 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (far) o[4 * i + c][r] += __builtin_amdgcn_ldexpf(add[c][r] * kCode, -e);
-                        else o[4 * i + c][r] = fmaf(add[c][r], g, o[4 * i + c][r]);
-                    }
+                    for (int r = 0; r < 4; ++r) o[4 * i + c][r] = fmaf(add[c][r], g, o[4 * i + c][r]);
             }
             kb = nb;
         };
@@ -472,12 +491,13 @@ hipError_t launch_attention8_decode(const Decode8Args &a, void *workspace, hipSt
         return hipGetLastError();
     }
     const dim3 grid((unsigned)p.blocks, (unsigned)a.c.Hkv);
-#define CFP32_DECODE8_ALIGN(E4M3, DP)                                                          \
-    do {                                                                                       \
-        if (p.fast && p.align == 16) decode8_kernel<E4M3, DP, 16, true, 4><<<grid, 256, 0, stream>>>(a, p);    \
-        else if (p.fast) decode8_kernel<E4M3, DP, 8, true, 4><<<grid, 256, 0, stream>>>(a, p);                 \
-        else if (p.align >= 8) decode8_kernel<E4M3, DP, 8, false, 4><<<grid, 256, 0, stream>>>(a, p);          \
-        else decode8_kernel<E4M3, DP, 1, false, 4><<<grid, 256, 0, stream>>>(a, p);                            \
+#define CFP32_DECODE8(E4M3, DP, A, FAST) decode8_kernel<E4M3, DP, A, FAST, 4><<<grid, 256, 0, stream>>>(a, p)
+#define CFP32_DECODE8_ALIGN(E4M3, DP)                                     \
+    do {                                                                  \
+        if (p.fast && p.align == 16) CFP32_DECODE8(E4M3, DP, 16, true);   \
+        else if (p.fast) CFP32_DECODE8(E4M3, DP, 8, true);                \
+        else if (p.align >= 8) CFP32_DECODE8(E4M3, DP, 8, false);         \
+        else CFP32_DECODE8(E4M3, DP, 1, false);                           \
     } while (0)
     if (a.c.e4m3) {
         if (a.c.D <= 64) CFP32_DECODE8_ALIGN(true, 64);
@@ -487,6 +507,7 @@ hipError_t launch_attention8_decode(const Decode8Args &a, void *workspace, hipSt
         else CFP32_DECODE8_ALIGN(false, 128);
     }
 #undef CFP32_DECODE8_ALIGN
+#undef CFP32_DECODE8
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.to.o) return e;
     return launch_join(Decode8Rows{a.out, a.out_seq, a.out_head, a.Hq, a.c.D}, p.to, (int64_t)a.B * a.Hq, stream);

@@ -10,21 +10,27 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int padded(int64_t D) { return D <= 64 ? 64 : 128; }
 bool grid_ok(int64_t blocks, int threads) { return blocks <= 0x7FFFFFFF && blocks * threads <= 0xFFFFFFFF; }
 
-// Parts are made until the grid has kBlocks blocks, of a step of all waves each
-// (a little more than one makes no parts).
-constexpr int64_t kBlocks = 512;
+// Parts are made until the grid has kBlocks blocks, each of a step of all waves
+// (128 or 256 keys) or more: two to a compute unit, which is what its registers
+// hold (with 256 / 512 / 1024 blocks at the most 16 x 4000 x 32/8 x 128 INT8 takes
+// 34 / 35 / 40 us, 12 x 2000 x 12 x 64 E4M3 21 / 19 / 19, 64 x 8000 x 32/8 x 128
+// 182 / 181 / 188).  Of up to three steps none are made, since joining them is a
+// launch of its own: in one part and in several 300 keys x 16 x 32/8 x 128 take
+// 10.0 / 11.7 us, 500 x 12 x 12 x 64 8.4 / 11.0; of four 500 x 4 x 32/8 x 128 11.4 /
+// 10.2.  Blocks of eight waves were no faster (1 x 500 11.3 us against 9.6).
+constexpr int64_t kBlocks = 512, kOneBlock = 3;
 int key_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t keys)
 {
-    const int64_t unit = 4 * (D <= 64 ? 64 : 32), blocks = B * ceil_div(Hq / Hkv, kRows) * Hkv;
-    const int64_t most = 4 * keys <= 5 * unit ? 1 : ceil_div(keys, unit), want = kBlocks / blocks;
-    return (int)(want <= 1 || most <= 1 ? 1 : most < want ? most : want);
+    const int64_t unit = 4 * (D <= 64 ? 64 : 32), steps = ceil_div(keys, unit);
+    const int64_t want = kBlocks / (B * ceil_div(Hq / Hkv, kRows) * Hkv);
+    return (int)(want <= 1 || steps <= kOneBlock ? 1 : steps < want ? steps : want);
 }
 
 }  // namespace
 
 size_t attention8_decode_workspace(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t W, int page_log2)
 {
-    if (B == 0 || Hkv == 0) return 0;
+    if (B == 0 || Hq == 0 || Hkv == 0) return 0;
     const int parts = key_parts(B, Hq, Hkv, D, W << page_log2);
     return parts > 1 ? (size_t)(B * Hq * parts) * (padded(D) + 2) * 4 : 0;
 }
