@@ -12,6 +12,7 @@
 // bounds the first launch, latency the second.
 #include "beam.h"
 #include "device_common.h"
+#include "lanes.h"
 
 namespace cfp32 {
 
@@ -34,34 +35,58 @@ __device__ __forceinline__ float key_logit(uint64_t k)
 }
 __device__ __forceinline__ int key_token(uint64_t k) { return (int)~(uint32_t)k; }
 
-template <class V>
-__device__ __forceinline__ V exchange(V v, int j, bool keep_larger)
+// A wave's values, sorted by a bitonic network whose exchanges stay out of LDS
+// (they took a third of the join's time there).
+template <int J, class V>
+__device__ __forceinline__ V exchange(V v, bool keep_larger)
 {
-    const V o = __shfl_xor(v, j);
+    const V o = from_lane<J>(v);
     return (v > o) == keep_larger ? v : o;
 }
-
-// Bitonic: the wave's values in order, the largest in lane 0.
-template <class V>
-__device__ __forceinline__ V sort_wave(V v)
+template <int J, class V>
+__device__ __forceinline__ V merge_steps(V v, bool down)
 {
     const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j; j >>= 1) v = exchange(v, j, ((lane & j) == 0) == ((lane & k) == 0));
-    return v;
+    v = exchange<J>(v, ((lane & J) == 0) == down);
+    if constexpr (J > 1) return merge_steps<J / 2>(v, down);
+    else return v;
 }
+template <int K, class V>
+__device__ __forceinline__ V sort_steps(V v)
+{
+    if constexpr (K > 2) v = sort_steps<K / 2>(v);
+    return merge_steps<K / 2>(v, (threadIdx.x & K & 63) == 0);
+}
+
+// In order, the largest in lane 0.
+template <class V>
+__device__ __forceinline__ V sort_wave(V v) { return sort_steps<64>(v); }
 
 // The 64 largest of two wave's lists that are in order, in order.
 __device__ __forceinline__ uint64_t merge_wave(uint64_t a, uint64_t b)
 {
-    const int lane = threadIdx.x & 63;
     const uint64_t r = __shfl_xor(b, 63);
-    uint64_t v = a > r ? a : r;
-#pragma unroll
-    for (int j = 32; j; j >>= 1) v = exchange(v, j, (lane & j) == 0);
-    return v;
+    return merge_steps<32>(a > r ? a : r, true);
+}
+
+// A wave's sum, and its maximum.
+template <class V>
+__device__ __forceinline__ V wave_sum(V v)
+{
+    v += from_lane<1>(v);
+    v += from_lane<2>(v);
+    v += from_lane<4>(v);
+    v += from_lane<8>(v);
+    v += from_lane<16>(v);
+    return v + from_lane<32>(v);
+}
+__device__ __forceinline__ float wave_max(float v)
+{
+    v = fmaxf(v, from_lane<1>(v));
+    v = fmaxf(v, from_lane<2>(v));
+    v = fmaxf(v, from_lane<4>(v));
+    v = fmaxf(v, from_lane<8>(v));
+    return max_of_quads(v);
 }
 
 // The largest keys seen by a wave, in order, and those that wait to be sorted
@@ -134,8 +159,7 @@ __global__ __launch_bounds__(256) void beam_rows_kernel(BeamArgs a, int chunks, 
     float sum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((x[e] - most) * kLog2e);
-#pragma unroll
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+    sum = wave_sum(sum);
     // A NaN, or infinity less itself, leaves a sum of NaN; of nothing but -infinity (and no NaN) it is 0.
     if (most == -INFINITY) {
         float odd = 0.0f;
@@ -152,16 +176,28 @@ __global__ __launch_bounds__(256) void beam_rows_kernel(BeamArgs a, int chunks, 
     if (lane == 0) stats[unit] = make_float2(most, sum);
 }
 
-// A wave's sum of doubles.
-__device__ __forceinline__ double wave_sum(double v)
+// An offer of a beam: larger totals first, of equal ones the lower place (beam,
+// then the order of its logits).
+struct Offer {
+    double total;
+    uint32_t place;
+    __device__ __forceinline__ bool operator>(const Offer &o) const { return total > o.total || (total == o.total && place < o.place); }
+};
+template <int J>
+__device__ __forceinline__ Offer from_lane(Offer v) { return {cfp32::from_lane<J>(v.total), cfp32::from_lane<J>(v.place)}; }
+
+template <int J>
+__device__ __forceinline__ Offer best_offer(Offer v)
 {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+    const Offer o = from_lane<J>(v);
+    if (o > v) v = o;
+    if constexpr (J > 1) return best_offer<J / 2>(v);
+    else return v;
 }
 
 __global__ __launch_bounds__(1024) void beam_join_kernel(BeamArgs a, int chunks, const float2 *stats, const uint64_t *lists)
 {
+    constexpr int kKeys = 8;                          // of a lane at a time
     extern __shared__ double totals[];                // [beams][n]
     int *tokens = (int *)(totals + a.beams * a.n);    // [beams][n]
     __shared__ uint64_t waiting[16][128];
@@ -170,36 +206,49 @@ __global__ __launch_bounds__(1024) void beam_join_kernel(BeamArgs a, int chunks,
     for (int b = wave; b < a.beams; b += waves) {
         const int64_t row = s * a.beams + b;
         const float score = a.scores[row];
+        const bool done = a.done && a.done[row];
         double total = -INFINITY;
         int token = -1;
         if (!(fabsf(score) < INFINITY)) {
-        } else if (a.done && a.done[row]) {
+        } else if (done) {
             if (lane == 0) {
                 total = score;
                 token = a.eos;
             }
         } else {
+            // The n largest of the row's lists, as of its logits.
+            Best best = {0, waiting[wave], 0, false};
+            const uint64_t *keys = lists + row * chunks * a.n;
+            const int64_t count = (int64_t)chunks * a.n;
             const float2 *st = stats + row * chunks;
-            float most = -INFINITY;
-            for (int i = lane; i < chunks; i += 64) most = fmaxf(most, st[i].x);
+            const float2 first = lane < chunks ? st[lane] : make_float2(-INFINITY, 0.0f);
+            for (int64_t i0 = 0; i0 < count; i0 += 64 * kKeys) {
+                uint64_t k[kKeys], mine = 0;
 #pragma unroll
-            for (int o = 32; o; o >>= 1) most = fmaxf(most, __shfl_xor(most, o));
-            double sum = 0.0;
-            for (int i = lane; i < chunks; i += 64) {
+                for (int e = 0; e < kKeys; ++e) {
+                    const int64_t i = i0 + 64 * e + lane;
+                    k[e] = i < count ? keys[i] : 0;
+                }
+#pragma unroll
+                for (int e = 0; e < kKeys; ++e) mine = k[e] > mine ? k[e] : mine;
+                uint64_t least = __shfl(sort_wave(mine), a.n - 1);
+                if (best.any) {
+                    const uint64_t have = __shfl(best.top, a.n - 1);
+                    least = have > least ? have : least;
+                }
+#pragma unroll
+                for (int e = 0; e < kKeys; ++e) best.add(k[e] >= least && k[e], k[e]);
+                if (best.count) best.flush();
+            }
+            float most = first.x;
+            for (int i = lane + 64; i < chunks; i += 64) most = fmaxf(most, st[i].x);
+            most = wave_max(most);
+            double sum = first.y != 0.0f ? (double)first.y * exp((double)first.x - (double)most) : 0.0;
+            for (int i = lane + 64; i < chunks; i += 64) {
                 const float2 c = st[i];
                 if (c.y != 0.0f) sum += (double)c.y * exp((double)c.x - (double)most);
             }
             sum = wave_sum(sum);
-            Best best = {0, waiting[wave], 0, false};
-            const uint64_t *keys = lists + row * chunks * a.n;
-            const int64_t count = (int64_t)chunks * a.n;
-            for (int64_t i0 = 0; i0 < count; i0 += 64) {
-                const int64_t i = i0 + lane;
-                const uint64_t k = i < count ? keys[i] : 0;
-                const uint64_t least = best.any ? __shfl(best.top, a.n - 1) : 0;
-                best.add(k > least, k);
-            }
-            if (best.count) best.flush();
             if (sum > 0.0 && sum < INFINITY && lane < a.n && best.any && best.top) {
                 const double lse = (double)most + log(sum);
                 total = (double)score + ((double)key_logit(best.top) - lse);
@@ -213,28 +262,29 @@ __global__ __launch_bounds__(1024) void beam_join_kernel(BeamArgs a, int chunks,
     }
     __syncthreads();
     if (wave) return;
+    auto put = [&](int i, const Offer &o) {
+        const int64_t out = s * a.n + i;
+        const bool some = o.total > -INFINITY;
+        const int b = some ? (int)(o.place / (uint32_t)a.n) : 0, token = some ? tokens[o.place] : a.eos;
+        const int64_t row = s * a.beams + b;
+        a.parents[out] = some ? (int)row : -1;
+        a.tokens[out] = token;
+        a.scores_out[out] = (float)o.total;
+        if (a.done_out) a.done_out[out] = !some || (a.done && a.done[row]) || (a.eos >= 0 && token == a.eos);
+    };
+    const int count = a.beams * a.n;
+    if (count <= 64) {
+        const Offer o = sort_wave(Offer{lane < count ? totals[lane] : -INFINITY, (uint32_t)lane});
+        if (lane < a.n) put(lane, o);
+        return;
+    }
     // Lane b holds the best offer of beam b that is left.
     int at = 0;
     for (int i = 0; i < a.n; ++i) {
-        double v = lane < a.beams && at < a.n ? totals[lane * a.n + at] : -INFINITY;
-        int who = lane;
-#pragma unroll
-        for (int o = 32; o; o >>= 1) {
-            const double w = __shfl_xor(v, o);
-            const int x = __shfl_xor(who, o);
-            if (w > v || (w == v && x < who)) v = w, who = x;
-        }
-        const bool some = v > -INFINITY;
-        const int64_t out = s * a.n + i;
-        if (lane == who) {
-            const int token = some ? tokens[lane * a.n + at] : a.eos;
-            const bool was = some && a.done && a.done[s * a.beams + lane];
-            a.parents[out] = some ? (int)(s * a.beams) + lane : -1;
-            a.tokens[out] = token;
-            a.scores_out[out] = (float)v;
-            if (a.done_out) a.done_out[out] = !some || was || (a.eos >= 0 && token == a.eos);
-            ++at;
-        }
+        const uint32_t place = lane * a.n + at;
+        const Offer o = best_offer<32>(Offer{lane < a.beams && at < a.n ? totals[place] : -INFINITY, place});
+        if (lane == 0) put(i, o);
+        at += o.place == place;
     }
 }
 
