@@ -4,6 +4,7 @@
 #include "attention_device.h"
 #include "cache8.h"
 #include "codes8.h"
+#include "lanes.h"
 
 namespace cfp32 {
 
@@ -11,27 +12,33 @@ namespace {
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFF; }
 
-// One block of a sequence's tokens and one head of K or V at a time.  Sequence s
-// owns the units from cu[s] / block + 2 s on: one more than its new tokens make
-// of whole blocks, and one because they may begin inside a block.
+// One block of a sequence's tokens and one head of K or V: a unit.  Sequence s
+// owns the blocks from cu[s] / block + 2 s on: one more than its new tokens make
+// of whole blocks, and one because they may begin inside a block.  A unit is a
+// wave's (GROUP 64, four to a thread block), or a whole thread block's where it
+// has more values than a wave holds in registers between finding the largest
+// and writing: what a unit waits for (its sequence, its page, its values) then
+// has more units beside it to hide it (6001 tokens of 32 x 64 E4M3 21 -> 14.7 us).
 // FOUR: four values at a time (16-byte loads, 4-byte stores).
-template <bool E4M3, int NT, bool FOUR>
-__global__ __launch_bounds__(NT) void cache8_append_kernel(HeadsView k, HeadsView v, const int32_t *cu, const int32_t *lens,
-                                                           int32_t *lens_out, Cache8 c, const int32_t *table, int64_t ld, int S,
-                                                           int W, int T, int64_t units)
+template <bool E4M3, int GROUP, bool FOUR>
+__global__ __launch_bounds__(256) void cache8_append_kernel(HeadsView k, HeadsView v, const int32_t *cu, const int32_t *lens,
+                                                            int32_t *lens_out, Cache8 c, const int32_t *table, int64_t ld, int S,
+                                                            int W, int T, int64_t units)
 {
-    constexpr int kHeld = 8;  // values of a thread that stay in registers between the two passes, by four
-    __shared__ uint32_t largest[NT / 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t s = (int64_t)blockIdx.x * NT + threadIdx.x; s < S; s += (int64_t)gridDim.x * NT)
+    constexpr int kHeld = 8, E = FOUR ? 4 : 1;  // a thread's values that stay in registers, by E
+    __shared__ uint32_t largest[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int me = GROUP == 64 ? lane : threadIdx.x;
+    for (int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x; s < S; s += (int64_t)gridDim.x * 256)
         lens_out[s] = lens[s] + (cu[s + 1] - cu[s]);
     const int64_t total = units * c.Hkv * 2;
-    const int per = FOUR ? c.D / 4 : c.D;
+    const int per = c.D / E;
     auto start = [&](int s) { return (int64_t)(cu[s] >> c.block_log2) + 2 * (int64_t)s; };
-    for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
-        const int h = (int)(u % c.Hkv);
-        const bool second = (u / c.Hkv) & 1;
-        const int64_t id = u / c.Hkv >> 1;
+    const int64_t first = GROUP == 64 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x, step = GROUP == 64 ? (int64_t)gridDim.x * 4 : gridDim.x;
+    for (int64_t u = first; u < total; u += step) {
+        const int64_t uh = over(u, c.Hkv), id = uh >> 1;
+        const int h = (int)(u - uh * c.Hkv);
+        const bool second = uh & 1;
         const int s = find_last(S, id, start);
         const int64_t c0 = cu[s], j = id - start(s), len = lens[s];
         const int64_t n = min((int64_t)cu[s + 1], (int64_t)T) - c0;
@@ -55,39 +62,40 @@ __global__ __launch_bounds__(NT) void cache8_append_kernel(HeadsView k, HeadsVie
 
         const int items = m * per;
         uint32_t most = 0;
-        float held[kHeld][FOUR ? 4 : 1];
-        auto load = [&](int i, float (&y)[FOUR ? 4 : 1]) {
-            const int t = i / per, d = i - t * per;
-            const float *p = in + t * x.tok;
-            if constexpr (FOUR) {
-                const floatx4_t w = *reinterpret_cast<const floatx4_t *>(p + 4 * d);
+        float held[kHeld][E];
+        auto load = [&](int i, float (&y)[E]) {
+            const int t = (int)over(i, per), d = i - t * per;
+            typedef float vec __attribute__((ext_vector_type(E)));
+            const vec w = __builtin_nontemporal_load(reinterpret_cast<const vec *>(in + t * x.tok + E * d));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) y[q] = w[q];
-            } else {
-                y[0] = p[d];
-            }
+            for (int q = 0; q < E; ++q) y[q] = w[q];
+        };
+        auto look = [&](const float (&y)[E]) {
+#pragma unroll
+            for (int q = 0; q < E; ++q) most = max(most, magnitude(y[q]));
         };
 #pragma unroll
-        for (int r = 0; r < kHeld; ++r) {
-            const int i = threadIdx.x + r * NT;
-            if (i < items) {
-                load(i, held[r]);
+        for (int r = 0; r < kHeld; ++r)
+            if (me + r * GROUP < items) load(me + r * GROUP, held[r]);
 #pragma unroll
-                for (int q = 0; q < (FOUR ? 4 : 1); ++q) most = max(most, magnitude(held[r][q]));
-            }
-        }
-        for (int i = threadIdx.x + kHeld * NT; i < items; i += NT) {
-            float y[FOUR ? 4 : 1];
+        for (int r = 0; r < kHeld; ++r)
+            if (me + r * GROUP < items) look(held[r]);
+        for (int i = me + kHeld * GROUP; i < items; i += GROUP) {
+            float y[E];
             load(i, y);
-#pragma unroll
-            for (int q = 0; q < (FOUR ? 4 : 1); ++q) most = max(most, magnitude(y[q]));
+            look(y);
         }
-#pragma unroll
-        for (int o = 32; o; o >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o));
-        if (lane == 0) largest[wave] = most;
-        __syncthreads();  // every thread has read the block's scale, too
-#pragma unroll
-        for (int w = 0; w < NT / 64; ++w) most = max(most, largest[w]);
+        most = max(most, from_lane<1>(most));
+        most = max(most, from_lane<2>(most));
+        most = max(most, from_lane<4>(most));
+        most = max(most, from_lane<8>(most));
+        most = max(most, from_lane<16>(most));
+        most = max(most, from_lane<32>(most));
+        if constexpr (GROUP == 256) {
+            if (lane == 0) largest[wave] = most;
+            __syncthreads();  // every thread has read the block's scale, too
+            most = max(max(largest[0], largest[1]), max(largest[2], largest[3]));
+        }
 
         float sc = NAN;
         int up = 0;
@@ -99,31 +107,29 @@ __global__ __launch_bounds__(NT) void cache8_append_kernel(HeadsView k, HeadsVie
                 sc = __builtin_amdgcn_ldexpf(had, up);
             }
         }
-        if (threadIdx.x == 0) *scale = sc;
+        if (me == 0) *scale = sc;
         const bool known = sc == sc;
         const float inv = 1.0f / sc;
-        auto store = [&](int i, const float (&y)[FOUR ? 4 : 1]) {
-            const int t = i / per, d = i - t * per;
+        auto store = [&](int i, const float (&y)[E]) {
+            const int t = (int)over(i, per), d = i - t * per;
             uint8_t *p = base + (old + t) * pool.tok;
             float w[4] = {};
 #pragma unroll
-            for (int q = 0; q < (FOUR ? 4 : 1); ++q) w[q] = y[q];
+            for (int q = 0; q < E; ++q) w[q] = y[q];
             const uint32_t codes = known ? encode<E4M3>(w, sc, inv) : 0u;
             if constexpr (FOUR) *reinterpret_cast<uint32_t *>(p + 4 * d) = codes;
             else p[d] = (uint8_t)codes;
         };
 #pragma unroll
-        for (int r = 0; r < kHeld; ++r) {
-            const int i = threadIdx.x + r * NT;
-            if (i < items) store(i, held[r]);
-        }
-        for (int i = threadIdx.x + kHeld * NT; i < items; i += NT) {
-            float y[FOUR ? 4 : 1];
+        for (int r = 0; r < kHeld; ++r)
+            if (me + r * GROUP < items) store(me + r * GROUP, held[r]);
+        for (int i = me + kHeld * GROUP; i < items; i += GROUP) {
+            float y[E];
             load(i, y);
             store(i, y);
         }
         if (known && up) {
-            for (int i = threadIdx.x; i < old * per; i += NT) {
+            for (int i = me; i < old * per; i += GROUP) {
                 const int t = i / per, d = i - t * per;
                 uint8_t *p = base + t * pool.tok;
                 if constexpr (FOUR) {
@@ -134,18 +140,22 @@ __global__ __launch_bounds__(NT) void cache8_append_kernel(HeadsView k, HeadsVie
                 }
             }
         }
-        __syncthreads();  // largest has been read
+        if constexpr (GROUP == 256) __syncthreads();  // largest has been read
     }
 }
 
-// E codes of a token and head at a time; a block takes `tokens` rows.
+// A block takes `tokens` rows; a thread E codes of a head, the same for all of
+// its tokens, so that a wave's stores are whole lines (with 16 codes to a
+// thread, whose results lay 64 bytes apart, 8574 tokens of 8 x 128 to FP32 took
+// 27 us) and few threads have to find out where they are.
 template <bool E4M3, class Out, int E>
 __global__ __launch_bounds__(256) void cache8_read_kernel(Cache8 c, const int32_t *table, int64_t ld, const int32_t *first,
                                                           const int32_t *cu, HeadsOut k, HeadsOut v, int S, int W, int T,
                                                           int tokens)
 {
-    constexpr int kMost = 64;
+    constexpr int kMost = 64, kAtOnce = 4;
     __shared__ int pages[kMost], offs[kMost];  // page -1: none, -2: no row of a sequence
+    __shared__ int starts[64];                 // of the sequences from the first token's on
     const int per = c.D / E;
     const bool second = blockIdx.y;
     const PagesView &pool = second ? c.v : c.k;
@@ -153,65 +163,81 @@ __global__ __launch_bounds__(256) void cache8_read_kernel(Cache8 c, const int32_
     const HeadsOut &to = second ? v : k;
     for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < T; t0 += (int64_t)gridDim.x * tokens) {
         const int nt = (int)min((int64_t)tokens, T - t0);
-        if (threadIdx.x < nt) {
+        if (threadIdx.x < 64) {
+            const int s0 = find_last(S, t0, [&](int s) { return (int64_t)cu[s]; });
+            starts[threadIdx.x] = s0 + (int)threadIdx.x < S ? cu[s0 + threadIdx.x] : 0x7FFFFFFF;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             const int64_t t = t0 + threadIdx.x;
-            int lo = 0, hi = S;  // the largest s < S with cu[s] <= t
+            // The last sequence that begins at t or before: among these 64, or (many empty ones) beyond.
+            int lo = 0, hi = 64;
             while (hi - lo > 1) {
-                const int m = lo + (hi - lo) / 2;
-                if (cu[m] <= t) lo = m;
+                const int m = (lo + hi) / 2;
+                if (starts[m] <= t) lo = m;
                 else hi = m;
             }
+            lo += s0;
+            if (lo == s0 + 63) {
+                hi = S;
+                while (hi - lo > 1) {
+                    const int m = lo + (hi - lo) / 2;
+                    if (cu[m] <= t) lo = m;
+                    else hi = m;
+                }
+            }
             int page = -2, off = 0;
-            if (cu[lo] <= t && t < cu[lo + 1]) {
+            if ((int)threadIdx.x < nt && cu[lo] <= t && t < cu[lo + 1]) {
                 const int64_t pos = (first ? first[lo] : 0) + (t - cu[lo]), entry = pos >> c.page_log2;
                 off = (int)(pos & (((int64_t)1 << c.page_log2) - 1));
                 page = -1;
                 if (pos >= 0 && entry < W) page = table[lo * ld + entry];
                 if (page < 0 || page >= c.P) page = -1;
             }
-            pages[threadIdx.x] = page;
-            offs[threadIdx.x] = off;
+            if ((int)threadIdx.x < nt) {
+                pages[threadIdx.x] = page;
+                offs[threadIdx.x] = off;
+            }
         }
         __syncthreads();
-        const int n = nt * c.Hkv * per;
-        for (int i = threadIdx.x; i < n; i += 256) {
-            const int th = i / per, d = (i - th * per) * E, t = th / c.Hkv, h = th - t * c.Hkv;
-            const int page = pages[t], off = offs[t];
-            if (page == -2) continue;
-            float y[E];
-            if (page < 0) {
+        const int wide = c.Hkv * per, slots = wide < 256 ? 256 / wide : 1;  // threads of a token; tokens at a time
+        const int slot = wide < 256 ? (int)threadIdx.x / wide : 0;
+        for (int i = (int)threadIdx.x - slot * wide; i < wide && slot < slots; i += 256) {
+            const int h = i / per, d = (i - h * per) * E;
+            const uint8_t *from = (const uint8_t *)pool.data + h * pool.head + d;
+            const float *scales = sv.data + h * sv.head;
+            Out *out = (Out *)to.data + t0 * to.tok + h * to.head + d;
+            for (int u = slot; u < nt; u += slots * kAtOnce) {
+                typedef uint32_t vec __attribute__((ext_vector_type(E < 4 ? 1 : E / 4)));
+                vec w[kAtOnce];
+                float s[kAtOnce];
 #pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = NAN;
-            } else {
-                const float s = sv.data[page * sv.page + h * sv.head + (off >> c.block_log2)];
-                const uint8_t *p = (const uint8_t *)pool.data + page * pool.page + h * pool.head + off * pool.tok + d;
-                if constexpr (E == 1) {
-                    y[0] = code_value<E4M3, 0>(*p) * s;
-                } else {
-                    typedef uint32_t vec __attribute__((ext_vector_type(E / 4)));
-                    const vec w = *reinterpret_cast<const vec *>(p);
+                for (int g = 0; g < kAtOnce; ++g) {
+                    const int t = u + g * slots, page = t < nt ? pages[t] : -2, off = t < nt ? offs[t] : 0;
+                    s[g] = NAN;
+                    w[g] = (vec)0;
+                    if (page < 0) continue;
+                    s[g] = scales[page * sv.page + (off >> c.block_log2)];
+                    const uint8_t *p = from + page * pool.page + off * pool.tok;
+                    if constexpr (E == 1) w[g] = *p;
+                    else w[g] = *reinterpret_cast<const vec *>(p);
+                }
 #pragma unroll
-                    for (int e = 0; e < E; e += 4) {
-                        y[e] = code_value<E4M3, 0>(w[e / 4]) * s;
-                        y[e + 1] = code_value<E4M3, 1>(w[e / 4]) * s;
-                        y[e + 2] = code_value<E4M3, 2>(w[e / 4]) * s;
-                        y[e + 3] = code_value<E4M3, 3>(w[e / 4]) * s;
+                for (int g = 0; g < kAtOnce; ++g) {
+                    const int t = u + g * slots;
+                    if (t >= nt || pages[t] == -2) continue;
+                    typedef Out piece __attribute__((ext_vector_type(E)));
+                    piece y;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const uint32_t word = w[g][e / 4];
+                        const float code = e % 4 == 0 ? code_value<E4M3, 0>(word) : e % 4 == 1 ? code_value<E4M3, 1>(word)
+                                                      : e % 4 == 2 ? code_value<E4M3, 2>(word) : code_value<E4M3, 3>(word);
+                        float x = code * s[g];
+                        // Two roundings in every form: else some make one mixed-precision instruction of product and conversion.
+                        asm("" : "+v"(x));
+                        y[e] = (Out)x;
                     }
+                    *reinterpret_cast<piece *>(out + t * to.tok) = y;
                 }
-            }
-            Out *out = (Out *)to.data + (t0 + t) * to.tok + h * to.head + d;
-            constexpr int O = E * sizeof(Out) <= 16 ? E : 16 / sizeof(Out);
-            typedef Out piece __attribute__((ext_vector_type(O)));
-#pragma unroll
-            for (int e = 0; e < E; e += O) {
-                piece w;
-#pragma unroll
-                for (int q = 0; q < O; ++q) {
-                    // Two roundings in every form: else some make one mixed-precision instruction of product and conversion.
-                    asm("" : "+v"(y[e + q]));
-                    w[q] = (Out)y[e + q];
-                }
-                *reinterpret_cast<piece *>(out + e) = w;
             }
         }
         __syncthreads();  // pages have been read
@@ -228,18 +254,29 @@ hipError_t launch_cache8_append(const HeadsView &k, const HeadsView &v, const in
                        c.v.tok;
     const bool four = c.D % 4 == 0 && in % 16 == 0 && to % 4 == 0;
     const int64_t units = T > 0 && c.P > 0 && c.D > 0 ? ((int64_t)T >> c.block_log2) + 2 * (int64_t)S : 0;
-    const bool small = T <= 8 * (int64_t)S;  // few tokens to a block
+    // A unit's values: of whole blocks, or of the new tokens where they are fewer.
+    int64_t tokens = S > 0 ? ((int64_t)T + S - 1) / S : 0;
+    if (tokens > (int64_t)1 << c.block_log2) tokens = (int64_t)1 << c.block_log2;
+    const bool wave = tokens * c.D <= 64 * 8 * (four ? 4 : 1);
     int64_t blocks = units * c.Hkv * 2;
+    if (wave) blocks = (blocks + 3) / 4;
     if (blocks < 1) blocks = 1;
     if (blocks > 1 << 20) blocks = 1 << 20;
-#define CFP32_APPEND8(NT, FOUR)                                                                                                    do {                                                                                                                               if (c.e4m3) cache8_append_kernel<true, NT, FOUR><<<(unsigned)blocks, NT, 0, stream>>>(k, v, cu, lens, lens_out, c, table, ld, S, W, T, units);         else cache8_append_kernel<false, NT, FOUR><<<(unsigned)blocks, NT, 0, stream>>>(k, v, cu, lens, lens_out, c, table, ld, S, W, T, units);           } while (0)
-    if (small) {
-        if (four) CFP32_APPEND8(64, true);
-        else CFP32_APPEND8(64, false);
+#define CFP32_APPEND8(E4M3, GROUP, FOUR) \
+    cache8_append_kernel<E4M3, GROUP, FOUR><<<(unsigned)blocks, 256, 0, stream>>>(k, v, cu, lens, lens_out, c, table, ld, S, W, T, units)
+#define CFP32_APPEND8_TYPE(GROUP, FOUR)                 \
+    do {                                                \
+        if (c.e4m3) CFP32_APPEND8(true, GROUP, FOUR);   \
+        else CFP32_APPEND8(false, GROUP, FOUR);         \
+    } while (0)
+    if (wave) {
+        if (four) CFP32_APPEND8_TYPE(64, true);
+        else CFP32_APPEND8_TYPE(64, false);
     } else {
-        if (four) CFP32_APPEND8(256, true);
-        else CFP32_APPEND8(256, false);
+        if (four) CFP32_APPEND8_TYPE(256, true);
+        else CFP32_APPEND8_TYPE(256, false);
     }
+#undef CFP32_APPEND8_TYPE
 #undef CFP32_APPEND8
     return hipGetLastError();
 }
@@ -249,26 +286,32 @@ hipError_t launch_cache8_read(const Cache8 &c, const int32_t *table, int64_t ld,
 {
     if (T == 0 || S == 0 || c.Hkv == 0 || c.D == 0) return hipSuccess;
     const int64_t eb = f16 ? 2 : 4;
-    // Codes to a load: what divides every address; results are stored 16 bytes at a time, or as many as these are.
-    int64_t m = 16 | c.D;
+    // Codes to a thread: results of 16 bytes, or fewer where an address does not allow them.
+    int64_t m = (f16 ? 8 : 4) | c.D;
     if (c.P > 0) m |= (int64_t)((uintptr_t)c.k.data | (uintptr_t)c.v.data) | c.k.page | c.k.head | c.k.tok | c.v.page | c.v.head | c.v.tok;
-    m &= -m;
     const int64_t to = (int64_t)((uintptr_t)k.data | (uintptr_t)v.data) | eb * (k.tok | k.head | v.tok | v.head);
-    while (m > 1 && to % (m * eb < 16 ? m * eb : 16)) m >>= 1;
-    const int E = m >= 16 ? 16 : m >= 8 ? 8 : m >= 4 ? 4 : 1;
-    const int64_t per = (int64_t)c.Hkv * (c.D / E);
-    int64_t tokens = per >= 1024 ? 1 : 1024 / per;
-    if (tokens > 64) tokens = 64;
+    m &= -m;
+    while (m > 1 && to % (m * eb)) m >>= 1;
+    const int E = m >= 8 ? 8 : m >= 4 ? 4 : 1;
+    int64_t tokens = (int64_t)T / 768;  // of both launched halves some 1536 blocks, of at least four tokens
+    tokens = tokens < 4 ? 4 : tokens > 32 ? 32 : tokens;
     int64_t blocks = (T + tokens - 1) / tokens;
     if (blocks > 1 << 20) blocks = 1 << 20;
     const dim3 grid((unsigned)blocks, 2);
-#define CFP32_READ8(E4M3, OUT, E)     cache8_read_kernel<E4M3, OUT, E><<<grid, 256, 0, stream>>>(c, table, ld, first, cu, k, v, S, W, T, (int)tokens)
-#define CFP32_READ8_TYPE(E)                                     do {                                                            if (c.e4m3) {                                                   if (f16) CFP32_READ8(true, _Float16, E);                    else CFP32_READ8(true, float, E);                       } else {                                                        if (f16) CFP32_READ8(false, _Float16, E);                   else CFP32_READ8(false, float, E);                      }                                                       } while (0)
-    switch (E) {
-    case 16: CFP32_READ8_TYPE(16); break;
-    case 8: CFP32_READ8_TYPE(8); break;
-    case 4: CFP32_READ8_TYPE(4); break;
-    default: CFP32_READ8_TYPE(1); break;
+#define CFP32_READ8(E4M3, OUT, E) \
+    cache8_read_kernel<E4M3, OUT, E><<<grid, 256, 0, stream>>>(c, table, ld, first, cu, k, v, S, W, T, (int)tokens)
+#define CFP32_READ8_TYPE(OUT, E)                    \
+    do {                                            \
+        if (c.e4m3) CFP32_READ8(true, OUT, E);      \
+        else CFP32_READ8(false, OUT, E);            \
+    } while (0)
+    if (f16) {
+        if (E == 8) CFP32_READ8_TYPE(_Float16, 8);
+        else if (E == 4) CFP32_READ8_TYPE(_Float16, 4);
+        else CFP32_READ8_TYPE(_Float16, 1);
+    } else {
+        if (E == 4) CFP32_READ8_TYPE(float, 4);
+        else CFP32_READ8_TYPE(float, 1);
     }
 #undef CFP32_READ8_TYPE
 #undef CFP32_READ8

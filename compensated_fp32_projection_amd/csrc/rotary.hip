@@ -135,7 +135,10 @@ hipError_t launch_rotary(const RotaryArgs &a, hipStream_t stream)
         if (x->heads) m |= x->in_tok | x->in_head | x->out_tok | x->out_head | ((uintptr_t)x->in | (uintptr_t)x->out) / size;
     const int vec = (int)(m & -m);
     const int turned = a.R / 2 / vec, per = turned + rest / vec;
-    const int tokens = 1;
+    // Tokens to a block: some 1024 items, as long as there are blocks enough.
+    int tokens = 1024 / (heads * per) < 16 ? 1024 / (heads * per) : 16;
+    if (tokens > a.T / 1024) tokens = a.T / 1024;
+    if (tokens < 1) tokens = 1;
     const int64_t blocks = ((int64_t)a.T + tokens - 1) / tokens;
     const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), 1);
     const size_t lds = (size_t)tokens * a.R * sizeof(float);
