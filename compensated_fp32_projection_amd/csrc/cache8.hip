@@ -63,10 +63,19 @@ __global__ __launch_bounds__(256) void cache8_append_kernel(HeadsView k, HeadsVi
         const int items = m * per;
         uint32_t most = 0;
         float held[kHeld][E];
-        auto load = [&](int i, float (&y)[E]) {
-            const int t = (int)over(i, per), d = i - t * per;
+        // A thread's items: item i is token i / per and dims E (i % per) of the unit, GROUP further each time.
+        const int by_t = GROUP / per, by_d = GROUP - by_t * per;
+        struct Walk {
+            int t, d;
+        };
+        auto begin = [&]() { return Walk{me / per, me - me / per * per}; };
+        auto next = [&](Walk &w) {
+            w.t += by_t, w.d += by_d;
+            if (w.d >= per) w.d -= per, ++w.t;
+        };
+        auto load = [&](const Walk &at, float (&y)[E]) {
             typedef float vec __attribute__((ext_vector_type(E)));
-            const vec w = __builtin_nontemporal_load(reinterpret_cast<const vec *>(in + t * x.tok + E * d));
+            const vec w = __builtin_nontemporal_load(reinterpret_cast<const vec *>(in + at.t * x.tok + E * at.d));
 #pragma unroll
             for (int q = 0; q < E; ++q) y[q] = w[q];
         };
@@ -74,15 +83,16 @@ __global__ __launch_bounds__(256) void cache8_append_kernel(HeadsView k, HeadsVi
 #pragma unroll
             for (int q = 0; q < E; ++q) most = max(most, magnitude(y[q]));
         };
+        Walk at = begin();
 #pragma unroll
-        for (int r = 0; r < kHeld; ++r)
-            if (me + r * GROUP < items) load(me + r * GROUP, held[r]);
+        for (int r = 0; r < kHeld; ++r, next(at))
+            if (at.t < m) load(at, held[r]);
 #pragma unroll
         for (int r = 0; r < kHeld; ++r)
             if (me + r * GROUP < items) look(held[r]);
-        for (int i = me + kHeld * GROUP; i < items; i += GROUP) {
+        for (; at.t < m; next(at)) {
             float y[E];
-            load(i, y);
+            load(at, y);
             look(y);
         }
         most = max(most, from_lane<1>(most));
@@ -110,39 +120,40 @@ __global__ __launch_bounds__(256) void cache8_append_kernel(HeadsView k, HeadsVi
         if (me == 0) *scale = sc;
         const bool known = sc == sc;
         const float inv = 1.0f / sc;
-        auto store = [&](int i, const float (&y)[E]) {
-            const int t = (int)over(i, per), d = i - t * per;
-            uint8_t *p = base + (old + t) * pool.tok;
+        auto store = [&](const Walk &at, const float (&y)[E]) {
+            uint8_t *p = base + (old + at.t) * pool.tok;
             float w[4] = {};
 #pragma unroll
             for (int q = 0; q < E; ++q) w[q] = y[q];
             const uint32_t codes = known ? encode<E4M3>(w, sc, inv) : 0u;
-            if constexpr (FOUR) *reinterpret_cast<uint32_t *>(p + 4 * d) = codes;
-            else p[d] = (uint8_t)codes;
+            if constexpr (FOUR) *reinterpret_cast<uint32_t *>(p + 4 * at.d) = codes;
+            else p[at.d] = (uint8_t)codes;
         };
+        at = begin();
 #pragma unroll
-        for (int r = 0; r < kHeld; ++r)
-            if (me + r * GROUP < items) store(me + r * GROUP, held[r]);
-        for (int i = me + kHeld * GROUP; i < items; i += GROUP) {
+        for (int r = 0; r < kHeld; ++r, next(at))
+            if (at.t < m) store(at, held[r]);
+        for (; at.t < m; next(at)) {
             float y[E];
-            load(i, y);
-            store(i, y);
+            load(at, y);
+            store(at, y);
         }
         if (known && up) {
-            for (int i = me; i < old * per; i += GROUP) {
-                const int t = i / per, d = i - t * per;
-                uint8_t *p = base + t * pool.tok;
+            for (at = begin(); at.t < old; next(at)) {
+                uint8_t *p = base + at.t * pool.tok;
                 if constexpr (FOUR) {
-                    uint32_t *w = reinterpret_cast<uint32_t *>(p + 4 * d);
+                    uint32_t *w = reinterpret_cast<uint32_t *>(p + 4 * at.d);
                     *w = shifted<E4M3>(*w, up);
                 } else {
-                    p[d] = (uint8_t)shifted<E4M3>(p[d], up);
+                    p[at.d] = (uint8_t)shifted<E4M3>(p[at.d], up);
                 }
             }
         }
         if constexpr (GROUP == 256) __syncthreads();  // largest has been read
     }
 }
+
+constexpr int kReadTokens = 64;
 
 // A block takes `tokens` rows; a thread E codes of a head, the same for all of
 // its tokens, so that a wave's stores are whole lines (with 16 codes to a
@@ -153,8 +164,8 @@ __global__ __launch_bounds__(256) void cache8_read_kernel(Cache8 c, const int32_
                                                           const int32_t *cu, HeadsOut k, HeadsOut v, int S, int W, int T,
                                                           int tokens)
 {
-    constexpr int kMost = 64, kAtOnce = 4;
-    __shared__ int pages[kMost], offs[kMost];  // page -1: none, -2: no row of a sequence
+    constexpr int kAtOnce = 8;
+    __shared__ int64_t codes_at[kReadTokens], scales_at[kReadTokens];  // element offsets; codes -1: no page, -2: no row of a sequence
     __shared__ int starts[64];                 // of the sequences from the first token's on
     const int per = c.D / E;
     const bool second = blockIdx.y;
@@ -193,8 +204,8 @@ __global__ __launch_bounds__(256) void cache8_read_kernel(Cache8 c, const int32_
                 if (page < 0 || page >= c.P) page = -1;
             }
             if ((int)threadIdx.x < nt) {
-                pages[threadIdx.x] = page;
-                offs[threadIdx.x] = off;
+                codes_at[threadIdx.x] = page < 0 ? page : page * pool.page + off * pool.tok;
+                scales_at[threadIdx.x] = page * sv.page + (off >> c.block_log2);
             }
         }
         __syncthreads();
@@ -209,21 +220,21 @@ __global__ __launch_bounds__(256) void cache8_read_kernel(Cache8 c, const int32_
                 typedef uint32_t vec __attribute__((ext_vector_type(E < 4 ? 1 : E / 4)));
                 vec w[kAtOnce];
                 float s[kAtOnce];
-#pragma unroll
-                for (int g = 0; g < kAtOnce; ++g) {
-                    const int t = u + g * slots, page = t < nt ? pages[t] : -2, off = t < nt ? offs[t] : 0;
-                    s[g] = NAN;
-                    w[g] = (vec)0;
-                    if (page < 0) continue;
-                    s[g] = scales[page * sv.page + (off >> c.block_log2)];
-                    const uint8_t *p = from + page * pool.page + off * pool.tok;
-                    if constexpr (E == 1) w[g] = *p;
-                    else w[g] = *reinterpret_cast<const vec *>(p);
-                }
+                int64_t at[kAtOnce];
 #pragma unroll
                 for (int g = 0; g < kAtOnce; ++g) {
                     const int t = u + g * slots;
-                    if (t >= nt || pages[t] == -2) continue;
+                    at[g] = t < nt ? codes_at[t] : -2;
+                    s[g] = NAN;
+                    w[g] = (vec)0;
+                    if (at[g] < 0) continue;
+                    s[g] = scales[scales_at[t]];
+                    if constexpr (E == 1) w[g] = from[at[g]];
+                    else w[g] = *reinterpret_cast<const vec *>(from + at[g]);
+                }
+#pragma unroll
+                for (int g = 0; g < kAtOnce; ++g) {
+                    if (at[g] == -2) continue;
                     typedef Out piece __attribute__((ext_vector_type(E)));
                     piece y;
 #pragma unroll
@@ -236,11 +247,11 @@ __global__ __launch_bounds__(256) void cache8_read_kernel(Cache8 c, const int32_
                         asm("" : "+v"(x));
                         y[e] = (Out)x;
                     }
-                    *reinterpret_cast<piece *>(out + t * to.tok) = y;
+                    *reinterpret_cast<piece *>(out + (u + g * slots) * to.tok) = y;
                 }
             }
         }
-        __syncthreads();  // pages have been read
+        __syncthreads();  // the offsets have been read
     }
 }
 
@@ -293,8 +304,11 @@ hipError_t launch_cache8_read(const Cache8 &c, const int32_t *table, int64_t ld,
     m &= -m;
     while (m > 1 && to % (m * eb)) m >>= 1;
     const int E = m >= 8 ? 8 : m >= 4 ? 4 : 1;
-    int64_t tokens = (int64_t)T / 768;  // of both launched halves some 1536 blocks, of at least four tokens
-    tokens = tokens < 4 ? 4 : tokens > 32 ? 32 : tokens;
+    // Some 512 blocks for K and as many for V: the sequences' lookups are few, and what a block waits for is hidden by
+    // the others (tokens to a block of T / 128, / 512 and / 1500: 8574 x 8 x 128 INT8 to FP32 29, 17 and 18 us, 6769 x
+    // 12 x 64 E4M3 to FP16 15, 10 and 15).
+    int64_t tokens = (int64_t)T / 512;
+    tokens = tokens < 4 ? 4 : tokens > kReadTokens ? kReadTokens : tokens;
     int64_t blocks = (T + tokens - 1) / tokens;
     if (blocks > 1 << 20) blocks = 1 << 20;
     const dim3 grid((unsigned)blocks, 2);
