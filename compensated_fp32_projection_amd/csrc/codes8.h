@@ -32,7 +32,7 @@ __device__ __forceinline__ float fresh_scale(uint32_t most)
         const int x = (int)(most >> 23) - 8 + ((most & 0x7FFFFF) > 0x600000);
         return __builtin_bit_cast(float, (uint32_t)max(x, 1) << 23);
     } else {
-        return fmaxf(__builtin_bit_cast(float, most) / 127.0f, kLeastScale);
+        return fmaxf(__builtin_bit_cast(float, most) * (1.0f / 127.0f), kLeastScale);
     }
 }
 
@@ -46,7 +46,7 @@ __device__ __forceinline__ int growth(float s, uint32_t most)
 }
 
 // x / s to the nearest integer, ties to even, of the exact quotient (|x| is at
-// most 127 s but for a rounding, s normal).  x * inv is off by 2^-16 at most,
+// most 127 s but for two roundings, s normal).  x * inv is off by 2^-16 at most,
 // so t is the nearest integer or, next to a tie, its neighbour; what x leaves
 // beside t s needs no more than FP32's bits, and decides.
 __device__ __forceinline__ int quotient(float x, float s, float inv)

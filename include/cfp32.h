@@ -567,9 +567,10 @@ CFP32_API cfp32_status cfp32_rotary(const void *q, int64_t q_tok, int64_t q_head
  * with scale s stands for c s.  Tables, lengths and counts are those of the
  * paged cache above (cfp32_cache_reserve and cfp32_cache_free serve both).
  *
- * A block's scale is made when its first token is written: the largest magnitude
- * m of what is written / 127 for integers (rounded to FP32), the least power of
- * two that brings m to 448 or below for floats, and 2^-126 at least.  A later
+ * A block's scale is made when its first token is written: of the largest
+ * magnitude m of what is written, m x 1/127 for integers (the factor and the
+ * product rounded to FP32), for floats the least power of two that brings m to
+ * 448 or below, and 2^-126 at least.  A later
  * token that does not fit (m > the largest code x the scale, in FP32) multiplies
  * the scale by the least power of two that holds it, and the block's codes are
  * divided by it: so a value of its first tokens is off by less than one step of

@@ -32,7 +32,7 @@ def nearest(y, kind):
 
 def fresh_scale(most, kind):
     if kind == "i8":
-        return max(float(np.float32(most) / np.float32(127)), LEAST)
+        return max(float(np.float32(most) * (np.float32(1) / np.float32(127))), LEAST)
     s = LEAST
     while most > 448 * s:
         s *= 2
