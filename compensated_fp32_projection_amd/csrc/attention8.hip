@@ -85,6 +85,18 @@ __device__ __forceinline__ half8_t column(const uint32_t (&w)[8])
     return h;
 }
 
+// Two values below 2^15 as FP16 parts: high, and what is left of each (exact in
+// FP32, a mixed-precision difference), rounded to nearest even both.
+__device__ __forceinline__ void two_parts(float x, float y, half2_t &hi, half2_t &lo)
+{
+    typedef float float2_t __attribute__((ext_vector_type(2)));
+    hi = __builtin_convertvector(float2_t{x, y}, half2_t);
+    float r, s;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r) : "v"(hi), "v"(x));
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(s) : "v"(hi), "v"(y));
+    lo = __builtin_convertvector(float2_t{r, s}, half2_t);
+}
+
 // Where a sequence's keys are.  A page id outside the pool is replaced by page 0
 // (the pool has pages) and remembered: rows that see it become NaN.  What is
 // the same for a block's lanes (the sequence, its pages) is in scalar registers.
@@ -285,10 +297,11 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
 #pragma unroll
         for (int i = 0; i < KL; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                _Float16 h, w;
-                split_scaled(x[i][e], e2, h, w);
-                qh[2 * i + e / 8][e % 8] = h, ql[2 * i + e / 8][e % 8] = w;
+            for (int e = 0; e < 16; e += 2) {
+                half2_t h, w;
+                two_parts(__builtin_amdgcn_ldexpf(x[i][e], e2), __builtin_amdgcn_ldexpf(x[i][e + 1], e2), h, w);
+                qh[2 * i + e / 8][e % 8] = h[0], qh[2 * i + e / 8][e % 8 + 1] = h[1];
+                ql[2 * i + e / 8][e % 8] = w[0], ql[2 * i + e / 8][e % 8 + 1] = w[1];
             }
         const float f = __builtin_amdgcn_ldexpf(scale * kLog2e * kCode, -e2);
 
@@ -316,10 +329,27 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
 #pragma unroll
                 for (int b = 0; b < NB; ++b) s[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[b], qh[i], s[b], 0, 0, 0);
             }
+            // One factor for a scale's four scores, unless it is beyond FP32's range (a product of 0 may be among them).
+            constexpr int R = FAST ? 1 : 4;
+            float fk[NB][R], peak = 0.0f;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[b][r] = s[b][r] * f * t.ks[b][FAST ? 0 : r];
+                for (int r = 0; r < R; ++r) {
+                    fk[b][r] = f * t.ks[b][r];
+                    peak = fmaxf(peak, fabsf(fk[b][r]));
+                }
+            if (__any(peak == INFINITY)) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[b][r] = s[b][r] * f * t.ks[b][r % R];
+            } else {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[b][r] *= fk[b][r % R];
+            }
             if (ends) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
@@ -365,10 +395,11 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    _Float16 h, u;
-                    split_scaled(w[b][r], e, h, u);
-                    wh[b / 2][b % 2 * 4 + r] = h, wl[b / 2][b % 2 * 4 + r] = u;
+                for (int r = 0; r < 4; r += 2) {
+                    half2_t h, u;
+                    two_parts(__builtin_amdgcn_ldexpf(w[b][r], e), __builtin_amdgcn_ldexpf(w[b][r + 1], e), h, u);
+                    wh[b / 2][b % 2 * 4 + r] = h[0], wh[b / 2][b % 2 * 4 + r + 1] = h[1];
+                    wl[b / 2][b % 2 * 4 + r] = u[0], wl[b / 2][b % 2 * 4 + r + 1] = u[1];
                 }
             const float g = __builtin_amdgcn_ldexpf(kCode, -e);
 #pragma unroll
