@@ -308,7 +308,8 @@ hipError_t launch_beam_select(const BeamArgs &a, void *workspace, hipStream_t st
 {
     const BeamPlan p = plan_beam(a.S, a.beams, a.V, a.n);
     const int64_t units = (int64_t)a.S * a.beams * p.chunks, blocks = (units + 3) / 4;
-    if (blocks > 0x7FFFFFFF || blocks * 256 > 0xFFFFFFFF) return hipErrorInvalidConfiguration;
+    const int waves = a.beams < 16 ? a.beams : 16;
+    if (blocks > 0x7FFFFFFF || blocks * 256 > 0xFFFFFFFF || (int64_t)a.S * 64 * waves > 0xFFFFFFFF) return hipErrorInvalidConfiguration;
     float2 *stats = (float2 *)workspace;
     uint64_t *lists = (uint64_t *)(stats + units);
     const bool wide = ((reinterpret_cast<uintptr_t>(a.logits) | (uintptr_t)(a.ld * 4)) & 15) == 0;
@@ -323,7 +324,6 @@ hipError_t launch_beam_select(const BeamArgs &a, void *workspace, hipStream_t st
 #undef CFP32_BEAM_ROWS
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int waves = a.beams < 16 ? a.beams : 16;
     const size_t lds = (size_t)a.beams * a.n * (sizeof(double) + sizeof(int));
     beam_join_kernel<<<(unsigned)a.S, 64 * waves, lds, stream>>>(a, p.chunks, stats, lists);
     return hipGetLastError();
