@@ -2,9 +2,10 @@
 //
 // Pair i of a token at position p turns by the angle p f_i, the same in every
 // head.  A block takes some tokens: it makes their sines and cosines once,
-// into LDS, and then passes over all of their heads.  Its first values are
-// asked for before that, so that the two latencies are one.  What bounds it is
-// the memory: each value is read and written once.
+// into LDS, and then passes over all of their heads.  What bounds it is the
+// memory: each value is read and written once (8192 x 32/8 x 128 FP32 62 us, 5.4
+// TB/s; 64 tokens of these 4 us, mostly a position's, a value's and the launch's
+// latency).
 //
 // Angles: p f_i / 2 pi in FP64 is reduced to a quarter turn there, since the
 // whole turns of a far position leave FP32 nothing (2^20 positions of 1 radian
