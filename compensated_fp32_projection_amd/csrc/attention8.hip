@@ -307,7 +307,9 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                 qh[2 * i + e / 8][e % 8] = h[0], qh[2 * i + e / 8][e % 8 + 1] = h[1];
                 ql[2 * i + e / 8][e % 8] = w[0], ql[2 * i + e / 8][e % 8 + 1] = w[1];
             }
-        const float f = __builtin_amdgcn_ldexpf(scale * kLog2e * kCode, -e2);
+        // 2^-e2 in two halves: of very small rows it is beyond FP32's range, where large scales bring scores back.
+        const int half = e2 / 2;
+        const float f = __builtin_amdgcn_ldexpf(scale * kLog2e * kCode, -half), f2 = __builtin_amdgcn_ldexpf(1.0f, half - e2);
 
         // A step's work on one tile, while the next one's is on its way into the other.
         auto step = [&](Tile &t, Tile &ahead) {
@@ -340,14 +342,14 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
             for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    fk[b][r] = f * t.ks[b][r];
+                    fk[b][r] = f * t.ks[b][r] * f2;
                     peak = fmaxf(peak, fabsf(fk[b][r]));
                 }
             if (__any(peak == INFINITY)) {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) s[b][r] = s[b][r] * f * t.ks[b][r % R];
+                    for (int r = 0; r < 4; ++r) s[b][r] = s[b][r] * f * t.ks[b][r % R] * f2;
             } else {
 #pragma unroll
                 for (int b = 0; b < NB; ++b)

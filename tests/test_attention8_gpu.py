@@ -129,7 +129,8 @@ def test_scale(scale, kind):
 def test_magnitudes(kind):
     """q and the scales of K and V from very small to very large, next to each other."""
     rng = np.random.default_rng(2)
-    for qs, kss, vss in ((1, 0, 60), (2.0 ** 60, -60, 0), (2.0 ** -60, 50, 100), (1, 0, 0), (2.0 ** 100, -105, 20)):
+    for qs, kss, vss in ((1, 0, 60), (2.0 ** 60, -60, 0), (2.0 ** -60, 50, 100), (1, 0, 0), (2.0 ** 100, -105, 20),
+                          (2.0 ** -120, 118, 0), (2.0 ** 115, -118, 10)):
         note(f"decode8 magnitudes {qs} {kss} {vss} {kind}")
         q, arrays, table, lens = problem(rng, [300, 40], 4, 2, 64, 16, 2, kind)
         q *= np.float32(qs)
