@@ -254,6 +254,7 @@ cfp32_status cfp32_beam_select(const float *logits, int64_t ld, const float *sco
     if (S == 0) return CFP32_OK;
     if (!logits || !scores || !parents || !tokens || !scores_out || !aligned_to(logits, 4) || !view_ok(S * beams, ld, 1, 0, 1, 0, V))
         return CFP32_ERR_INVALID_VALUE;
+    if (scores_out == scores || (done && done_out == done)) return CFP32_ERR_INVALID_VALUE;  // a block reads what others write
     if (!workspace || workspace_bytes < cfp32_beam_select_workspace_bytes(S, beams, V, n)) return CFP32_ERR_INVALID_VALUE;
     cfp32_status st = api_check_device();
     if (st != CFP32_OK) return st;

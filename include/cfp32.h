@@ -674,12 +674,13 @@ CFP32_API size_t cfp32_beam_select_workspace_bytes(int64_t S, int64_t beams, int
  *   beams, n : 1 .. 64;  V >= 1, below 2^31.
  *   eos    : the token that finishes a beam (negative: none does).
  *   parents, tokens : int32 [S, n];  scores_out : FP32 [S, n];
- *   done_out : uint8 [S, n] (0 or 1) or NULL.
+ *   done_out : uint8 [S, n] (0 or 1) or NULL.  Outputs are not inputs.
  * Beam b offers token t with scores[b] + x_t - log sum exp(x) (the sum's terms
  * FP32, off by some 2^-22, FP64 from there on; rounded once, at the end).  A
- * finished beam offers itself alone, with its score and the token eos.  Offers are taken in order of their scores, of equal ones the lowest beam's
- * and of a beam's equal logits the lowest token first; a beam's are in the order
- * of its logits.  A token whose logit is -infinity is not offered, nor is
+ * finished beam offers itself alone, with its score and the token eos.  Offers
+ * are taken in order of their scores, of equal ones the lowest beam's and of a
+ * beam's equal logits the lowest token first; a beam's are in the order of its
+ * logits.  A token whose logit is -infinity is not offered, nor is
  * anything of a beam whose score is not finite, or of one whose logits hold a
  * NaN or +infinity.  Where there are fewer than n offers, the rest has parent
  * -1, token eos, score -infinity and is done.  Two kernel launches. */
@@ -689,7 +690,8 @@ CFP32_API cfp32_status cfp32_beam_select(const float *logits, int64_t ld, const 
 
 /* Rows of states in the order of their parents: row i of out [n] is row
  * parents[i] of states [rows], or zeros where that is no row.  Rows are row_bytes
- * long, at strides of bytes (>= row_bytes; those of states >= 0).  One kernel launch. */
+ * long, at strides of bytes (>= row_bytes; those of states >= 0).  out does not
+ * overlap states.  One kernel launch. */
 CFP32_API cfp32_status cfp32_beam_reorder(const void *states, int64_t stride, void *out, int64_t out_stride,
                                 const int32_t *parents, int64_t rows, int64_t n, int64_t row_bytes, void *stream);
 

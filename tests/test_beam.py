@@ -35,6 +35,7 @@ def test_the_calls_as_they_stand_are_accepted():
 @pytest.mark.parametrize("changed", [
     dict(logits=None), dict(scores=None), dict(parents=None), dict(tokens=None), dict(scores_out=None), dict(workspace=None),
     dict(S=-1), dict(beams=0), dict(beams=65), dict(n=0), dict(n=65), dict(V=0), dict(V=1 << 31), dict(ld=999), dict(ld=1 << 46),
+    dict(scores_out=FAKE), dict(done_out=FAKE), dict(scores_out=FAKE, done=None),
     dict(logits=FAKE + 2), dict(workspace_bytes=100), dict(S=1 << 30), dict(eos=1 << 40), dict(eos=-(1 << 40))])
 def test_refused_selections(changed):
     assert select(**changed) == E
