@@ -64,7 +64,6 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int tokens, i
     const int pairs = a.R / 2;
     for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
         const int nt = (int)min((int64_t)tokens, a.T - t0);
-        const int h0 = blockIdx.y * heads, nh = min(heads, a.q.heads + a.k.heads - h0);
         for (int i = threadIdx.x; i < nt * pairs; i += 256) {
             const int t = i / pairs, p = i - t * pairs;
             const double pos = (double)(a.positions ? a.positions[t0 + t] : t0 + t);
@@ -74,9 +73,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int tokens, i
             table[2 * i + 1] = (a.transpose ? -s : s) * a.amplitude;
         }
         __syncthreads();
-        const int n = nt * nh * per;
+        const int n = nt * heads * per;
         for (int i = threadIdx.x; i < n; i += 256) {
-            const int th = i / per, item = i - th * per, t = th / nh, h = h0 + th - t * nh;
+            const int th = i / per, item = i - th * per, t = th / heads, h = th - t * heads;
             const bool second = h >= a.q.heads;
             const RotaryTensor &x = second ? a.k : a.q;
             const int hh = second ? h - a.q.heads : h;
@@ -141,7 +140,7 @@ hipError_t launch_rotary(const RotaryArgs &a, hipStream_t stream)
     if (tokens > a.T / 1024) tokens = a.T / 1024;
     if (tokens < 1) tokens = 1;
     const int64_t blocks = ((int64_t)a.T + tokens - 1) / tokens;
-    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), 1);
+    const unsigned grid = (unsigned)(blocks < 65536 ? blocks : 65536);
     const size_t lds = (size_t)tokens * a.R * sizeof(float);
 #define CFP32_ROTARY(T, VEC)                                                                                      \
     do {                                                                                                          \
