@@ -17,8 +17,8 @@
 // A step of 32 keys x 128 costs a wave some 650 vector and 32 matrix
 // instructions for its 8 KiB, which with two waves to a SIMD is 7 TB/s over the
 // chip; its codes are asked for a step ahead, 64 KiB to a compute unit.  Long
-// contexts are bounded by the memory (64 x 4000 to 8000 keys x 32/8 x 128 INT8 170
-// us, 4.6 TB/s), short ones by what they wait for one after the other: a length, a
+// contexts are bounded by the memory (64 x 4000 to 8000 keys x 32/8 x 128 INT8 162
+// us, 4.9 TB/s), short ones by what they wait for one after the other: a length, a
 // page, codes, the join (130 keys 7.6 us).
 #include "attention8.h"
 #include "attention_join.h"
@@ -447,9 +447,8 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
         l += from_lane<32>(l);
     }
     // O^T: this lane's column, dims NV (4 quad + r) + c.
-    CFP32_LDS float *sums = to.o[0];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) sums = wave == w ? to.o[w] : sums;
+    // Not to.o[wave]: an index would put the pointers into private memory (16 x 4000 keys x 32/8 x 128 31 -> 34 us).
+    CFP32_LDS float *sums = to.o[0] + wave * Joined<DP, NW>::kWave;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll

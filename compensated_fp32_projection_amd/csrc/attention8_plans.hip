@@ -13,11 +13,11 @@ bool grid_ok(int64_t blocks, int threads) { return blocks <= 0x7FFFFFFF && block
 // Parts are made until the grid has kBlocks blocks, each of a step of all waves
 // (128 or 256 keys) or more: two to a compute unit, which is what its registers
 // hold (with 256 / 512 / 1024 blocks at the most 16 x 4000 x 32/8 x 128 INT8 takes
-// 34 / 35 / 40 us, 12 x 2000 x 12 x 64 E4M3 21 / 19 / 19, 64 x 8000 x 32/8 x 128
-// 182 / 181 / 188).  Of up to three steps none are made, since joining them is a
-// launch of its own: in one part and in several 300 keys x 16 x 32/8 x 128 take
-// 10.0 / 11.7 us, 500 x 12 x 12 x 64 8.4 / 11.0; of four 500 x 4 x 32/8 x 128 11.4 /
-// 10.2.  Blocks of eight waves were no faster (1 x 500 11.3 us against 9.6).
+// 35 / 32 / 37 us, 12 x 2000 x 12 x 64 E4M3 22 / 17 / 18, 2 x 65536 x 32/8 x 128 50 /
+// 44 / 50).  Of up to three steps none are made, since joining them is a launch of
+// its own: in one part and in several 300 keys x 16 x 32/8 x 128 take 10.0 / 11.7 us,
+// 500 x 12 x 12 x 64 8.4 / 11.0; of four 500 x 4 x 32/8 x 128 11.4 / 10.2.  Blocks of
+// eight waves were no faster (1 x 500 11.3 us against 9.6).
 constexpr int64_t kBlocks = 512, kOneBlock = 3;
 int key_parts(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t keys)
 {
