@@ -1,7 +1,7 @@
 // The 8-bit cache: tokens written with their blocks' scales, and read back
 // (include/cfp32.h).  Both are bounded by the memory: writing reads 4 bytes and
 // writes one for each value, reading back the other way (8190 tokens of 8 x 128
-// INT8 written in 21 us, 4.0 TB/s, 8574 read to FP32 in 17, 5.1 TB/s).  One token of
+// INT8 written in 19 us, 4.4 TB/s, 8574 read to FP32 in 17, 5.1 TB/s).  One token of
 // 64 sequences takes 5 us: sequence, page and values, one after the other.
 #include "attention_device.h"
 #include "cache8.h"
@@ -20,7 +20,7 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_ca
 // wave's (GROUP 64, four to a thread block), or a whole thread block's where it
 // has more values than a wave holds in registers between finding the largest
 // and writing: what a unit waits for (its sequence, its page, its values) then
-// has more units beside it to hide it (6001 tokens of 32 x 64 E4M3 21 -> 14.7 us).
+// has more units beside it to hide it (6001 tokens of 12 x 64 E4M3 21 -> 14.7 us).
 // FOUR: four values at a time (16-byte loads, 4-byte stores).
 template <bool E4M3, int GROUP, bool FOUR>
 __global__ __launch_bounds__(256) void cache8_append_kernel(HeadsView k, HeadsView v, const int32_t *cu, const int32_t *lens,
@@ -37,7 +37,12 @@ __global__ __launch_bounds__(256) void cache8_append_kernel(HeadsView k, HeadsVi
     const int per = c.D / E;
     auto start = [&](int s) { return (int64_t)(cu[s] >> c.block_log2) + 2 * (int64_t)s; };
     const int64_t first = GROUP == 64 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x, step = GROUP == 64 ? (int64_t)gridDim.x * 4 : gridDim.x;
-    for (int64_t u = first; u < total; u += step) {
+    // A unit's index in scalar registers, and with it all of its addresses' common part: with that and the walks
+    // made anew a thread needs 70 registers, not 118 (8190 tokens of 8 x 128 INT8 21 -> 19 us, 6001 of 12 x 64 E4M3
+    // 14.5 -> 12.4).
+    for (int64_t next_u = first; next_u < total; next_u += step) {
+        const int64_t u = (int64_t)__builtin_amdgcn_readfirstlane((int)(next_u >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)next_u);
         const int64_t uh = over(u, c.Hkv), id = uh >> 1;
         const int h = (int)(u - uh * c.Hkv);
         const bool second = uh & 1;
@@ -70,7 +75,12 @@ __global__ __launch_bounds__(256) void cache8_append_kernel(HeadsView k, HeadsVi
         struct Walk {
             int t, d;
         };
-        auto begin = [&]() { return Walk{me / per, me - me / per * per}; };
+        auto begin = [&]() {
+            int i = me;
+            asm volatile("" : "+v"(i));  // made anew where values are written, not held since they were loaded
+            const int t = i / per;
+            return Walk{t, i - t * per};
+        };
         auto next = [&](Walk &w) {
             w.t += by_t, w.d += by_d;
             if (w.d >= per) w.d -= per, ++w.t;
