@@ -426,8 +426,17 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _mat(t, dtypes, name):
-    """(pointer, rows, cols, ld) of a 2-D device tensor with unit column stride."""
+def _row_step(t, name, shared=False):
+    """Elements from one row of a 2-D tensor to the next, at least its columns; `shared`: or 0, all rows being one."""
+    rows, cols = t.shape
+    step = t.stride(0) if rows > 1 else cols
+    if step < cols and not (shared and step == 0):
+        raise ValueError(f"{name}: rows overlap (stride(0) is {step}, of {cols} columns)")
+    return step
+
+
+def _mat(t, dtypes, name, shared=False):
+    """(pointer, rows, cols, ld) of a 2-D device tensor with unit column stride; `shared`: as ``_row_step`` has it."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise TypeError(f"{name}: expected a GPU tensor")
@@ -438,8 +447,8 @@ def _mat(t, dtypes, name):
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: columns must be contiguous (stride(1) == 1)")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    return t.data_ptr(), rows, cols, max(ld, cols)
+    ld = _row_step(t, name, shared)
+    return t.data_ptr(), rows, cols, ld if shared else max(ld, 1)
 
 
 def _f16_dtypes():
@@ -1297,7 +1306,8 @@ def beam_select(logits, scores, n: int | None = None, done=None, eos: int = -1, 
                 stream=None):
     """(parents, tokens, scores, done), [S, n] each (n: as many beams as there
     are unless given; at most 64): the best continuations of S sequences.
-    logits FP32 [S * beams, V]; scores FP32 [S, beams], the beams' sums of
+    logits FP32 [S * beams, V], one row for all beams among them
+    (``row.expand(S * beams, V)``); scores FP32 [S, beams], the beams' sums of
     log-probabilities; done bool [S, beams] or None; eos: the token that
     finishes a beam.  parents are rows of the batch of S * beams beams, as
     ``beam_reorder`` and ``cache_fork`` take them (-1 where there is no
@@ -1307,7 +1317,7 @@ def beam_select(logits, scores, n: int | None = None, done=None, eos: int = -1, 
         if done_ is not None:
             return done_
     torch = _torch()
-    px, rows, V, ld = _mat(logits, (torch.float32,), "logits")
+    px, rows, V, ld = _mat(logits, (torch.float32,), "logits", shared=True)
     dev = logits.device
     if not isinstance(scores, torch.Tensor) or scores.dtype != torch.float32 or scores.device != dev:
         raise TypeError("scores: expected a float32 tensor on logits' device")

@@ -249,7 +249,7 @@ cfp32_status cfp32_beam_select(const float *logits, int64_t ld, const float *sco
                                float *scores_out, uint8_t *done_out, void *workspace, size_t workspace_bytes, void *stream)
 {
     if (!size_ok(S) || S > kMaxSize / kMaxBeams || beams < 1 || beams > kMaxBeams || n < 1 || n > kMaxBeams || V < 1 ||
-        V > kMaxSize - 4096 || ld < V || eos < -kMaxSize || eos > kMaxSize)
+        V > kMaxSize - 4096 || (ld < V && ld) || eos < -kMaxSize || eos > kMaxSize)
         return CFP32_ERR_INVALID_VALUE;
     if (S == 0) return CFP32_OK;
     if (!logits || !scores || !parents || !tokens || !scores_out || !aligned_to(logits, 4) || !view_ok(S * beams, ld, 1, 0, 1, 0, V))

@@ -668,7 +668,8 @@ CFP32_API cfp32_status cfp32_attention8_decode(const float *q, int64_t q_seq, in
 CFP32_API size_t cfp32_beam_select_workspace_bytes(int64_t S, int64_t beams, int64_t V, int64_t n);
 
 /* The n best continuations of each sequence.
- *   logits : FP32 [S * beams, V], leading dimension ld >= V.
+ *   logits : FP32 [S * beams, V], leading dimension ld >= V, or 0 where all
+ *            beams have one row.
  *   scores : FP32 [S, beams], the beams' sums of log-probabilities.
  *   done   : uint8 [S, beams], nonzero for finished beams, or NULL for none.
  *   beams, n : 1 .. 64;  V >= 1, below 2^31.
