@@ -750,8 +750,8 @@ def _ints(t, name, device, dim):
     return t.data_ptr()
 
 
-def _ld(t):
-    return max(t.stride(0) if t.shape[0] > 1 else 0, t.shape[1])
+def _ld(t, name="table", shared=False):
+    return _row_step(t, name, shared)
 
 
 def _pools(k_pages, v_pages):
@@ -866,7 +866,7 @@ def attention_decode(q, k_pages, v_pages, table, lens, shared_pages: int = 0, sc
     po = _heads(out, (torch.float32,), "out", dev)
     need = cfp32_attention_decode_workspace_bytes(B, Hq, Hkv, D, W, page, shared_pages, kv)
     buf, ws, st = _scratch(need, dev, workspace, stream)
-    _check(cfp32_attention_decode(*pq, *at, kv, P, page, pt, _ld(table), W, pl, shared_pages, *po, B, Hq, Hkv, D,
+    _check(cfp32_attention_decode(*pq, *at, kv, P, page, pt, _ld(table, shared=True), W, pl, shared_pages, *po, B, Hq, Hkv, D,
                                   D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention_decode")
     return out
 
@@ -892,7 +892,7 @@ def cache_reserve(table, lens, refs, cu, page: int, missing=None, table_out=None
     pm = None if missing is None else _ints(missing, "missing", dev, 1)
     if table_out.shape != table.shape or refs_out.shape != refs.shape or (missing is not None and not missing.numel()):
         raise ValueError("table_out, refs_out or missing has the wrong shape")
-    _check(cfp32_cache_reserve(pt, _ld(table), pl, pc, pr, pto, _ld(table_out), pro, pm, S, W, refs.shape[0], page,
+    _check(cfp32_cache_reserve(pt, _ld(table), pl, pc, pr, pto, _ld(table_out, "table_out"), pro, pm, S, W, refs.shape[0], page,
                                _stream(stream)), "cfp32_cache_reserve")
     return table_out, refs_out
 
@@ -981,7 +981,7 @@ def cache_free(rows, refs, refs_out=None, stream=None):
     if refs_out.shape != refs.shape:
         raise ValueError("refs_out has the wrong shape")
     R, W = rows.shape
-    _check(cfp32_cache_free(pw, _ld(rows), pr, pro, R, W, refs.shape[0], _stream(stream)), "cfp32_cache_free")
+    _check(cfp32_cache_free(pw, _ld(rows, "rows"), pr, pro, R, W, refs.shape[0], _stream(stream)), "cfp32_cache_free")
     return refs_out
 
 
@@ -1008,7 +1008,7 @@ def cache_compact(k_pages, v_pages, table, refs, table_out=None, refs_out=None, 
     live = _empty(1, torch.int32, dev, stream)
     need = cfp32_cache_compact_workspace_bytes(P)
     buf, ws, st = _scratch(need, dev, workspace, stream)
-    _check(cfp32_cache_compact(*at, kv, P, page, Hkv, D, pt, _ld(table), pr, pto, _ld(table_out), pro,
+    _check(cfp32_cache_compact(*at, kv, P, page, Hkv, D, pt, _ld(table), pr, pto, _ld(table_out, "table_out"), pro,
                                live.data_ptr(), S, W, ws, need, st), "cfp32_cache_compact")
     return table_out, refs_out, live
 
@@ -1206,7 +1206,7 @@ def cache8_read(cache: Cache8, table, cu, tokens: int, first=None, dtype=None, k
             raise ValueError(f"{name} has the wrong shape")
         outs.append(out)
     pk, pv = (_heads(o, (dtype,), n, dev) for o, n in zip(outs, ("k_out", "v_out")))
-    _launch(cfp32_cache8_read, "cfp32_cache8_read", dev, cache.addr, pt, _ld(table), pf, pc, *pk, *pv,
+    _launch(cfp32_cache8_read, "cfp32_cache8_read", dev, cache.addr, pt, _ld(table, shared=True), pf, pc, *pk, *pv,
             KV_F16 if dtype == torch.float16 else KV_F32, S, W, tokens, stream=stream)
     return outs[0], outs[1]
 
@@ -1263,7 +1263,7 @@ def cache8_compact(cache: Cache8, table, refs, table_out=None, refs_out=None, wo
         live = _empty(1, torch.int32, dev, stream)
         need = cfp32_cache_compact_workspace_bytes(P)
         buf, ws, st = _scratch(need, dev, workspace, stream)
-        _check(cfp32_cache8_compact(cache.addr, pt, _ld(table), pr, pto, _ld(table_out), pro, live.data_ptr(), S, W, ws, need,
+        _check(cfp32_cache8_compact(cache.addr, pt, _ld(table), pr, pto, _ld(table_out, "table_out"), pro, live.data_ptr(), S, W, ws, need,
                                     st), "cfp32_cache8_compact")
     return table_out, refs_out, live
 
@@ -1271,7 +1271,8 @@ def cache8_compact(cache: Cache8, table, refs, table_out=None, refs_out=None, wo
 def attention8_decode(q, cache: Cache8, table, lens, scale: float | None = None, out=None,
                       workspace: Workspace | None = None, stream=None):
     """Attention of one new token per sequence against an 8-bit cache: q FP32
-    [B, Hq, D]; table int32 [B, W]; lens int32 [B].  Returns FP32 [B, Hq, D]."""
+    [B, Hq, D]; table int32 [B, W] (one row for all: ``row.expand(B, W)``);
+    lens int32 [B].  Returns FP32 [B, Hq, D]."""
     torch = _torch()
     P, Hkv, page, D2 = _cache8(cache).shape
     if stream is None and workspace is None:
@@ -1295,7 +1296,7 @@ def attention8_decode(q, cache: Cache8, table, lens, scale: float | None = None,
         po = _heads(out, (torch.float32,), "out", dev)
         need = cfp32_attention8_decode_workspace_bytes(B, Hq, Hkv, D, W, page)
         buf, ws, st = _scratch(need, dev, workspace, stream)
-        _check(cfp32_attention8_decode(*pq, cache.addr, pt, _ld(table), W, pl, *po, B, Hq,
+        _check(cfp32_attention8_decode(*pq, cache.addr, pt, _ld(table, shared=True), W, pl, *po, B, Hq,
                                        D ** -0.5 if scale is None else scale, ws, need, st), "cfp32_attention8_decode")
     return out
 

@@ -63,9 +63,10 @@ inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintp
 
 inline void *align_up(void *p) { return reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(p) + kAlign - 1) & ~(uintptr_t)(kAlign - 1)); }
 
-inline bool table_ok(const void *t, int64_t ld, int64_t rows, int64_t W)
+// one: of a table that is only read, all rows may be one (ld 0).
+inline bool table_ok(const void *t, int64_t ld, int64_t rows, int64_t W, bool one = false)
 {
-    return ld >= W && term_ok(rows, ld) && (t || rows == 0 || W == 0);
+    return (ld >= W || (one && ld == 0)) && term_ok(rows, ld) && (t || rows == 0 || W == 0);
 }
 
 }  // namespace cfp32

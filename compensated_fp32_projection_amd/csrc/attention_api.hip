@@ -93,7 +93,7 @@ cfp32_status cfp32_attention_decode(const float *q, int64_t q_seq, int64_t q_hea
         return CFP32_ERR_INVALID_VALUE;
     if (B == 0 || Hq == 0 || D == 0) return CFP32_OK;
     if (B > (kMaxDim >> 20) / Hq) return CFP32_ERR_INVALID_VALUE;
-    if (!q || !out || !lens || !table_ok(table, ld_table, B, W)) return CFP32_ERR_INVALID_VALUE;
+    if (!q || !out || !lens || !table_ok(table, ld_table, B, W, true)) return CFP32_ERR_INVALID_VALUE;
     if (P > 0 && !pool_ok(k_pages, k_page, k_head, k_tok, v_pages, v_page, v_head, v_tok, P, Hkv, page, D, kv_type, false))
         return CFP32_ERR_INVALID_VALUE;
     if (!aligned_to(q, 4) || !aligned_to(out, 4) || !view_ok(B, q_seq, Hq, q_head, 1, 0, D) ||

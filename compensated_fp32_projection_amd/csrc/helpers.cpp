@@ -82,7 +82,8 @@ bool ints(const at::Tensor *t, c10::Device dev, int dim, int32_t *&p)
     return true;
 }
 
-int64_t ld(const at::Tensor &t) { return std::max(t.size(0) > 1 ? t.stride(0) : 0, t.size(1)); }
+// Elements from one row to the next, as they are: the C ABI refuses rows that overlap.
+int64_t ld(const at::Tensor &t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
 
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, c10::Device dev)
 {
@@ -494,8 +495,7 @@ PyObject *select(PyObject *const *a)
     if (done && ((done->scalar_type() != at::kBool && done->scalar_type() != at::kByte) || done->device() != dev ||
                  done->sizes() != scores->sizes() || !done->is_contiguous()))
         return none();
-    const int64_t S = scores->size(0), beams = scores->size(1), V = x->size(1), step = x->size(0) > 1 ? x->stride(0) : V;
-    if (step && step < V) return none();  // rows overlap; of step 0 they are one
+    const int64_t S = scores->size(0), beams = scores->size(1), V = x->size(1);
     if (a[2] == Py_None) n = beams;
     if (n < 1 || n > 64) return none();
     const at::Tensor parents = empty({S, n}, at::kInt, dev), tokens = empty({S, n}, at::kInt, dev),
@@ -503,7 +503,7 @@ PyObject *select(PyObject *const *a)
     Call c;
     const size_t need = api.select_ws(S, beams, V, n);
     if (!c.ready(dev, need)) return nullptr;
-    if (api.select((const float *)x->data_ptr(), step, (const float *)scores->data_ptr(), done ? (const uint8_t *)done->data_ptr() : nullptr,
+    if (api.select((const float *)x->data_ptr(), ld(*x), (const float *)scores->data_ptr(), done ? (const uint8_t *)done->data_ptr() : nullptr,
                    S, beams, V, n, eos, (int32_t *)parents.data_ptr(), (int32_t *)tokens.data_ptr(), (float *)out.data_ptr(),
                    (uint8_t *)ended.data_ptr(), c.ws, need, c.stream) != CFP32_OK)
         return none();

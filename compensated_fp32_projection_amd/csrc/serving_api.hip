@@ -144,7 +144,7 @@ cfp32_status cfp32_cache8_read(const cfp32_cache8 *cache, const int32_t *table, 
     const int64_t H = cache->Hkv, D = cache->D;
     if (S == 0 || T == 0 || H == 0 || D == 0) return CFP32_OK;
     const size_t al = out_type == CFP32_KV_F16 ? 2 : 4;
-    if (!cu || !k || !v || !aligned_to(k, al) || !aligned_to(v, al) || !table_ok(table, ld_table, S, W) || !pools_ok(cache, false))
+    if (!cu || !k || !v || !aligned_to(k, al) || !aligned_to(v, al) || !table_ok(table, ld_table, S, W, true) || !pools_ok(cache, false))
         return CFP32_ERR_INVALID_VALUE;
     if (!view_ok(T, k_tok, H, k_head, 1, 0, D) || !view_ok(T, v_tok, H, v_head, 1, 0, D) ||
         !distinct_ok(T, k_tok, H, k_head, 1, 0, D) || !distinct_ok(T, v_tok, H, v_head, 1, 0, D))
@@ -223,7 +223,7 @@ cfp32_status cfp32_attention8_decode(const float *q, int64_t q_seq, int64_t q_he
     const int64_t D = cache->D;
     if (B == 0 || Hq == 0 || D == 0) return CFP32_OK;
     if (B > (kMaxDim >> 20) / Hq) return CFP32_ERR_INVALID_VALUE;
-    if (!q || !out || !lens || !table_ok(table, ld_table, B, W) || !pools_ok(cache, false)) return CFP32_ERR_INVALID_VALUE;
+    if (!q || !out || !lens || !table_ok(table, ld_table, B, W, true) || !pools_ok(cache, false)) return CFP32_ERR_INVALID_VALUE;
     if (!aligned_to(q, 4) || !aligned_to(out, 4) || !view_ok(B, q_seq, Hq, q_head, 1, 0, D) ||
         !view_ok(B, out_seq, Hq, out_head, 1, 0, D) || !distinct_ok(B, out_seq, Hq, out_head, 1, 0, D))
         return CFP32_ERR_INVALID_VALUE;

@@ -417,7 +417,8 @@ CFP32_API size_t cfp32_attention_decode_workspace_bytes(int64_t B, int64_t Hq, i
 /* Attention of one new token per sequence against a paged cache.
  *   q, out       : FP32 [B, Hq, D].
  *   k_pages, v_pages : pools of P pages of kv_type.
- *   table        : int32 [B, W], leading dimension ld_table >= W.
+ *   table        : int32 [B, W], leading dimension ld_table >= W, or 0 where
+ *                  all sequences have one row.
  *   lens         : int32 [B]: sequence b sees its first lens[b] tokens
  *                  (clamped to [0, W * page]); 0 gives a row of 0.
  *   shared_pages : the first shared_pages (<= W) table entries are the same
@@ -611,7 +612,8 @@ CFP32_API cfp32_status cfp32_cache8_append(const float *k, int64_t k_tok, int64_
 
 /* Reads tokens back, packed as cfp32_attention_prompt takes them: rows cu[s] ..
  * cu[s+1] - 1 of k, v [T, Hkv, D] of out_type (a cfp32_kv_type) get tokens
- * first[s], first[s] + 1, ... of sequence s (first NULL: from 0 on).  c s is
+ * first[s], first[s] + 1, ... of sequence s (first NULL: from 0 on; ld_table 0:
+ * all sequences have one row of the table).  c s is
  * rounded to FP32, then, where asked for, to FP16.  A token that has no page in
  * the table, or a position that is negative or beyond it, reads as NaN; rows
  * outside all sequences are not written.  One kernel launch. */
@@ -639,7 +641,8 @@ CFP32_API size_t cfp32_attention8_decode_workspace_bytes(int64_t B, int64_t Hq, 
 /* Attention of one new token per sequence against an 8-bit cache: as
  * cfp32_attention_decode, with K and V the codes times their scales.
  *   q, out : FP32 [B, Hq, D], Hq a multiple of the cache's Hkv.
- *   table  : int32 [B, W], leading dimension ld_table >= W.
+ *   table  : int32 [B, W], leading dimension ld_table >= W, or 0 where all
+ *            sequences have one row.
  *   lens   : int32 [B]: sequence b sees its first lens[b] tokens (clamped to
  *            [0, W * page]); 0 gives a row of 0.
  * Codes are exact operands; q, and each row's products of weights and V's
