@@ -343,6 +343,8 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     fk[b][r] = f * t.ks[b][r] * f2;
+                    // A scale that no key of the row has may be anything, and must not choose the form either.
+                    if (ends) fk[b][r] = 16 * b + r < room ? fk[b][r] : 0.0f;
                     peak = fmaxf(peak, fabsf(fk[b][r]));
                 }
             if (__any(peak == INFINITY)) {
