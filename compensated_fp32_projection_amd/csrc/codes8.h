@@ -36,13 +36,21 @@ __device__ __forceinline__ float fresh_scale(uint32_t most)
     }
 }
 
-// The least k >= 0 for which a block of scale s x 2^k holds `most` (its bits, finite).
+// The least k for which `s` 2^k is `least` or more (bits of both, normal).
+__device__ __forceinline__ int doublings(uint32_t s, uint32_t least)
+{
+    return least <= s ? 0 : (int)(least >> 23) - (int)(s >> 23) + ((least & 0x7FFFFF) > (s & 0x7FFFFF));
+}
+
+// The least k >= 0 for which a block of scale s x 2^k holds `most` (its bits, finite): the largest code x the scale is
+// `most` or more, or (integers, where that is rounded) the scale is one that `most` would be given itself.  With the
+// first alone, every 20th `most` did not fit the scale that it had been given.
 template <bool E4M3>
 __device__ __forceinline__ int growth(float s, uint32_t most)
 {
-    const uint32_t holds = __builtin_bit_cast(uint32_t, s * (E4M3 ? 448.0f : 127.0f));
-    if (most <= holds) return 0;
-    return (int)(most >> 23) - (int)(holds >> 23) + ((most & 0x7FFFFF) > (holds & 0x7FFFFF));
+    const int k = doublings(__builtin_bit_cast(uint32_t, s * (E4M3 ? 448.0f : 127.0f)), most);
+    if constexpr (E4M3) return k;
+    else return min(k, doublings(__builtin_bit_cast(uint32_t, s), __builtin_bit_cast(uint32_t, fresh_scale<false>(most))));
 }
 
 // x / s to the nearest integer, ties to even, of the exact quotient (|x| is at

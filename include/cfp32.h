@@ -571,11 +571,12 @@ CFP32_API cfp32_status cfp32_rotary(const void *q, int64_t q_tok, int64_t q_head
  * A block's scale is made when its first token is written: of the largest
  * magnitude m of what is written, m x 1/127 for integers (the factor and the
  * product rounded to FP32), for floats the least power of two that brings m to
- * 448 or below, and 2^-126 at least.  A later
- * token that does not fit (m > the largest code x the scale, in FP32) multiplies
- * the scale by the least power of two that holds it, and the block's codes are
- * divided by it: so a value of its first tokens is off by less than one step of
- * the block's last scale however often that grew, and by half a step where it
+ * 448 or below, and 2^-126 at least.  A later token fits if its m is at most the
+ * largest code x the scale, in FP32, or the scale is at least the one that m would
+ * be given itself.  One that does not multiplies the scale by the least power of
+ * two with which it does, and the block's codes are divided by it: so a value of
+ * its first tokens is off by less than one step of the block's last scale however
+ * often that grew, and by half a step where it
  * did not.  Codes are x / s rounded to nearest even, of the exact quotient (with
  * scales of floats that are not powers of two, which no call makes: of the
  * product with 1 / s).  A block that is given an infinity or NaN, or holds
