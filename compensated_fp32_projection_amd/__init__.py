@@ -1050,7 +1050,7 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
     [R / 2] for the first R dims; positions int64 [T] (0 .. T-1 if None).
     layout: "half" (pairs i, i + R/2) or "interleaved" (2i, 2i + 1).
     ``transpose`` takes gradients of the outputs to those of the inputs.
-    q_out and k_out may be q and k."""
+    q_out and k_out may be q and k, in this order, and overlap nothing else."""
     if layout not in ("half", "interleaved"):
         raise ValueError("layout must be 'half' or 'interleaved'")
     if stream is None:
@@ -1088,6 +1088,8 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
         outs.append(out)
     po = _heads(outs[0], (q.dtype,), "q_out", dev)
     pko = (None, 0, 0) if k is None else _heads(outs[1], (q.dtype,), "k_out", dev)
+    if T * Hq * Hkv * D and (po[0] in (pk[0], pko[0]) or pko[0] == pq[0]):
+        raise ValueError("q_out and k_out may be q and k, in this order, and nothing that the other is")
     _launch(cfp32_rotary, "cfp32_rotary", dev, *pq, *pk, KV_F16 if q.dtype == torch.float16 else KV_F32, pp,
             frequencies.data_ptr(), float(amplitude), ROTARY_INTERLEAVED if layout == "interleaved" else ROTARY_HALF,
             1 if transpose else 0, *po, *pko, T, Hq, Hkv, D, 2 * frequencies.shape[0], stream=stream)

@@ -394,6 +394,7 @@ PyObject *rotary(PyObject *const *a)
     const at::Tensor oq = qo ? *qo : empty(q->sizes(), type, dev), ok = !k ? at::Tensor() : ko ? *ko : empty(k->sizes(), type, dev);
     if (oq.sizes() != q->sizes() || !heads(&oq, type, dev, vqo) || (k && (ok.sizes() != k->sizes() || !heads(&ok, type, dev, vko))))
         return none();
+    if (T && Hq && Hkv && D && (vqo.p == vko.p || vqo.p == vk.p || vko.p == vq.p)) return none();
     Call c;
     if (!c.ready(dev, 0)) return nullptr;
     if (api.rotary(vq.p, vq.s0, vq.s1, vk.p, vk.s0, vk.s1, kv, pos ? (const int64_t *)pos->data_ptr() : nullptr,

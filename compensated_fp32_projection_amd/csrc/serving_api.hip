@@ -105,6 +105,8 @@ cfp32_status cfp32_rotary(const void *q, int64_t q_tok, int64_t q_head, const vo
     };
     if (!ok(q, q_tok, q_head, q_out, qo_tok, qo_head, Hq) || !ok(k, k_tok, k_head, k_out, ko_tok, ko_head, Hkv))
         return CFP32_ERR_INVALID_VALUE;
+    // Rows that another thread reads or writes, too.
+    if (Hq > 0 && Hkv > 0 && q != k && (q_out == k_out || q_out == k || k_out == q)) return CFP32_ERR_INVALID_VALUE;
     if ((R > 0 && !frequencies) || !aligned_to(frequencies, 8) || !aligned_to(positions, 8)) return CFP32_ERR_INVALID_VALUE;
     cfp32_status st = api_check_device();
     if (st != CFP32_OK) return st;

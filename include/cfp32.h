@@ -547,7 +547,9 @@ CFP32_API cfp32_status cfp32_rotary_frequencies(double theta, int64_t R, int sca
  *                 a token and head contiguous, strides of tokens and heads in
  *                 elements (those of inputs >= 0).  k, k_out: [T, Hkv, D].
  *                 Hq or Hkv may be 0.  An output may be its input, with the same
- *                 strides (in place).
+ *                 strides (in place); otherwise outputs overlap neither inputs
+ *                 nor each other (refused where q and k are apart and an output
+ *                 begins where the other's tensors do).
  *   positions   : int64 [T], device (any values), or NULL for 0 .. T-1.
  *   frequencies : FP64 [R / 2], device, as cfp32_rotary_frequencies makes them.
  *   R           : even, 0 <= R <= D <= 1024; dims from R on are copied.
