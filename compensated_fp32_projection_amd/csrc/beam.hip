@@ -3,7 +3,7 @@
 // A beam's offers are ordered as its logits are, so the n best of a sequence are
 // among the n largest logits of each beam.  One launch passes over the logits:
 // a wave takes 512 or 2048 of a row, holds them in registers, and leaves
-//   * the largest of its logits and the sum of exp(x - largest);
+//   * the sum of exp(x - c), c next to the largest of its logits, and c;
 //   * its n largest logits with their tokens, in order.  The n-th largest of
 //     the lanes' own largest is a lower bound of the n-th largest of all, so
 //     few logits but the wanted ones reach the sort.
@@ -11,6 +11,8 @@
 // to a beam, and merges the beams' lists.  The logits are read once; that
 // bounds the first launch (256 x 128000 25 us, 5.2 TB/s), latency the second (10 us
 // for 8 beams of 63 lists, 6.5 for 4 of them).
+#include <cfloat>
+
 #include "beam.h"
 #include "device_common.h"
 #include "lanes.h"
@@ -90,6 +92,34 @@ __device__ __forceinline__ float wave_max(float v)
     return max_of_quads(v);
 }
 
+// Terms exp(x) of a sum, relative to a power of two next to the largest.  x log2 e = n + f to the nearest integer n; f is
+// formed by two fused multiply-adds, the second with what FP32 leaves of log2 e, so that rounding takes bits off f (2^-26
+// each time) and not off x log2 e.  2^f is off by its instruction's last place; two terms are added in FP32, pairs in
+// FP64, and their sum becomes FP32: 4.03 x 2^-24 of it in all.  (Rounded products x log2 e and FP32 sums left 2^-19 of a
+// row of 2048 logits all but one of which are equal; with these 256 x 128000 takes 1 us more.)
+struct Terms {
+    static constexpr float kRound = 0x1.8p23f;  // what is added to it loses its fraction
+    float least, round;
+    // Of x up to `top` (below 2^22 in magnitude), 2^power being the unit.
+    __device__ __forceinline__ Terms(float top, float power) : least(top - 80.0f), round(kRound - power) {}
+    // x as two factors: 2^f, and the power of two.  Below `least` the power stays, and 2^f goes on to 0.
+    __device__ __forceinline__ void factors(float x, float &p, float &s) const
+    {
+        constexpr float kRest = 1.9259629911e-8f;  // log2 e - kLog2e
+        const float up = __builtin_amdgcn_fmed3f(x, least, INFINITY);  // fmaxf takes two instructions
+        const float r = fmaf(up, kLog2e, round), n = r - round;
+        p = __builtin_amdgcn_exp2f(fmaf(x, kRest, fmaf(x, kLog2e, -n)));
+        s = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, r) << 23) + 0x3F800000u);
+    }
+    __device__ __forceinline__ float two(float x, float y) const
+    {
+        float p, q, s, t;
+        factors(x, p, s);
+        factors(y, q, t);
+        return fmaf(q, t, p * s);
+    }
+};
+
 // The largest keys seen by a wave, in order, and those that wait to be sorted
 // into them (in LDS, of this wave alone).
 struct Best {
@@ -157,24 +187,38 @@ __global__ __launch_bounds__(256) void beam_rows_kernel(BeamArgs a, int chunks, 
     for (int e = 0; e < E; ++e) mine = fmaxf(mine, x[e]);
     const float sorted = sort_wave(mine);
     const float most = __shfl(sorted, 0), least = __shfl(sorted, a.n - 1);
-    float sum = 0.0f;
+    const float bar = fmaxf(least, -FLT_MAX);  // -infinity is not offered
+    Best best = {0, waiting[wave], 0, false};
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum += __builtin_amdgcn_exp2f((x[e] - most) * kLog2e);
-    sum = wave_sum(sum);
+    for (int e = 0; e < E; ++e) best.add(x[e] >= bar, offer_key(x[e], (int)token(e)));
+    if (best.count) best.flush();
+    if (lane < a.n) lists[unit * a.n + lane] = best.top;
+
     // A NaN, or infinity less itself, leaves a sum of NaN; of nothing but -infinity (and no NaN) it is 0.
     if (most == -INFINITY) {
         float odd = 0.0f;
 #pragma unroll
         for (int e = 0; e < E; ++e) odd = x[e] != x[e] ? NAN : odd;
-        sum = __any(odd != odd) ? NAN : 0.0f;
+        if (lane == 0) stats[unit] = make_float2(most, __any(odd != odd) ? NAN : 0.0f);
+        return;
     }
-
-    Best best = {0, waiting[wave], 0, false};
+    // Far from 0 only differences from the largest have a fraction to be kept, and those that count are exact.
+    const bool far = fabsf(most) >= 1024.0f;
+    if (far) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) best.add(x[e] >= least && x[e] > -INFINITY, offer_key(x[e], (int)token(e)));
-    if (best.count) best.flush();
-    if (lane < a.n) lists[unit * a.n + lane] = best.top;
-    if (lane == 0) stats[unit] = make_float2(most, sum);
+        for (int e = 0; e < E; ++e) x[e] -= most;
+    }
+    const float power = far ? 0.0f : rintf(most * kLog2e);
+    const Terms terms(far ? 0.0f : most, power);
+    double sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) sum += (double)terms.two(x[e], x[e + 1]);
+    sum = wave_sum(sum);
+    // The unit, 2^power, as e to the power of an FP32 number and a factor next to 1.
+    const double unit_log = (double)power * 0.693147180559945309417232;
+    const float from = far ? most : (float)unit_log;
+    const double rest = far ? 0.0 : unit_log - (double)from;
+    if (lane == 0) stats[unit] = make_float2(from, (float)(sum * (1.0 + rest * (1.0 + 0.5 * rest))));
 }
 
 // An offer of a beam: larger totals first, of equal ones the lower place (beam,
