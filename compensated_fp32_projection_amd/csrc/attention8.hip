@@ -307,9 +307,10 @@ __device__ __forceinline__ void attend_share8(const float *q, bool q_wide, int D
                 qh[2 * i + e / 8][e % 8] = h[0], qh[2 * i + e / 8][e % 8 + 1] = h[1];
                 ql[2 * i + e / 8][e % 8] = w[0], ql[2 * i + e / 8][e % 8 + 1] = w[1];
             }
-        // 2^-e2 in two halves: of very small rows it is beyond FP32's range, where large scales bring scores back.
-        const int half = e2 / 2;
-        const float f = __builtin_amdgcn_ldexpf(scale * kLog2e * kCode, -half), f2 = __builtin_amdgcn_ldexpf(1.0f, half - e2);
+        // What scores are multiplied by, but for their keys' scales: scale log2 e 2^-e2, as two factors of which neither is
+        // beyond FP32's range, where very small rows, large scales of theirs or of the scores bring each other back.
+        const int up = __builtin_amdgcn_frexp_expf(scale) - e2 + (E4M3 ? 8 : 0), half = up / 2;
+        const float f = __builtin_amdgcn_ldexpf(__builtin_amdgcn_frexp_mantf(scale) * kLog2e, half), f2 = __builtin_amdgcn_ldexpf(1.0f, up - half);
 
         // A step's work on one tile, while the next one's is on its way into the other.
         auto step = [&](Tile &t, Tile &ahead) {
