@@ -1360,6 +1360,9 @@ def beam_reorder(states, parents, out=None, stream=None):
         raise TypeError("parents: expected an int32 tensor on states' device")
     if not parents.is_contiguous():
         raise ValueError("parents must be contiguous")
+    for t, name in ((states, "states"), (out, "out")):
+        if t is not None and (t.is_conj() or t.is_neg()):
+            raise ValueError(f"{name}: a view whose values are not those in memory (resolve_conj() or resolve_neg() copies it)")
     rest = states.shape[1:]
     if states.dim() < 1 or (states.shape[0] and not states[0].is_contiguous()):
         raise ValueError("states must have contiguous rows")

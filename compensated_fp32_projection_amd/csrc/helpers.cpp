@@ -517,7 +517,7 @@ PyObject *reorder(PyObject *const *a)
     const at::Tensor *x = tensor(a[0]), *parents = tensor(a[1]);
     if (!x || !parents || !x->is_cuda()) return none();
     const c10::Device dev = x->device();
-    if (!current(dev) || x->dim() < 1 || !x->is_contiguous() || parents->scalar_type() != at::kInt || parents->device() != dev ||
+    if (!current(dev) || x->dim() < 1 || !x->is_contiguous() || x->is_conj() || x->is_neg() || parents->scalar_type() != at::kInt || parents->device() != dev ||
         !parents->is_contiguous())
         return none();
     const int64_t rows = x->size(0), n = parents->numel();
