@@ -1102,9 +1102,19 @@ class Cache8:
     """The pools of an 8-bit cache: codes k, v [P, Hkv, page, D] (int8 or
     float8_e4m3fn, any strides with contiguous D) and FP32 scales [P, Hkv,
     page / block], one for each block of tokens and head (``blocks`` of a
-    page: powers of two).  Holds the tensors; the calls read and write them."""
+    page: powers of two).  The calls read and write the memory of the tensors
+    that it is made of, which it keeps, whatever becomes of those: its
+    attributes are not to be set, nor their storages resized."""
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "desc", "addr", "device", "index", "shape", "block")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "desc", "addr", "device", "index", "shape", "block", "_held")
+
+    def __setattr__(self, name, value):
+        if hasattr(self, name):
+            raise AttributeError(f"{name}: the pools of a Cache8 are those it was made of")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name}: the pools of a Cache8 are those it was made of")
 
     def __init__(self, k, v, k_scales, v_scales):
         torch = _torch()
@@ -1129,6 +1139,8 @@ class Cache8:
         if blocks < 1 or page % blocks or page & (page - 1) or blocks & (blocks - 1) or not 1 <= page <= 65536:
             raise ValueError("tokens and blocks of a page must be powers of two, of at most 65536 tokens")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        # What `desc` points to: of a tensor that is given another storage, the old one stays here.
+        self._held = tuple(t.detach() for t in (k, v, k_scales, v_scales))
         self.device, self.shape, self.block = k.device, k.shape, page // blocks
         self.desc = Cache8Desc(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3], k_scales.data_ptr(),
                                v_scales.data_ptr(), *k_scales.stride()[:2], *v_scales.stride()[:2], P, Hkv, page,
