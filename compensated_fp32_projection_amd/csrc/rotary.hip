@@ -10,7 +10,7 @@
 // Angles: p f_i / 2 pi in FP64 is reduced to a quarter turn there, since the
 // whole turns of a far position leave FP32 nothing (2^20 positions of 1 radian
 // are off by 0.03 in it); the remainder, within an eighth of a turn, is FP32
-// with 2^-28 at most lost, and goes through the Taylor polynomials of sine and
+// with 2^-25 radians at most lost, and goes through the Taylor polynomials of sine and
 // cosine (terms to x^9 and x^10: 1.8e-9 left at pi / 4).
 #include "device_common.h"
 #include "rotary.h"

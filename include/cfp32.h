@@ -651,10 +651,13 @@ CFP32_API size_t cfp32_attention8_decode_workspace_bytes(int64_t B, int64_t Hq, 
  * Codes are exact operands; q, and each row's products of weights and V's
  * scales, are cut into two FP16 parts (22 bits: a product is off by 2^-22 of
  * itself or 2^-36 of the largest of the row's 32 or 64 keys beside it); sums
- * and softmax statistics are FP32.  Weights below 2^-126 of the row's largest may
- * count as 0, and scores beyond 2^127 in powers of two as infinite.  A page id
- * outside [0, P) where lens needs a page, and a scale that is NaN, make the rows
- * that see it NaN, as an infinity or NaN of q does its own row; scales of tokens
+ * and softmax statistics are FP32.  At the ends of that range: weights below
+ * 2^-126 of the row's largest may count as 0, and products of weights and scales
+ * keep multiples of 2^-149; a row whose sums of weights times values are beyond it
+ * is not finite; scores beyond 2^127 in powers of two count as infinite, so a row
+ * is NaN with a +infinite one, and 0 if all are -infinite.  A page id outside
+ * [0, P) where lens needs a page, and a scale that is NaN, make the rows that see
+ * it NaN, as an infinity or NaN of q does its own row; scales of tokens
  * that no row sees reach none. */
 CFP32_API cfp32_status cfp32_attention8_decode(const float *q, int64_t q_seq, int64_t q_head, const cfp32_cache8 *cache,
                                      const int32_t *table, int64_t ld_table, int64_t W, const int32_t *lens, float *out,
