@@ -9,7 +9,7 @@
 //     few logits but the wanted ones reach the sort.
 // The second launch, a block to a sequence, joins a row's sums and lists, a wave
 // to a beam, and merges the beams' lists.  The logits are read once; that
-// bounds the first launch (256 x 128000 25 us, 5.2 TB/s), latency the second (10 us
+// bounds the first launch (256 x 128000 27 us, 4.8 TB/s), latency the second (10 us
 // for 8 beams of 63 lists, 6.5 for 4 of them).
 #include <cfloat>
 
@@ -96,17 +96,18 @@ __device__ __forceinline__ float wave_max(float v)
 // formed by two fused multiply-adds, the second with what FP32 leaves of log2 e, so that rounding takes bits off f (2^-26
 // each time) and not off x log2 e.  2^f is off by its instruction's last place; two terms are added in FP32, pairs in
 // FP64, and their sum becomes FP32: 4.03 x 2^-24 of it in all.  (Rounded products x log2 e and FP32 sums left 2^-19 of a
-// row of 2048 logits all but one of which are equal; with these 256 x 128000 takes 1 us more.)
+// row of 2048 logits all but one of which are equal; 256 x 128000 took 25.5 us with them.)
 struct Terms {
     static constexpr float kRound = 0x1.8p23f;  // what is added to it loses its fraction
     float least, round;
-    // Of x up to `top` (below 2^22 in magnitude), 2^power being the unit.
+    // Of x up to `top` (below 2^20 in magnitude), 2^power being the unit.
     __device__ __forceinline__ Terms(float top, float power) : least(top - 80.0f), round(kRound - power) {}
     // x as two factors: 2^f, and the power of two.  Below `least` the power stays, and 2^f goes on to 0.
     __device__ __forceinline__ void factors(float x, float &p, float &s) const
     {
         constexpr float kRest = 1.9259629911e-8f;  // log2 e - kLog2e
-        const float up = __builtin_amdgcn_fmed3f(x, least, INFINITY);  // fmaxf takes two instructions
+        // Not fmaxf, or the median with infinity, which take two instructions (256 x 128000 27.2 -> 28 us).
+        const float up = __builtin_amdgcn_fmed3f(x, least, 0x1p20f);
         const float r = fmaf(up, kLog2e, round), n = r - round;
         p = __builtin_amdgcn_exp2f(fmaf(x, kRest, fmaf(x, kLog2e, -n)));
         s = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, r) << 23) + 0x3F800000u);
