@@ -1049,7 +1049,8 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", amplitude: f
     (or None), FP32 or FP16, any strides with contiguous D; frequencies FP64
     [R / 2] for the first R dims; positions int64 [T] (0 .. T-1 if None).
     layout: "half" (pairs i, i + R/2) or "interleaved" (2i, 2i + 1).
-    ``transpose`` takes gradients of the outputs to those of the inputs.
+    ``transpose`` takes gradients of the outputs to those of the inputs (as
+    all calls here, it records no graph for autograd).
     q_out and k_out may be q and k, in this order, and overlap nothing else."""
     if layout not in ("half", "interleaved"):
         raise ValueError("layout must be 'half' or 'interleaved'")
